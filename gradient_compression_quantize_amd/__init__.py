@@ -19,6 +19,11 @@ Two method families (see include/gcq.h for exact semantics):
     which needs no workspace), qsgd_maxnorm_quantize,
     qsgd_dequant_sum, qsgd_quantize_sum (the W quantizes and the level sum fused),
     grandk_indices, gather_f32, and grandk_mn_step (the whole GRandK-MN step).
+
+Training operators, whose gradients the two families compress (activations in
+float32, bfloat16 or float16; gradients of parameters in float32):
+  * dropout and dropout_backward, on the same counter-based generator, the
+    mask drawn again where it is needed instead of stored.
 """
 from __future__ import annotations
 
@@ -33,6 +38,10 @@ GC_EINVAL = -1
 GC_EHIP = -2
 GC_EUNSUPPORTED = -3
 GC_MAX_WORKERS = 64
+
+GC_F32 = 0
+GC_BF16 = 1
+GC_F16 = 2
 
 
 class GcqError(RuntimeError):
@@ -96,13 +105,17 @@ def _declare(L):
     L.gather_f32.argtypes = [_vp, _vp, _sz, _vp, _vp]
     L.grandk_mn_step.argtypes = [ctypes.POINTER(_vp), _i, _sz, ctypes.c_uint32, ctypes.c_uint64,
                                  _i, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(_sz), _vp]
+    u64, u32, dbl = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_double
+    L.dropout.argtypes = [_vp, _vp, _sz, _i, dbl, u64, u32, u64, _vp, _vp, _vp]
+    L.dropout_backward.argtypes = [_vp, _sz, _i, dbl, u64, u32, u64, _vp, _vp, _vp]
     for name in ("compress_2bit", "decompress_2bit", "decompress_2bit_sum",
                  "compress_ternary", "decompress_ternary", "decompress_ternary_sum",
                  "gc_plan_2bit_multi_create", "gc_plan_block_offsets", "compress_2bit_multi",
                  "qsgd_global_maxnorm", "qsgd_global_maxnorm_noalloc",
                  "qsgd_maxnorm_quantize", "qsgd_dequant_sum",
                  "qsgd_quantize_sum",
-                 "grandk_indices", "gather_f32", "grandk_mn_step"):
+                 "grandk_indices", "gather_f32", "grandk_mn_step",
+                 "dropout", "dropout_backward"):
         getattr(L, name).restype = _i
     return L
 
@@ -501,3 +514,68 @@ def grandk_mn_step(grads: Sequence, K: int, seed: int, s: int, idx, dense, ws, s
                                  _dev(dense, torch.float32, "dense"),
                                  _dev(norm, torch.float32, "norm"), _dev(ws, torch.uint8, "ws"),
                                  ctypes.byref(size), _stream(stream)))
+
+
+# ---- training operators -------------------------------------------------------
+
+_dtypes = None
+
+
+def _dtype(t, what: str) -> int:
+    """gc_dtype of a tensor of activations."""
+    global _dtypes
+    if _dtypes is None:
+        torch = _torch()
+        _dtypes = {torch.float32: GC_F32, torch.bfloat16: GC_BF16, torch.float16: GC_F16}
+    code = _dtypes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: expected float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _step(step) -> ctypes.c_void_p:
+    """A device counter added to the seed: an int64 tensor of one element."""
+    if step is None:
+        return _vp(None)
+    if step.numel() != 1:
+        raise ValueError("step must hold one element")
+    return _dev(step, _torch().int64, "step")
+
+
+def _u64(v: int) -> int:
+    return int(v) & (2 ** 64 - 1)
+
+
+def _worker(worker: int) -> int:
+    if not 0 <= int(worker) < 2 ** 32:
+        raise ValueError("worker must lie in 0 .. 2^32 - 1")
+    return int(worker)
+
+
+def _offset(offset: int) -> int:
+    if not 0 <= int(offset) < 2 ** 64:
+        raise ValueError("offset must lie in 0 .. 2^64 - 1")
+    return int(offset)
+
+
+def dropout(x, p: float, seed: int, worker: int, out, residual=None, offset: int = 0, step=None,
+            stream=None) -> None:
+    """out = dropout(x) (+ residual). out may be x or residual itself; step:
+    one-element int64 device tensor added to the seed on the device."""
+    n = x.numel()
+    if out.numel() != n or (residual is not None and residual.numel() != n):
+        raise ValueError("dropout: x, out and residual differ in size")
+    _check(load().dropout(_dev(x, x.dtype, "x"), _dev(residual, x.dtype, "residual"), n,
+                          _dtype(x, "x"), float(p), _u64(seed), _worker(worker), _offset(offset),
+                          _step(step), _dev(out, x.dtype, "out"), _stream(stream)))
+
+
+def dropout_backward(grad_out, p: float, seed: int, worker: int, grad_in, offset: int = 0,
+                     step=None, stream=None) -> None:
+    n = grad_out.numel()
+    if grad_in.numel() != n:
+        raise ValueError("dropout_backward: grad_out and grad_in differ in size")
+    _check(load().dropout_backward(_dev(grad_out, grad_out.dtype, "grad_out"), n,
+                                   _dtype(grad_out, "grad_out"), float(p), _u64(seed),
+                                   _worker(worker), _offset(offset), _step(step),
+                                   _dev(grad_in, grad_out.dtype, "grad_in"), _stream(stream)))

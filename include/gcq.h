@@ -2,7 +2,8 @@
  * gcq.h -- C ABI of libgcq.so: gradient quantization kernels for MI355X
  * (gfx950).
  *
- * Two families of element-wise gradient compression for data-parallel SGD:
+ * Two families of element-wise gradient compression for data-parallel SGD,
+ * and the training operators that produce such gradients (3):
  *
  *  (1) 2-bit threshold quantization with residual error feedback, from the
  *      apache/incubator-mxnet pull request #8342 "[WIP] 2bit gradient
@@ -52,6 +53,13 @@ typedef enum gc_status {
     GC_EHIP = -2,         /* a HIP call or kernel launch failed */
     GC_EUNSUPPORTED = -3  /* valid request outside what the library supports */
 } gc_status;
+
+/* Element types of the training operators' activations. */
+typedef enum gc_dtype {
+    GC_F32 = 0,
+    GC_BF16 = 1,
+    GC_F16 = 2
+} gc_dtype;
 
 /* Largest number of simulated workers a single call combines. */
 #define GC_MAX_WORKERS 64
@@ -288,6 +296,44 @@ int grandk_mn_step(const float* const* grads, int W, size_t n, uint32_t K,
                    uint64_t seed, int s, uint32_t* idx, int32_t* sums,
                    float* dense, float* norm, void* ws, size_t* ws_bytes,
                    hipStream_t stream);
+
+/* ====================================================================
+ * Training operators. Activations are of one gc_dtype and need their
+ * element's alignment (16-byte-aligned ones are faster); arithmetic is fp32,
+ * each output rounds once.
+ * ==================================================================== */
+
+/* ---- dropout, its mask never stored --------------------------------------- */
+
+/* out[i] = (keep_i ? x[i] * (1 / (1 - p)) : 0) + residual[i], with
+ *   keep_i = (u_i >= p), u_i = (r >> 8) * 2^-24 for
+ *   r = word (j mod 4) of Philox4x32-10(key = (seed lo, seed hi),
+ *                                counter = (j/4 lo, j/4 hi, worker, 2)),
+ *   j = i + offset.
+ * The mask depends on (seed, worker, j) alone, not on the type or the values:
+ * the generator, seeds and workers are those of qsgd_maxnorm_quantize, whose
+ * rounding draws from other counters. Calls with the same seed, worker and
+ * overlapping ranges of j draw the same mask there: give each place of a
+ * model its own range or seed. A dropped value is 0 whatever x[i] holds.
+ *   x, out    [n] of `dtype`
+ *   residual  [n] of `dtype`, or NULL
+ *   p         0 .. 1 (0 keeps, 1 drops everything)
+ *   offset    offset + n <= 2^64
+ *   step      device uint64 added to the seed (mod 2^64) when the kernel
+ *             runs, or NULL: a captured call draws a new mask at each replay
+ *             once the graph (or the caller) advances it
+ * `out` may be x or residual itself; other overlaps are not allowed. */
+int dropout(const void* x, const void* residual, size_t n, int dtype, double p,
+            uint64_t seed, uint32_t worker, uint64_t offset, const uint64_t* step,
+            void* out, hipStream_t stream);
+
+/* The gradient of dropout with respect to x (with respect to residual it is
+ * grad_out itself): grad_in[i] = keep_i ? grad_out[i] * (1 / (1 - p)) : 0,
+ * with the mask of the same (p, seed, worker, offset, *step). `grad_in` may
+ * be grad_out itself. */
+int dropout_backward(const void* grad_out, size_t n, int dtype, double p,
+                     uint64_t seed, uint32_t worker, uint64_t offset,
+                     const uint64_t* step, void* grad_in, hipStream_t stream);
 
 #ifdef __cplusplus
 }
