@@ -23,7 +23,9 @@ Two method families (see include/gcq.h for exact semantics):
 Training operators, whose gradients the two families compress (activations in
 float32, bfloat16 or float16; gradients of parameters in float32):
   * dropout and dropout_backward, on the same counter-based generator, the
-    mask drawn again where it is needed instead of stored.
+    mask drawn again where it is needed instead of stored;
+  * linear_xent_loss and linear_xent_grad: softmax cross entropy of a linear
+    layer over a large vocabulary, the logits never kept.
 """
 from __future__ import annotations
 
@@ -108,6 +110,11 @@ def _declare(L):
     u64, u32, dbl = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_double
     L.dropout.argtypes = [_vp, _vp, _sz, _i, dbl, u64, u32, u64, _vp, _vp, _vp]
     L.dropout_backward.argtypes = [_vp, _sz, _i, dbl, u64, u32, u64, _vp, _vp, _vp]
+    i64 = ctypes.c_int64
+    L.linear_xent_loss.argtypes = [_vp, _vp, _i, _sz, _sz, _sz, _vp, i64, _vp, _vp, _vp,
+                                   ctypes.POINTER(_sz), _vp]
+    L.linear_xent_grad.argtypes = [_vp, _vp, _i, _sz, _sz, _sz, _vp, i64, _vp, _vp, _vp, _i, _vp,
+                                   _i, _vp, ctypes.POINTER(_sz), _vp]
     for name in ("compress_2bit", "decompress_2bit", "decompress_2bit_sum",
                  "compress_ternary", "decompress_ternary", "decompress_ternary_sum",
                  "gc_plan_2bit_multi_create", "gc_plan_block_offsets", "compress_2bit_multi",
@@ -115,7 +122,7 @@ def _declare(L):
                  "qsgd_maxnorm_quantize", "qsgd_dequant_sum",
                  "qsgd_quantize_sum",
                  "grandk_indices", "gather_f32", "grandk_mn_step",
-                 "dropout", "dropout_backward"):
+                 "dropout", "dropout_backward", "linear_xent_loss", "linear_xent_grad"):
         getattr(L, name).restype = _i
     return L
 
@@ -579,3 +586,84 @@ def dropout_backward(grad_out, p: float, seed: int, worker: int, grad_in, offset
                                    _dtype(grad_out, "grad_out"), float(p), _u64(seed),
                                    _worker(worker), _offset(offset), _step(step),
                                    _dev(grad_in, grad_out.dtype, "grad_in"), _stream(stream)))
+
+
+def _dtype_code(dtype) -> int:
+    """gc_dtype of a torch dtype."""
+    torch = _torch()
+    return _dtype(torch.empty(0, dtype=dtype), "dtype")
+
+
+def linear_xent_loss_ws_bytes(N: int, V: int, D: int, dtype) -> int:
+    """dtype: the torch dtype of hidden and weight."""
+    size = _sz(0)
+    _check(load().linear_xent_loss(None, None, _dtype_code(dtype), N, V, D, None, 0, None, None,
+                                   None, ctypes.byref(size), None))
+    return int(size.value)
+
+
+def linear_xent_grad_ws_bytes(N: int, V: int, D: int, dtype, dhidden_dtype=None,
+                              dweight_dtype=None) -> int:
+    """The gradients' dtypes default to that of hidden and weight."""
+    size = _sz(0)
+    code = _dtype_code(dtype)
+    _check(load().linear_xent_grad(
+        None, None, code, N, V, D, None, 0, None, None, None,
+        code if dhidden_dtype is None else _dtype_code(dhidden_dtype), None,
+        code if dweight_dtype is None else _dtype_code(dweight_dtype), None, ctypes.byref(size),
+        None))
+    return int(size.value)
+
+
+def _xent_sizes(hidden, weight, what: str):
+    """(N, V, D) of hidden [..., D] and weight [V, D]."""
+    if weight.dim() != 2 or hidden.dim() < 1 or hidden.shape[-1] != weight.shape[1]:
+        raise ValueError(f"{what}: hidden must be [..., D] and weight [V, D]")
+    V, D = weight.shape
+    if D == 0:
+        raise ValueError(f"{what}: the hidden size must be at least 1")
+    return hidden.numel() // D, V, D
+
+
+def linear_xent_loss(hidden, weight, target, loss, lse, ws, ignore_index: int = -100,
+                     stream=None) -> None:
+    """hidden [..., D] and weight [V, D] of one dtype; target int64, loss and
+    lse float32, one value a token; ws: uint8 device tensor of at least
+    linear_xent_loss_ws_bytes(N, V, D, dtype) bytes."""
+    torch = _torch()
+    N, V, D = _xent_sizes(hidden, weight, "linear_xent_loss")
+    if target.numel() != N or loss.numel() != N or lse.numel() != N:
+        raise ValueError("linear_xent_loss: target, loss and lse must hold one value a token")
+    size = _sz(ws.numel())
+    _check(load().linear_xent_loss(
+        _dev(hidden, hidden.dtype, "hidden"), _dev(weight, hidden.dtype, "weight"),
+        _dtype(hidden, "hidden"), N, V, D, _dev(target, torch.int64, "target"), int(ignore_index),
+        _dev(loss, torch.float32, "loss"), _dev(lse, torch.float32, "lse"),
+        _dev(ws, torch.uint8, "ws"), ctypes.byref(size), _stream(stream)))
+
+
+def linear_xent_grad(hidden, weight, target, lse, dloss, dhidden, dweight, ws,
+                     ignore_index: int = -100, stream=None) -> None:
+    """The gradient of (dloss * loss).sum(); dhidden or dweight may be None.
+    Each has the dtype of hidden and weight, or float32. ws: uint8 device
+    tensor of at least linear_xent_grad_ws_bytes(...) bytes for these dtypes
+    (a gradient left out counts as one of the inputs' dtype)."""
+    torch = _torch()
+    N, V, D = _xent_sizes(hidden, weight, "linear_xent_grad")
+    if target.numel() != N or dloss.numel() != N or lse.numel() != N:
+        raise ValueError("linear_xent_grad: target, lse and dloss must hold one value a token")
+    if dhidden is not None and dhidden.numel() != N * D:
+        raise ValueError("linear_xent_grad: dhidden differs from hidden in size")
+    if dweight is not None and dweight.numel() != V * D:
+        raise ValueError("linear_xent_grad: dweight differs from weight in size")
+    code = _dtype(hidden, "hidden")
+    h_code = code if dhidden is None else _dtype(dhidden, "dhidden")
+    w_code = code if dweight is None else _dtype(dweight, "dweight")
+    size = _sz(ws.numel())
+    _check(load().linear_xent_grad(
+        _dev(hidden, hidden.dtype, "hidden"), _dev(weight, hidden.dtype, "weight"), code, N, V, D,
+        _dev(target, torch.int64, "target"), int(ignore_index), _dev(lse, torch.float32, "lse"),
+        _dev(dloss, torch.float32, "dloss"),
+        _dev(dhidden, None if dhidden is None else dhidden.dtype, "dhidden"), h_code,
+        _dev(dweight, None if dweight is None else dweight.dtype, "dweight"), w_code,
+        _dev(ws, torch.uint8, "ws"), ctypes.byref(size), _stream(stream)))

@@ -1,0 +1,803 @@
+// linear_xent.hip -- softmax cross entropy of a linear layer over a large
+// vocabulary, and its gradient; the logits are never kept.
+//
+//   l_nv = <hidden_n, weight_v>,  lse_n = log sum_v exp(l_nv),
+//   loss_n = lse_n - l_n,target(n)
+//   G_nv = dloss_n (exp(l_nv - lse_n) - [v = target(n)])
+//   dhidden = G weight,  dweight = G^T hidden
+//
+// Loss: one product whose tiles end in the running maximum and sum of their
+// part of the vocabulary; a wave for each token joins the parts.
+// Gradient: piece by piece of the vocabulary, the logits are computed again
+// and turned into G in the tile's registers; G of one piece is the only
+// matrix of tokens x vocabulary that is ever in memory, and the two products
+// of the gradient read it back from the cache.
+#include <algorithm>
+#include <limits>
+#include <string>
+#include <type_traits>
+
+#include "mfma_product.h"
+
+namespace gcq {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;       // log2(e) rounded
+constexpr float kLog2eRest = 1.92596299112661746887e-8f; // what that rounding left
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// exp(x) for x <= 0 (and a little above): 2^(x log2 e) by v_exp_f32, the
+// rounding of the product put back as a factor.
+__device__ __forceinline__ float exp_neg(float x)
+{
+    const float hi = x * kLog2e;
+    const float lo = __builtin_fmaf(x, kLog2e, -hi) + x * kLog2eRest;
+    const float r = __builtin_amdgcn_exp2f(hi);
+    return r == 0.0f ? 0.0f : __builtin_fmaf(r, lo * kLn2, r);
+}
+
+// ---- operands as bf16 planes ------------------------------------------------
+
+constexpr int kMaxPlanes = 3;
+
+// The next plane of x: its bf16 rounding, which is taken off x (exactly). A
+// finite x never becomes infinite; an infinity or NaN stays in the first
+// plane alone.
+__device__ __forceinline__ bf16_t next_plane(float& x)
+{
+    const float top = 0x1.FEp127f;  // largest bf16
+    if (!(fabsf(x) <= std::numeric_limits<float>::max())) {
+        const bf16_t h = bf16_t(x);
+        x = 0.0f;
+        return h;
+    }
+    const bf16_t h = bf16_t(fminf(fmaxf(x, -top), top));
+    x -= float(h);
+    return h;
+}
+
+constexpr int kPlaneThreads = 256;
+
+// src [rows][d] -> kPlanes planes [rows_out][d_out] (d_out a multiple of 8),
+// one behind the other, zeros behind the last column and row and in the rows
+// whose target is no row of the vocabulary (`target` not NULL): what such
+// rows hold, NaN included, reaches nothing.
+template <typename T, int kPlanes>
+__global__ __launch_bounds__(kPlaneThreads) void planes_kernel(
+    const T* __restrict__ src, size_t rows, size_t d, bf16_t* __restrict__ out, size_t rows_out, size_t d_out,
+    const int64_t* __restrict__ target, int64_t ignore, size_t V)
+{
+    const size_t chunks = d_out / 8, total = rows_out * chunks;
+    const bool vec = (d & 7) == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+    for (size_t q = size_t(blockIdx.x) * kPlaneThreads + threadIdx.x; q < total;
+         q += size_t(gridDim.x) * kPlaneThreads) {
+        const size_t row = q / chunks, c = (q - row * chunks) * 8;
+        bool live = row < rows;
+        if (live && target) {
+            const int64_t t = target[row];
+            live = t != ignore && t >= 0 && size_t(t) < V;
+        }
+        float v[8] = {};
+        if (live && c < d) {
+            const T* p = src + row * d + c;
+            if (vec) {
+#pragma unroll
+                for (int k = 0; k < 8; k += kVec<T>) {
+                    const vec_f32<T> x = load_vec(p + k);
+#pragma unroll
+                    for (int e = 0; e < kVec<T>; ++e)
+                        v[k + e] = x[e];
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c + k < d)
+                        v[k] = float(p[k]);
+            }
+        }
+#pragma unroll
+        for (int plane = 0; plane < kPlanes; ++plane) {
+            bf16x8 h;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                h[k] = next_plane(v[k]);
+            *reinterpret_cast<bf16x8*>(out + plane * (rows_out * d_out) + row * d_out + c) = h;
+        }
+    }
+}
+
+// ---- tiles of the logits -------------------------------------------------------
+
+template <int TA, int TB, int WA, int WB>
+struct LogitTile {
+    using Product = TileProduct<false, false, TA, TB, WA, WB>;
+    static constexpr int kRowsA = TA / WA, kRowsB = TB / WB;  // of one wave
+};
+
+struct LossPart {
+    float top, sum;  // the maximum, and the sum of exp(l - top)
+};
+
+// Vocabulary tile x token tile. A wave's part of a token's row is kRowsA
+// logits, half of them in each half of the wave.
+template <int TA, int TB, int WA, int WB>
+__global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
+    MatOperand weight, MatOperand hidden, ProductShape sh, uint32_t N, uint32_t V,
+    const int64_t* __restrict__ target, LossPart* __restrict__ parts, uint32_t nparts,
+    float* __restrict__ target_logit)
+{
+    using L = LogitTile<TA, TB, WA, WB>;
+    using P = typename L::Product;
+    __shared__ bf16_t la0[TA * kStageK], la1[TA * kStageK], lb0[TB * kStageK], lb1[TB * kStageK];
+    uint32_t ta, tb;
+    tile_of(xcd_contiguous(blockIdx.x, gridDim.x), sh.tiles_a, sh.tiles_b, ta, tb);
+    typename P::Acc acc;
+    P::run(weight, hidden, sh, ta * TA, tb * TB, 0, sh.stages * sh.segments, la0, la1, lb0, lb1, acc);
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wa = wave % WA, wb = wave / WA;
+    const uint32_t a_wave = ta * TA + wa * L::kRowsA;
+#pragma unroll
+    for (int j = 0; j < P::RB; ++j) {
+        const uint32_t n = tb * TB + wb * L::kRowsB + j * 32 + acc_col(lane);
+        const int64_t t = n < N ? target[n] : -1;
+        // the target's place in this lane's part, if it is there
+        const uint32_t at = t >= 0 && t < int64_t(V) ? uint32_t(t) - a_wave : 0xFFFFFFFFu;
+        const uint32_t left = V > a_wave ? V - a_wave : 0;
+        float top = -INFINITY, mine = 0.0f;
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const uint32_t v = i * 32 + acc_row(e, lane);
+                if (v >= left)
+                    acc.v[i][j][e] = -INFINITY;
+                if (v == at) {
+                    mine = acc.v[i][j][e];
+                    found = true;
+                }
+                top = fmaxf(top, acc.v[i][j][e]);
+            }
+        if (found)
+            target_logit[n] = mine;
+        top = fmaxf(top, __shfl_xor(top, 32));
+        float sum = 0.0f;
+        // a part that holds no logit above -inf adds nothing
+        const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                sum += __builtin_amdgcn_exp2f((acc.v[i][j][e] - ref) * kLog2e);
+        sum += __shfl_xor(sum, 32);
+        if (lane < 32 && n < N)
+            parts[size_t(n) * nparts + ta * WA + wa] = LossPart{top, sum};
+    }
+}
+
+// One wave for each token joins the parts of its row.
+constexpr int kJoinThreads = 256;
+
+__global__ __launch_bounds__(kJoinThreads) void loss_join_kernel(
+    const LossPart* __restrict__ parts, uint32_t nparts, const float* __restrict__ target_logit,
+    const int64_t* __restrict__ target, int64_t ignore, uint32_t N, uint32_t V,
+    float* __restrict__ loss, float* __restrict__ lse)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    for (uint32_t n = blockIdx.x * (kJoinThreads / kWave) + threadIdx.x / kWave; n < N;
+         n += gridDim.x * (kJoinThreads / kWave)) {
+        float top = -INFINITY, sum = 0.0f;
+        for (uint32_t k = lane; k < nparts; k += kWave) {
+            const LossPart p = parts[size_t(n) * nparts + k];
+            const float both = fmaxf(top, p.top), ref = both == -INFINITY ? 0.0f : both;
+            sum = sum * exp_neg(top - ref) + p.sum * exp_neg(p.top - ref);
+            top = both;
+        }
+#pragma unroll
+        for (int off = kWave / 2; off > 0; off >>= 1) {
+            const float t2 = __shfl_xor(top, off), s2 = __shfl_xor(sum, off);
+            const float both = fmaxf(top, t2), ref = both == -INFINITY ? 0.0f : both;
+            sum = sum * exp_neg(top - ref) + s2 * exp_neg(t2 - ref);
+            top = both;
+        }
+        if (lane == 0) {
+            const float all = top + logf(sum);
+            lse[n] = all;
+            const int64_t t = target[n];
+            float x = 0.0f;
+            if (t != ignore)
+                x = t >= 0 && t < int64_t(V) ? all - target_logit[n]
+                                             : std::numeric_limits<float>::quiet_NaN();
+            loss[n] = x;
+        }
+    }
+}
+
+// G of one piece: columns v0 .. of the vocabulary, for rows 0 .. rows_out - 1
+// (zeros from N on, and behind the vocabulary). Each wave turns its part of
+// the tile into rows of G through LDS, so that the stores are whole rows.
+struct GradOut {
+    bf16_t* plane0;  // [rows_out][ld]
+    size_t plane_stride;
+    uint32_t ld, rows_out;
+};
+
+template <int TA, int TB, int WA, int WB, int kPlanes>
+__global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
+    MatOperand weight, MatOperand hidden, ProductShape sh, uint32_t N, uint32_t v0, uint32_t V,
+    const int64_t* __restrict__ target, int64_t ignore, const float* __restrict__ lse,
+    const float* __restrict__ dloss, GradOut out)
+{
+    using L = LogitTile<TA, TB, WA, WB>;
+    using P = typename L::Product;
+    __shared__ bf16_t la0[TA * kStageK], la1[TA * kStageK], lb0[TB * kStageK], lb1[TB * kStageK];
+    uint32_t ta, tb;
+    tile_of(xcd_contiguous(blockIdx.x, gridDim.x), sh.tiles_a, sh.tiles_b, ta, tb);
+    typename P::Acc acc;
+    P::run(weight, hidden, sh, ta * TA, tb * TB, 0, sh.stages * sh.segments, la0, la1, lb0, lb1, acc);
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wa = wave % WA, wb = wave / WA;
+    const uint32_t a_wave = ta * TA + wa * L::kRowsA, b_wave = tb * TB + wb * L::kRowsB;
+
+    // this wave's part of the staging buffers: kRowsB tokens x kRowsA values
+    constexpr int kPart = L::kRowsA * L::kRowsB, kPerBuffer = TA * kStageK / kPart;
+    static_assert(TA == TB || P::kWaves <= 2 * kPerBuffer, "the parts fit the buffers");
+    const int at = wave / kPerBuffer;
+    bf16_t* part = (at == 0 ? la0 : at == 1 ? la1 : at == 2 ? lb0 : lb1) + (wave % kPerBuffer) * kPart;
+    constexpr int kChunks = L::kRowsA / 8;
+
+#pragma unroll
+    for (int j = 0; j < P::RB; ++j) {
+        const uint32_t n = b_wave + j * 32 + acc_col(lane);
+        bool live = n < N;
+        uint32_t t = 0;
+        float z = 0.0f, d = 0.0f;
+        if (live) {
+            const int64_t tn = target[n];
+            live = tn != ignore && tn >= 0 && tn < int64_t(V);
+            t = uint32_t(tn);
+            z = lse[n];
+            d = dloss[n];
+        }
+#pragma unroll
+        for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const uint32_t v = v0 + a_wave + i * 32 + acc_row(e, lane);
+                const float p = exp_neg(acc.v[i][j][e] - z) - (v == t ? 1.0f : 0.0f);
+                acc.v[i][j][e] = live && v < V ? d * p : 0.0f;
+            }
+    }
+#pragma unroll
+    for (int plane = 0; plane < kPlanes; ++plane) {
+#pragma unroll
+        for (int j = 0; j < P::RB; ++j) {
+            const int row = j * 32 + int(acc_col(lane));
+#pragma unroll
+            for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                    bf16x4 w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = bf16_t(acc.v[i][j][q * 4 + e]);
+                        if (plane + 1 < kPlanes)
+                            acc.v[i][j][q * 4 + e] -= float(w[e]);
+                    }
+                    const int col = i * 32 + 8 * q + 4 * (lane >> 5);
+                    const int chunk = (col >> 3) ^ (row & (kChunks - 1));
+                    *reinterpret_cast<bf16x4*>(part + row * L::kRowsA + chunk * 8 + (col & 4)) = w;
+                }
+        }
+        wave_lds_sync();
+        constexpr int kRows = kWave / kChunks;
+#pragma unroll
+        for (int r = 0; r < L::kRowsB; r += kRows) {
+            const int row = r + lane / kChunks, chunk = lane % kChunks;
+            const uint32_t n = b_wave + row;
+            const bf16x8 w = *reinterpret_cast<const bf16x8*>(
+                part + row * L::kRowsA + ((chunk ^ (row & (kChunks - 1))) << 3));
+            if (n < out.rows_out)
+                *reinterpret_cast<bf16x8*>(out.plane0 + plane * out.plane_stride + size_t(n) * out.ld + a_wave + chunk * 8) = w;
+        }
+        wave_lds_sync();
+    }
+}
+
+// ---- the two products of the gradient ----------------------------------------
+
+// Where a product's tiles go: out[b][a], rows of ld values.
+template <typename T>
+struct ProductOut {
+    T* p;
+    size_t ld, split_stride;  // split s writes at p + s * split_stride
+    uint32_t na, nb;          // valid columns and rows
+    bool vec;                 // four values from a multiple of 4 on are aligned to their size
+    bool add;                 // onto what is there
+};
+
+template <bool kBK, int TA, int TB, int WA, int WB, typename T>
+__global__ __launch_bounds__(WA* WB* kWave, 2) void product_kernel(MatOperand A, MatOperand B,
+                                                                  ProductShape sh, ProductOut<T> out)
+{
+    using P = TileProduct<true, kBK, TA, TB, WA, WB>;
+    __shared__ bf16_t la0[TA * kStageK], la1[TA * kStageK], lb0[TB * kStageK], lb1[TB * kStageK];
+    const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x);
+    const uint32_t tiles = sh.tiles_a * sh.tiles_b, split = id / tiles;
+    uint32_t ta, tb;
+    tile_of(id - split * tiles, sh.tiles_a, sh.tiles_b, ta, tb);
+    const uint64_t all = uint64_t(sh.stages) * sh.segments;
+    typename P::Acc acc;
+    P::run(A, B, sh, ta * TA, tb * TB, uint32_t(all * split / sh.splits),
+           uint32_t(all * (split + 1) / sh.splits), la0, la1, lb0, lb1, acc);
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wa = wave % WA, wb = wave / WA;
+    T* p = out.p + split * out.split_stride;
+#pragma unroll
+    for (int j = 0; j < P::RB; ++j) {
+        const uint32_t b = tb * TB + wb * (TB / WB) + j * 32 + acc_col(lane);
+        if (b >= out.nb)
+            continue;
+#pragma unroll
+        for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t a = ta * TA + wa * (TA / WA) + i * 32 + acc_row(4 * q, lane);
+                T* o = p + size_t(b) * out.ld + a;
+                vec_of<float, 4> w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = acc.v[i][j][q * 4 + e];
+                if (out.vec && a + 4 <= out.na) {
+                    auto* o4 = reinterpret_cast<vec_of<T, 4>*>(o);
+                    if (out.add)
+                        w += __builtin_convertvector(*o4, vec_of<float, 4>);
+                    *o4 = __builtin_convertvector(w, vec_of<T, 4>);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (a + e < out.na)
+                            o[e] = T(out.add ? float(o[e]) + w[e] : w[e]);
+                }
+            }
+    }
+}
+
+// out[r][c] = sum over splits, in their order, of slab[s][r][c].
+constexpr int kSumThreads = 256;
+
+template <typename T>
+__global__ __launch_bounds__(kSumThreads) void sum_splits_kernel(const float* __restrict__ slab,
+                                                                 size_t ld, size_t split_stride,
+                                                                 uint32_t splits, size_t rows, size_t d,
+                                                                 T* __restrict__ out)
+{
+    // four columns a lane: slabs are padded to a multiple of 4
+    const size_t quads = ld / 4, total = rows * quads;
+    const bool vec = (d & 3) == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(T) - 1)) == 0;
+    for (size_t q = size_t(blockIdx.x) * kSumThreads + threadIdx.x; q < total;
+         q += size_t(gridDim.x) * kSumThreads) {
+        const size_t r = q / quads, c = (q - r * quads) * 4;
+        vec_of<float, 4> v = *reinterpret_cast<const vec_of<float, 4>*>(slab + r * ld + c);
+        for (uint32_t s = 1; s < splits; ++s)
+            v += *reinterpret_cast<const vec_of<float, 4>*>(slab + s * split_stride + r * ld + c);
+        T* o = out + r * d + c;
+        if (vec) {
+            *reinterpret_cast<vec_of<T, 4>*>(o) = __builtin_convertvector(v, vec_of<T, 4>);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < d)
+                    o[e] = T(v[e]);
+        }
+    }
+}
+
+// ---- host side -----------------------------------------------------------------
+
+size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
+size_t round_up(size_t a, size_t b) { return ceil_div(a, b) * b; }
+
+// Room for consecutive buffers in a workspace.
+struct Carver {
+    size_t used = 0;
+    size_t take(size_t bytes)
+    {
+        const size_t at = used;
+        used += align256(bytes);
+        return at;
+    }
+};
+
+// Sizes the index arithmetic of the kernels holds: 32-bit tokens, vocabulary
+// and channels, 32-bit byte offsets within a tile of 256 rows (2^31 / 512
+// values a row).
+constexpr size_t kMaxTokens = size_t(1) << 28, kMaxVocab = size_t(1) << 28, kMaxChannels = size_t(1) << 20;
+
+int check_sizes(const char* what, size_t N, size_t V, size_t D, int dtype)
+{
+    if (!dtype_bytes(dtype))
+        return fail(GC_EINVAL, std::string(what) + ": unknown dtype");
+    if (V == 0 || D == 0)
+        return fail(GC_EINVAL, std::string(what) + ": the vocabulary and the hidden size must be at least 1");
+    if (N > kMaxTokens || V > kMaxVocab || D > kMaxChannels)
+        return fail(GC_EUNSUPPORTED, std::string(what) + ": sizes beyond 2^28 tokens, 2^28 rows of the "
+                                                         "vocabulary or 2^20 channels");
+    return GC_OK;
+}
+
+// Whether the product can read the matrix where it is: exact in bf16, rows
+// aligned for 16-byte loads, whole stages.
+bool direct_ok(const void* p, size_t D, int dtype)
+{
+    return dtype == GC_BF16 && D % kStageK == 0 && aligned16(p);
+}
+
+// bf16 planes that hold a value of the type exactly (fp32 to 2^-24).
+int planes_of(int dtype) { return dtype == GC_BF16 ? 1 : dtype == GC_F16 ? 2 : 3; }
+
+// An operand's planes: the matrix itself, or copies in the workspace, which
+// has room for them whatever the address.
+struct PlaneRoom {
+    size_t rows, d, off;
+    int planes;
+};
+
+PlaneRoom plane_room(Carver& c, size_t rows, size_t D, int dtype)
+{
+    PlaneRoom r{};
+    r.rows = rows;
+    r.d = round_up(D, kStageK);
+    r.planes = planes_of(dtype);
+    r.off = c.take(r.planes * rows * r.d * 2);
+    return r;
+}
+
+unsigned stride_grid(size_t items, size_t per)
+{
+    return unsigned(std::max<size_t>(1, std::min(ceil_div(items, per), max_grid_blocks())));
+}
+
+// Lays out src as planes (or takes it as it is) and describes it as an
+// operand by rows; `rows_valid` of its rows may be read.
+MatOperand make_operand(const void* src, size_t rows, size_t D, int dtype, const PlaneRoom& room, char* ws,
+                        bool copy, const int64_t* target, int64_t ignore, size_t V, hipStream_t stream)
+{
+    MatOperand m{};
+    if (!copy) {
+        m.plane0 = static_cast<const bf16_t*>(src);
+        m.ld = uint32_t(D);
+        m.extent = uint32_t(rows);
+        return m;
+    }
+    bf16_t* out = reinterpret_cast<bf16_t*>(ws + room.off);
+    with_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        constexpr int kPlanes = sizeof(T) == 4 ? 3 : std::is_same_v<T, f16_t> ? 2 : 1;
+        hipLaunchKernelGGL((planes_kernel<T, kPlanes>), dim3(stride_grid(room.rows * (room.d / 8), kPlaneThreads)),
+                           dim3(kPlaneThreads), 0, stream, static_cast<const T*>(src), rows, D, out, room.rows,
+                           room.d, target, ignore, V);
+        return 0;
+    });
+    m.plane0 = out;
+    m.plane_stride = room.rows * room.d;
+    m.ld = uint32_t(room.d);
+    m.extent = uint32_t(room.rows);
+    return m;
+}
+
+// Products that feed fp32 results run to 2^-24 of a term, those of a 16-bit
+// result to 2^-16 (fp16) or 2^-8 (bf16): see g_planes.
+constexpr int kFullLimit = kMaxPlanes - 1;
+
+// Planes of G for a gradient of the type: one more rounding of the size of
+// the gradient's own for bf16, none that shows for the others.
+int g_planes(int dtype) { return dtype == GC_BF16 ? 1 : dtype == GC_F16 ? 2 : 3; }
+
+// ---- loss
+
+struct LossConfig {
+    int ta, tb, wa;
+};
+
+LossConfig loss_config(size_t N)
+{
+    return N <= 32 ? LossConfig{64, 32, 2} : LossConfig{256, 256, 2};
+}
+
+struct LossLayout {
+    LossConfig cfg;
+    PlaneRoom weight, hidden;
+    size_t parts, target_logit, nparts, total;
+};
+
+LossLayout loss_layout(size_t N, size_t V, size_t D, int dtype)
+{
+    LossLayout L{};
+    Carver c;
+    L.cfg = loss_config(N);
+    L.weight = plane_room(c, V, D, dtype);
+    L.hidden = plane_room(c, N, D, dtype);
+    L.nparts = ceil_div(V, L.cfg.ta) * L.cfg.wa;
+    L.parts = c.take(N * L.nparts * sizeof(LossPart));
+    L.target_logit = c.take(N * 4);
+    L.total = c.used;
+    return L;
+}
+
+// ---- gradient
+
+// G of one piece is kept to about this many bytes, which the last-level cache
+// holds (256 MB).
+constexpr size_t kPieceBytes = size_t(256) << 20;
+constexpr int kTile = 256;
+constexpr size_t kCus = 256;
+
+struct GradLayout {
+    PlaneRoom weight, hidden;
+    size_t n_pad, piece, pieces;  // rows of G, vocabulary of one piece
+    int g_planes;
+    size_t g, h_slab, w_slab, total;
+    size_t d4;  // row length of the slabs
+    uint32_t h_splits, w_splits;
+};
+
+// Splits of a product of `tiles` tiles over `stages` stages: enough to give
+// every compute unit a tile, at least 8 stages each.
+uint32_t splits_for(size_t tiles, size_t stages)
+{
+    return uint32_t(std::max<size_t>(1, std::min(kCus / std::max<size_t>(tiles, 1), stages / 8)));
+}
+
+ProductShape grad_shape(int planes_a, int out_dtype)
+{
+    ProductShape sh{};
+    set_pairs(sh, planes_a, g_planes(out_dtype), g_planes(out_dtype) - 1);
+    return sh;
+}
+
+GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, int dw_dtype)
+{
+    GradLayout L{};
+    Carver c;
+    L.weight = plane_room(c, V, D, dtype);
+    L.n_pad = round_up(N, kStageK);
+    L.hidden = plane_room(c, L.n_pad, D, dtype);
+    L.d4 = round_up(D, 4);
+    L.g_planes = std::max(g_planes(dh_dtype), g_planes(dw_dtype));
+    const size_t columns = kPieceBytes / (L.n_pad * 2 * L.g_planes) / kTile * kTile;
+    L.piece = std::min(std::max<size_t>(columns, kTile), round_up(V, kTile));
+    L.pieces = ceil_div(V, L.piece);
+    L.g = c.take(L.g_planes * L.n_pad * L.piece * 2);
+    const size_t ta = ceil_div(D, kTile);
+    L.h_splits = splits_for(ceil_div(N, kTile) * ta,
+                            L.piece / kStageK * grad_shape(L.weight.planes, dh_dtype).segments);
+    L.w_splits = splits_for(L.piece / kTile * ta, L.n_pad / kStageK * grad_shape(L.hidden.planes, dw_dtype).segments);
+    L.h_slab = c.take(L.h_splits > 1 || L.pieces > 1 ? L.h_splits * N * L.d4 * 4 : 0);
+    L.w_slab = c.take(L.w_splits > 1 ? L.w_splits * L.piece * L.d4 * 4 : 0);
+    L.total = c.used;
+    return L;
+}
+
+// A product into `out` of type T (or into the slab, when there is one).
+template <bool kBK, typename T>
+void launch_product(const MatOperand& A, const MatOperand& B, ProductShape sh, const ProductOut<T>& out,
+                    hipStream_t stream)
+{
+    hipLaunchKernelGGL((product_kernel<kBK, kTile, kTile, 2, 4, T>),
+                       dim3(sh.tiles_a * sh.tiles_b * sh.splits), dim3(8 * kWave), 0, stream, A, B, sh, out);
+}
+
+template <bool kBK>
+void launch_product_any(const MatOperand& A, const MatOperand& B, const ProductShape& sh, void* out, int dtype,
+                        size_t nb, size_t D, hipStream_t stream)
+{
+    with_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        ProductOut<T> o{};
+        o.p = static_cast<T*>(out);
+        o.ld = D;
+        o.na = uint32_t(D);
+        o.nb = uint32_t(nb);
+        o.vec = D % 4 == 0 && aligned_to(out, 4 * sizeof(T));
+        launch_product<kBK, T>(A, B, sh, o, stream);
+        return 0;
+    });
+}
+
+void launch_sum(const float* slab, size_t d4, size_t split_stride, uint32_t splits, size_t rows, size_t D,
+                void* out, int dtype, hipStream_t stream)
+{
+    with_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        hipLaunchKernelGGL(sum_splits_kernel<T>, dim3(stride_grid(rows * (d4 / 4), kSumThreads)),
+                           dim3(kSumThreads), 0, stream, slab, d4, split_stride, splits, rows, D,
+                           static_cast<T*>(out));
+        return 0;
+    });
+}
+
+__global__ __launch_bounds__(kSumThreads) void zero_kernel(uint16_t* out, size_t n)
+{
+    for (size_t i = size_t(blockIdx.x) * kSumThreads + threadIdx.x; i < n; i += size_t(gridDim.x) * kSumThreads)
+        out[i] = 0;
+}
+
+// bytes: even, as every type's size is.
+void launch_zero(void* out, size_t bytes, hipStream_t stream)
+{
+    hipLaunchKernelGGL(zero_kernel, dim3(stride_grid(bytes / 2, kSumThreads)), dim3(kSumThreads), 0, stream,
+                       static_cast<uint16_t*>(out), bytes / 2);
+}
+
+}  // namespace
+}  // namespace gcq
+
+using namespace gcq;
+
+GCQ_API int linear_xent_loss(const void* hidden, const void* weight, int dtype, size_t N, size_t V,
+                             size_t D, const int64_t* target, int64_t ignore_index, float* loss,
+                             float* lse, void* ws, size_t* ws_bytes, hipStream_t stream)
+{
+    clear_error();
+    if (int rc = check_sizes("linear_xent_loss", N, V, D, dtype))
+        return rc;
+    if (!ws_bytes)
+        return fail(GC_EINVAL, "linear_xent_loss: ws_bytes is NULL");
+    const LossLayout L = loss_layout(N, V, D, dtype);
+    if (!ws) {
+        *ws_bytes = L.total;
+        return GC_OK;
+    }
+    if (N == 0)
+        return GC_OK;
+    const size_t b = dtype_bytes(dtype);
+    if (!hidden || !weight || !target || !loss || !lse || !aligned_to(hidden, b) || !aligned_to(weight, b) ||
+        !aligned_to(target, 8) || !aligned4(loss) || !aligned4(lse))
+        return fail(GC_EINVAL, "linear_xent_loss: a buffer is NULL or misaligned");
+    if (!aligned16(ws) || *ws_bytes < L.total)
+        return fail(GC_EINVAL, "linear_xent_loss: workspace too small or not 16-byte aligned");
+    char* w = static_cast<char*>(ws);
+    const MatOperand wo = make_operand(weight, V, D, dtype, L.weight, w, !direct_ok(weight, D, dtype), nullptr,
+                                       0, 0, stream);
+    const MatOperand ho = make_operand(hidden, N, D, dtype, L.hidden, w, !direct_ok(hidden, D, dtype), nullptr,
+                                       0, 0, stream);
+    ProductShape sh{};
+    sh.stages = uint32_t(round_up(D, kStageK) / kStageK);
+    set_pairs(sh, L.weight.planes, L.hidden.planes, kFullLimit);
+    sh.tiles_a = uint32_t(ceil_div(V, L.cfg.ta));
+    sh.tiles_b = uint32_t(ceil_div(N, L.cfg.tb));
+    sh.splits = 1;
+    LossPart* parts = reinterpret_cast<LossPart*>(w + L.parts);
+    float* tl = reinterpret_cast<float*>(w + L.target_logit);
+    const dim3 grid(sh.tiles_a * sh.tiles_b);
+    if (L.cfg.ta == 64)
+        hipLaunchKernelGGL((loss_tiles_kernel<64, 32, 2, 1>), grid, dim3(2 * kWave), 0, stream, wo, ho, sh,
+                           uint32_t(N), uint32_t(V), target, parts, uint32_t(L.nparts), tl);
+    else
+        hipLaunchKernelGGL((loss_tiles_kernel<256, 256, 2, 4>), grid, dim3(8 * kWave), 0, stream, wo, ho, sh,
+                           uint32_t(N), uint32_t(V), target, parts, uint32_t(L.nparts), tl);
+    hipLaunchKernelGGL(loss_join_kernel, dim3(stride_grid(N, kJoinThreads / kWave)), dim3(kJoinThreads), 0,
+                       stream, parts, uint32_t(L.nparts), tl, target, ignore_index, uint32_t(N), uint32_t(V),
+                       loss, lse);
+    return check_launch("linear_xent_loss");
+}
+
+GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, size_t N, size_t V,
+                             size_t D, const int64_t* target, int64_t ignore_index, const float* lse,
+                             const float* dloss, void* dhidden, int dhidden_dtype, void* dweight,
+                             int dweight_dtype, void* ws, size_t* ws_bytes, hipStream_t stream)
+{
+    clear_error();
+    if (int rc = check_sizes("linear_xent_grad", N, V, D, dtype))
+        return rc;
+    if ((dhidden_dtype != dtype && dhidden_dtype != GC_F32) || (dweight_dtype != dtype && dweight_dtype != GC_F32))
+        return fail(GC_EINVAL, "linear_xent_grad: a gradient has the inputs' type or fp32");
+    if (!ws_bytes)
+        return fail(GC_EINVAL, "linear_xent_grad: ws_bytes is NULL");
+    if (!ws) {
+        *ws_bytes = N ? grad_layout(N, V, D, dtype, dhidden_dtype, dweight_dtype).total : 0;
+        return GC_OK;
+    }
+    const size_t b = dtype_bytes(dtype);
+    if (!aligned_to(dhidden, dtype_bytes(dhidden_dtype)) || !aligned_to(dweight, dtype_bytes(dweight_dtype)))
+        return fail(GC_EINVAL, "linear_xent_grad: a gradient is misaligned");
+    if (N == 0) {
+        if (dweight)
+            launch_zero(dweight, V * D * dtype_bytes(dweight_dtype), stream);
+        return check_launch("linear_xent_grad");
+    }
+    if (!hidden || !weight || !target || !lse || !dloss || !aligned_to(hidden, b) || !aligned_to(weight, b) ||
+        !aligned_to(target, 8) || !aligned4(lse) || !aligned4(dloss))
+        return fail(GC_EINVAL, "linear_xent_grad: a buffer is NULL or misaligned");
+    const GradLayout L = grad_layout(N, V, D, dtype, dhidden_dtype, dweight_dtype);
+    if (!aligned16(ws) || *ws_bytes < L.total)
+        return fail(GC_EINVAL, "linear_xent_grad: workspace too small or not 16-byte aligned");
+    if (!dhidden && !dweight)
+        return GC_OK;
+
+    char* w = static_cast<char*>(ws);
+    const MatOperand wo = make_operand(weight, V, D, dtype, L.weight, w, !direct_ok(weight, D, dtype), nullptr,
+                                       0, 0, stream);
+    // always a copy: rows without a target become zeros
+    const MatOperand ho = make_operand(hidden, N, D, dtype, L.hidden, w, true, target, ignore_index, V, stream);
+    GradOut g{};
+    MatOperand go{};
+    go.plane0 = g.plane0 = reinterpret_cast<bf16_t*>(w + L.g);
+    go.plane_stride = g.plane_stride = L.n_pad * L.piece;
+    go.ld = g.ld = uint32_t(L.piece);
+    g.rows_out = uint32_t(L.n_pad);
+    float* h_slab = reinterpret_cast<float*>(w + L.h_slab);
+    float* w_slab = reinterpret_cast<float*>(w + L.w_slab);
+    const bool h_direct = L.h_splits == 1 && L.pieces == 1;
+
+    for (size_t v0 = 0; v0 < V; v0 += L.piece) {
+        const size_t vp = std::min(L.piece, V - v0);
+        MatOperand wp = wo;
+        wp.plane0 += v0 * wo.ld;
+        wp.extent = uint32_t(vp);
+        ProductShape sh{};
+        sh.stages = uint32_t(round_up(D, kStageK) / kStageK);
+        set_pairs(sh, L.weight.planes, L.hidden.planes, kFullLimit);
+        sh.tiles_a = uint32_t(ceil_div(vp, kTile));
+        sh.tiles_b = uint32_t(ceil_div(L.n_pad, kTile));
+        sh.splits = 1;
+        const dim3 grid(sh.tiles_a * sh.tiles_b), block(8 * kWave);
+        const auto logits = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid, block, 0, stream, wp, ho, sh, uint32_t(N), uint32_t(v0), uint32_t(V),
+                               target, ignore_index, lse, dloss, g);
+        };
+        if (L.g_planes == 1)
+            logits(logit_grad_kernel<kTile, kTile, 2, 4, 1>);
+        else if (L.g_planes == 2)
+            logits(logit_grad_kernel<kTile, kTile, 2, 4, 2>);
+        else
+            logits(logit_grad_kernel<kTile, kTile, 2, 4, 3>);
+        if (dhidden) {
+            MatOperand A = wp, B = go;
+            A.extent = uint32_t(wo.ld);
+            A.krows = uint32_t(vp);
+            B.extent = uint32_t(N);
+            ProductShape ps = grad_shape(L.weight.planes, dhidden_dtype);
+            ps.stages = uint32_t(ceil_div(vp, kStageK));
+            ps.tiles_a = uint32_t(ceil_div(D, kTile));
+            ps.tiles_b = uint32_t(ceil_div(N, kTile));
+            ps.splits = L.h_splits;
+            if (h_direct) {
+                launch_product_any<false>(A, B, ps, dhidden, dhidden_dtype, N, D, stream);
+            } else {
+                ProductOut<float> o{h_slab, L.d4, N * L.d4, uint32_t(L.d4), uint32_t(N), true, v0 > 0};
+                launch_product<false, float>(A, B, ps, o, stream);
+            }
+        }
+        if (dweight) {
+            MatOperand A = ho, B = go;
+            A.extent = uint32_t(ho.ld);
+            A.krows = B.krows = uint32_t(L.n_pad);
+            B.extent = uint32_t(L.piece);
+            ProductShape ps = grad_shape(L.hidden.planes, dweight_dtype);
+            ps.stages = uint32_t(L.n_pad / kStageK);
+            ps.tiles_a = uint32_t(ceil_div(D, kTile));
+            ps.tiles_b = uint32_t(ceil_div(vp, kTile));
+            ps.splits = L.w_splits;
+            char* out = static_cast<char*>(dweight) + v0 * D * dtype_bytes(dweight_dtype);
+            if (L.w_splits == 1) {
+                launch_product_any<true>(A, B, ps, out, dweight_dtype, vp, D, stream);
+            } else {
+                ProductOut<float> o{w_slab, L.d4, L.piece * L.d4, uint32_t(L.d4), uint32_t(vp), true, false};
+                launch_product<true, float>(A, B, ps, o, stream);
+                launch_sum(w_slab, L.d4, L.piece * L.d4, L.w_splits, vp, D, out, dweight_dtype, stream);
+            }
+        }
+    }
+    if (dhidden && !h_direct)
+        launch_sum(h_slab, L.d4, N * L.d4, L.h_splits, N, D, dhidden, dhidden_dtype, stream);
+    return check_launch("linear_xent_grad");
+}

@@ -335,6 +335,51 @@ int dropout_backward(const void* grad_out, size_t n, int dtype, double p,
                      uint64_t seed, uint32_t worker, uint64_t offset,
                      const uint64_t* step, void* grad_in, hipStream_t stream);
 
+/* ---- softmax cross entropy of a linear layer over a large vocabulary ------- */
+
+/* For tokens n < N, with logits l_nv = <hidden[n], weight[v]> over v < V:
+ *   lse[n]  = log sum_v exp(l_nv)
+ *   loss[n] = lse[n] - l_n,target[n];  0 where target[n] == ignore_index; NaN
+ *             where target[n] is neither that nor a row of the vocabulary
+ * The logits are never kept: tiles of the product end in a running maximum
+ * and sum of their part of the vocabulary. bf16 inputs are multiplied as they
+ * are; fp16 and fp32 ones as two and three bf16 planes, which hold an fp16
+ * value exactly and an fp32 value to 2^-24 (four and six products). Sums are
+ * fp32.
+ *   hidden  [N, D], weight [V, D] of `dtype`, rows contiguous
+ *   target  [N] int64;  loss, lse [N] fp32 (lse is written for every row)
+ *   ws      16-byte-aligned workspace; ws == NULL: *ws_bytes is set to the
+ *           size needed for (N, V, D, dtype) and nothing is enqueued.
+ *           Otherwise *ws_bytes is its size and must be at least that.
+ *   N, V <= 2^28, D <= 2^20, V and D at least 1; N may be 0. */
+int linear_xent_loss(const void* hidden, const void* weight, int dtype, size_t N,
+                     size_t V, size_t D, const int64_t* target,
+                     int64_t ignore_index, float* loss, float* lse, void* ws,
+                     size_t* ws_bytes, hipStream_t stream);
+
+/* The gradient of sum_n dloss[n] * loss[n]. With
+ *   G_nv = dloss[n] * (exp(l_nv - lse[n]) - [v == target[n]]),  0 in the rows
+ *   whose target is ignore_index or no row of the vocabulary:
+ *   dhidden[n] = sum_v G_nv weight[v],   dweight[v] = sum_n G_nv hidden[n].
+ * A row without a target adds nothing, whatever hidden[n], lse[n] and
+ * dloss[n] hold there. G is formed piece by piece of the vocabulary (about
+ * 256 MB of the workspace); sums are fp32 in a fixed order.
+ *   lse, dloss  [N] fp32 (lse as linear_xent_loss gives it)
+ *   dhidden     [N, D] of dhidden_dtype, or NULL: not computed
+ *   dweight     [V, D] of dweight_dtype, or NULL: not computed
+ *   a gradient's type is the inputs' or fp32, and says how exactly it is
+ *   computed: for a bf16 gradient G is rounded to bf16 on its way into the
+ *   product, for an fp16 one to 16, for an fp32 one to 24 bits. An fp32
+ *   dweight is what compress_2bit and qsgd_maxnorm_quantize take.
+ *   ws          as in linear_xent_loss. The query asks by the types alone.
+ * N may be 0: dweight is then zero. */
+int linear_xent_grad(const void* hidden, const void* weight, int dtype, size_t N,
+                     size_t V, size_t D, const int64_t* target,
+                     int64_t ignore_index, const float* lse, const float* dloss,
+                     void* dhidden, int dhidden_dtype, void* dweight,
+                     int dweight_dtype, void* ws, size_t* ws_bytes,
+                     hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
