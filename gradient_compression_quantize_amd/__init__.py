@@ -24,6 +24,8 @@ Training operators, whose gradients the two families compress (activations in
 float32, bfloat16 or float16; gradients of parameters in float32):
   * dropout and dropout_backward, on the same counter-based generator, the
     mask drawn again where it is needed instead of stored;
+  * norm_residual and norm_residual_grad: the norms around a block fused with
+    its dropout, gate and residual scale;
   * linear_xent_loss and linear_xent_grad: softmax cross entropy of a linear
     layer over a large vocabulary, the logits never kept.
 """
@@ -110,6 +112,11 @@ def _declare(L):
     u64, u32, dbl = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_double
     L.dropout.argtypes = [_vp, _vp, _sz, _i, dbl, u64, u32, u64, _vp, _vp, _vp]
     L.dropout_backward.argtypes = [_vp, _sz, _i, dbl, u64, u32, u64, _vp, _vp, _vp]
+    L.norm_residual.argtypes = [_vp, _vp, _i, _sz, _sz, _vp, _vp, _sz, _vp, _f, _f, dbl, u64, u32,
+                                _vp, _vp, _vp, _vp, _vp, _vp]
+    L.norm_residual_grad.argtypes = [_vp, _vp, _i, _sz, _sz, _vp, _vp, _sz, _vp, _f, dbl, u64, u32,
+                                     _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     ctypes.POINTER(_sz), _vp]
     i64 = ctypes.c_int64
     L.linear_xent_loss.argtypes = [_vp, _vp, _i, _sz, _sz, _sz, _vp, i64, _vp, _vp, _vp,
                                    ctypes.POINTER(_sz), _vp]
@@ -122,7 +129,8 @@ def _declare(L):
                  "qsgd_maxnorm_quantize", "qsgd_dequant_sum",
                  "qsgd_quantize_sum",
                  "grandk_indices", "gather_f32", "grandk_mn_step",
-                 "dropout", "dropout_backward", "linear_xent_loss", "linear_xent_grad"):
+                 "dropout", "dropout_backward", "norm_residual", "norm_residual_grad",
+                 "linear_xent_loss", "linear_xent_grad"):
         getattr(L, name).restype = _i
     return L
 
@@ -586,6 +594,79 @@ def dropout_backward(grad_out, p: float, seed: int, worker: int, grad_in, offset
                                    _dtype(grad_out, "grad_out"), float(p), _u64(seed),
                                    _worker(worker), _offset(offset), _step(step),
                                    _dev(grad_in, grad_out.dtype, "grad_in"), _stream(stream)))
+
+
+def _norm_shape(y, what: str, same, gate, columns, per_row):
+    """(rows, d, gates) of y [..., d], after the sizes of everything else:
+    `same` like y, `columns` of d values, `per_row` of one value a row."""
+    if y.dim() < 1 or y.shape[-1] == 0:
+        raise ValueError(f"{what}: a row must hold at least one value")
+    d = y.shape[-1]
+    rows = y.numel() // d
+    if any(t is not None and t.numel() != rows * d for t in same):
+        raise ValueError(f"{what}: the activations differ in size")
+    if any(t is not None and t.numel() != d for t in columns):
+        raise ValueError(f"{what}: a gain must hold one value a column")
+    if any(t is not None and t.numel() != rows for t in per_row):
+        raise ValueError(f"{what}: rstd_post and rstd_pre must hold one value a row")
+    if gate is None:
+        return rows, d, 1
+    gates = gate.numel() // d
+    if gates == 0 or gate.numel() != gates * d or rows % gates:
+        raise ValueError(f"{what}: gate must be [gates, d], gates dividing the rows")
+    return rows, d, gates
+
+
+def norm_residual(x, y, z, h=None, post_gain=None, gate=None, pre_gain=None,
+                  residual_scale: float = 1.0, eps: float = 1e-6, p: float = 0.0, seed: int = 0,
+                  worker: int = 0, step=None, rstd_post=None, rstd_pre=None, stream=None) -> None:
+    """z = residual_scale * x + gate * dropout(norm(y) * post_gain) and
+    h = norm(z) * pre_gain. x, y, z, h: [..., d] of one dtype; gains [d], gate
+    [gates, d] or [d], rstd_post and rstd_pre (one value a row) float32."""
+    torch = _torch()
+    rows, d, gates = _norm_shape(y, "norm_residual", (x, z, h), gate, (post_gain, pre_gain),
+                                 (rstd_post, rstd_pre))
+    f32 = torch.float32
+    _check(load().norm_residual(
+        _dev(x, y.dtype, "x"), _dev(y, y.dtype, "y"), _dtype(y, "y"), rows, d,
+        _dev(post_gain, f32, "post_gain"), _dev(gate, f32, "gate"), gates,
+        _dev(pre_gain, f32, "pre_gain"), float(residual_scale), float(eps), float(p), _u64(seed),
+        _worker(worker), _step(step), _dev(z, y.dtype, "z"), _dev(h, y.dtype, "h"),
+        _dev(rstd_post, f32, "rstd_post"), _dev(rstd_pre, f32, "rstd_pre"), _stream(stream)))
+
+
+def norm_residual_grad_ws_bytes(rows: int, d: int, gates: int = 1) -> int:
+    size = _sz(0)
+    null = [None] * 11
+    _check(load().norm_residual_grad(None, None, GC_F32, rows, d, None, None, gates, None, 1.0,
+                                     0.0, 0, 0, None, *null[:10], ctypes.byref(size), None))
+    return int(size.value)
+
+
+def norm_residual_grad(z, y, dx, dy, ws, dz=None, dh=None, post_gain=None, gate=None,
+                       pre_gain=None, residual_scale: float = 1.0, p: float = 0.0, seed: int = 0,
+                       worker: int = 0, step=None, rstd_post=None, rstd_pre=None, dpost_gain=None,
+                       dgate=None, dpre_gain=None, stream=None) -> None:
+    """The gradient of norm_residual, from its z, y, arguments and rstd. ws:
+    uint8 device tensor of at least norm_residual_grad_ws_bytes(rows, d,
+    gates) bytes. The gains' and gate's gradients are float32, or None."""
+    torch = _torch()
+    rows, d, gates = _norm_shape(y, "norm_residual_grad", (z, dx, dy, dz, dh), gate,
+                                 (post_gain, pre_gain, dpost_gain, dpre_gain),
+                                 (rstd_post, rstd_pre))
+    if dgate is not None and (gate is None or dgate.numel() != gate.numel()):
+        raise ValueError("norm_residual_grad: dgate differs from gate in size")
+    f32 = torch.float32
+    size = _sz(ws.numel())
+    _check(load().norm_residual_grad(
+        _dev(z, y.dtype, "z"), _dev(y, y.dtype, "y"), _dtype(y, "y"), rows, d,
+        _dev(post_gain, f32, "post_gain"), _dev(gate, f32, "gate"), gates,
+        _dev(pre_gain, f32, "pre_gain"), float(residual_scale), float(p), _u64(seed),
+        _worker(worker), _step(step), _dev(rstd_post, f32, "rstd_post"),
+        _dev(rstd_pre, f32, "rstd_pre"), _dev(dz, y.dtype, "dz"), _dev(dh, y.dtype, "dh"),
+        _dev(dx, y.dtype, "dx"), _dev(dy, y.dtype, "dy"), _dev(dpost_gain, f32, "dpost_gain"),
+        _dev(dgate, f32, "dgate"), _dev(dpre_gain, f32, "dpre_gain"), _dev(ws, torch.uint8, "ws"),
+        ctypes.byref(size), _stream(stream)))
 
 
 def _dtype_code(dtype) -> int:

@@ -24,7 +24,8 @@ LIB_PATH = PKG / "libgcq.so"
 CEILINGS_LIB_PATH = PKG / "libgcq_ceilings.so"
 BUILD_DIR = PKG / "_build"
 
-SOURCES = ["status.hip", "twobit.hip", "ternary.hip", "qsgd.hip", "dropout.hip", "linear_xent.hip"]
+SOURCES = ["status.hip", "twobit.hip", "ternary.hip", "qsgd.hip", "dropout.hip", "norm_residual.hip",
+           "linear_xent.hip"]
 # the benchmark's HBM ceiling kernels: a library of their own
 CEILINGS_SOURCES = ["hbm_ceilings.hip"]
 

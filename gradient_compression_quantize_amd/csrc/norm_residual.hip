@@ -1,0 +1,688 @@
+// norm_residual.hip -- the path between two blocks of a transformer, and its
+// gradient: the norm behind a block, its dropout, its gate, the scaled
+// residual sum, and the norm in front of the next block.
+//
+//   u = y rstd(y) post,   z = s x + gate drop(u),   h = z rstd(z) pre
+//   rstd(v) = (mean v^2 + eps)^-1/2
+//
+// A row is held in the registers of its team of threads (a wave up to four
+// 16-byte vectors a lane, then 4 to 16 waves), so that each activation is
+// read once and written once. A team takes a contiguous range of rows and
+// keeps what its columns need of the gains and the gate in registers.
+//
+// Gradient, with t the whole gradient of z, q = gate mask post yhat:
+//   t = dz + rstd_z (dh pre - zhat c1),  c1 = mean(dh pre zhat)
+//   dx = s t,   dy = rstd_y (t gate mask post - yhat c2)
+//   c2 = mean(t q) = mean(q (dz + rstd_z dh pre)) - rstd_z c1 mean(q zhat)
+// so one exchange of three sums serves both means. The gradients of the gains
+// and the gate are sums over rows: a workgroup adds its rows in registers,
+// writes one partial row, and a second launch adds the partial rows in their
+// order.
+#include "dropout_mask.h"
+
+#include <algorithm>
+#include <string>
+
+namespace gcq {
+namespace {
+
+constexpr size_t kMaxNormD = 16384;
+
+struct NormArgs {
+    const float *post, *gate, *pre;  // NULL: 1 and no norm, 1, no h
+    size_t rows, rows_per_gate;
+    uint32_t d;
+    float scale, eps, inv_d;
+    DropoutArgs drop;
+};
+
+// ---- a row in the registers of a team -----------------------------------------
+
+// Vector v of team lane t is v * kTeam + t; kAligned: every row starts on 16
+// bytes (otherwise the loads and stores are aligned to the element alone).
+template <typename T, int kTeam, int kVecs, bool kAligned>
+struct Row {
+    static constexpr int V = kVec<T>;
+    static constexpr int kWg = kTeam < 256 ? 256 : kTeam;
+    static constexpr int kTeams = kWg / kTeam;  // of a workgroup
+    using F = vec_f32<T>;
+    typedef T Raw __attribute__((ext_vector_type(kVec<T>)));
+    typedef Raw RawAny __attribute__((aligned(sizeof(T))));
+
+    static __device__ __forceinline__ uint32_t col(int v, int t) { return (v * kTeam + t) * V; }
+
+    static __device__ __forceinline__ Raw load_raw(const T* row, uint32_t c, uint32_t d)
+    {
+        if (c + V <= d) {
+            if (kAligned)
+                return *reinterpret_cast<const Raw*>(row + c);
+            return *reinterpret_cast<const RawAny*>(row + c);
+        }
+        Raw r = {};
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (c + e < d)
+                r[e] = row[c + e];
+        return r;
+    }
+
+    static __device__ __forceinline__ void load(Raw (&r)[kVecs], const T* p, size_t row, uint32_t d, int t)
+    {
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            r[v] = load_raw(p + row * d, col(v, t), d);
+    }
+
+    static __device__ __forceinline__ F wide(Raw r) { return __builtin_convertvector(r, F); }
+
+    static __device__ __forceinline__ void store(T* row, uint32_t c, uint32_t d, F x)
+    {
+        const Raw r = __builtin_convertvector(x, Raw);
+        if (c + V <= d) {
+            if (kAligned)
+                *reinterpret_cast<Raw*>(row + c) = r;
+            else
+                *reinterpret_cast<RawAny*>(row + c) = r;
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (c + e < d)
+                row[c + e] = r[e];
+    }
+
+    // fp32 values of columns: 1 where there is no array.
+    static __device__ __forceinline__ F columns(const float* p, uint32_t c, uint32_t d)
+    {
+        F f;
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            f[e] = !p ? 1.0f : c + e < d ? p[c + e] : 0.0f;
+        return f;
+    }
+
+    // 0 or 1 / (1 - p) for the values i .. i + V - 1 of the mask; i mod 4 is
+    // the same for a whole row.
+    static __device__ __forceinline__ F mask(const DropoutArgs& a, uint64_t key, uint64_t i)
+    {
+        const uint32_t phase = __builtin_amdgcn_readfirstlane(uint32_t(i) & 3);
+        uint32_t w[V + 4];
+#pragma unroll
+        for (int s = 0; s < V / 4; ++s) {
+            const U4 r = dropout_words(a, key, (i >> 2) + s);
+            w[4 * s] = r.x;
+            w[4 * s + 1] = r.y;
+            w[4 * s + 2] = r.z;
+            w[4 * s + 3] = r.w;
+        }
+        if (phase) {
+            const U4 r = dropout_words(a, key, (i >> 2) + V / 4);
+            w[V] = r.x;
+            w[V + 1] = r.y;
+            w[V + 2] = r.z;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                w[e] = phase == 1 ? w[e + 1] : phase == 2 ? w[e + 2] : w[e + 3];
+        }
+        F f;
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            f[e] = dropout_keeps(a, w[e]) ? a.scale : 0.0f;
+        return f;
+    }
+};
+
+// Sums over a team; every lane gets them. Teams of several waves are whole
+// workgroups and exchange through LDS, alternating between two halves so that
+// one barrier an exchange suffices.
+template <int kTeam, int kCount>
+struct TeamSum {
+    static constexpr int kWaves = kTeam / kWave;
+
+    static __device__ __forceinline__ void run(float (&x)[kCount], float* lds, int& half)
+    {
+#pragma unroll
+        for (int k = 0; k < kCount; ++k)
+#pragma unroll
+            for (int off = kWave / 2; off > 0; off >>= 1)
+                x[k] += __shfl_xor(x[k], off);
+        if (kWaves == 1)
+            return;
+        float* at = lds + half * (kWaves * kCount);
+        half ^= 1;
+        const int wave = threadIdx.x / kWave;
+        if ((threadIdx.x & (kWave - 1)) == 0) {
+#pragma unroll
+            for (int k = 0; k < kCount; ++k)
+                at[k * kWaves + wave] = x[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kCount; ++k) {
+            x[k] = at[k * kWaves];
+            for (int w = 1; w < kWaves; ++w)
+                x[k] += at[k * kWaves + w];
+        }
+    }
+};
+
+// ---- forward --------------------------------------------------------------------
+//
+// Outputs may be the inputs' own buffers: a thread writes only the values that
+// it alone has read before.
+
+template <typename T, int kTeam, int kVecs, bool kAligned>
+__global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_kernel(
+    const T* x, const T* y, NormArgs a, T* z, T* h, float* rstd_post, float* rstd_pre, size_t teams)
+{
+    using R = Row<T, kTeam, kVecs, kAligned>;
+    using F = typename R::F;
+    __shared__ float lds[2 * (kTeam / kWave)];
+    int half = 0;
+    const int t = threadIdx.x % kTeam;
+    const size_t team = size_t(blockIdx.x) * R::kTeams + threadIdx.x / kTeam;
+    if (team >= teams)
+        return;  // only teams of one wave share a workgroup
+    const size_t lo = a.rows * team / teams, hi = a.rows * (team + 1) / teams;
+    if (lo >= hi)
+        return;
+    const uint64_t key = dropout_key(a.drop);
+    F w[kVecs], pre[kVecs];  // gate * post of the current group, and pre
+    size_t group_end = 0;  // the first row of the next group
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+        pre[v] = R::columns(a.pre, R::col(v, t), a.d);
+    typename R::Raw rx[kVecs], ry[kVecs];
+    R::load(rx, x, lo, a.d, t);
+    R::load(ry, y, lo, a.d, t);
+    for (size_t row = lo; row < hi; ++row) {
+        if (row >= group_end) {
+            const size_t group = row / a.rows_per_gate;
+            group_end = (group + 1) * a.rows_per_gate;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                const uint32_t c = R::col(v, t);
+                w[v] = R::columns(a.post, c, a.d) * R::columns(a.gate ? a.gate + group * a.d : nullptr, c, a.d);
+            }
+        }
+        F fx[kVecs], fy[kVecs];
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            fx[v] = R::wide(rx[v]);
+            fy[v] = R::wide(ry[v]);
+        }
+        if (row + 1 < hi) {  // under this row's arithmetic
+            R::load(rx, x, row + 1, a.d, t);
+            R::load(ry, y, row + 1, a.d, t);
+        }
+        float rp = 1.0f;
+        if (a.post) {
+            float s[1] = {0.0f};
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+                for (int e = 0; e < R::V; ++e)
+                    s[0] += fy[v][e] * fy[v][e];
+            TeamSum<kTeam, 1>::run(s, lds, half);
+            rp = 1.0f / sqrtf(s[0] * a.inv_d + a.eps);
+            if (t == 0)
+                rstd_post[row] = rp;
+        }
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            const uint32_t c = R::col(v, t);
+            F b = fy[v] * rp * w[v];
+            if (a.drop.threshold) {
+                const F m = R::mask(a.drop, key, uint64_t(row) * a.d + c);
+#pragma unroll
+                for (int e = 0; e < R::V; ++e)  // 0 where dropped, whatever y holds
+                    b[e] = m[e] == 0.0f ? 0.0f : b[e] * m[e];
+            }
+            fx[v] = fx[v] * a.scale + b;
+#pragma unroll
+            for (int e = 0; e < R::V; ++e)
+                s[0] += fx[v][e] * fx[v][e];
+            R::store(z + row * a.d, c, a.d, fx[v]);
+        }
+        if (a.pre) {
+            TeamSum<kTeam, 1>::run(s, lds, half);
+            const float rz = 1.0f / sqrtf(s[0] * a.inv_d + a.eps);
+            if (t == 0)
+                rstd_pre[row] = rz;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+                R::store(h + row * a.d, R::col(v, t), a.d, fx[v] * rz * pre[v]);
+        }
+    }
+}
+
+// ---- backward -------------------------------------------------------------------
+
+struct NormGradArgs {
+    const float *rstd_post, *rstd_pre;
+    float *part_post, *part_pre;  // [workgroups][d]
+    float* gate_out;              // [gate strips][d]: partial rows, or dgate itself
+    size_t strips;                // workgroup ranges: strips of rows
+    size_t strips_per_gate;       // > 1: a gate's rows are split over so many strips
+    size_t gates_per_strip;       // > 1: a strip has so many gates (then strips_per_gate is 1)
+};
+
+// One workgroup for each strip of rows; its teams take the rows in turn. The
+// rows of a strip share a gate, or the strip holds whole gates.
+template <typename T, int kTeam, int kVecs, bool kAligned>
+__global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_grad_kernel(
+    const T* z, const T* y, const T* dz, const T* dh, NormArgs a, NormGradArgs g, T* dx, T* dy)
+{
+    using R = Row<T, kTeam, kVecs, kAligned>;
+    using F = typename R::F;
+    // exchanges of a team of several waves, or the sum over teams of one wave
+    constexpr int kLds = R::kTeams > 1 ? (R::kTeams - 1) * kTeam * kVecs * R::V : 2 * 3 * (kTeam / kWave);
+    __shared__ float lds[kLds];
+    int half = 0;
+    const int t = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
+    const uint64_t key = dropout_key(a.drop);
+    const size_t strip = blockIdx.x;
+    const size_t gates = a.rows / a.rows_per_gate;
+    // gates [g_lo, g_hi) of this strip, and its rows of the first one
+    const size_t g_lo = g.strips_per_gate > 1 ? strip / g.strips_per_gate : strip * g.gates_per_strip;
+    const size_t g_hi = g.strips_per_gate > 1 ? g_lo + 1 : std::min(g_lo + g.gates_per_strip, gates);
+
+    F post[kVecs], pre[kVecs], sum_post[kVecs], sum_pre[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+        post[v] = R::columns(a.post, R::col(v, t), a.d);
+        pre[v] = R::columns(a.pre, R::col(v, t), a.d);
+        sum_post[v] = F{};
+        sum_pre[v] = F{};
+    }
+    // teams of one wave: sums over the workgroup's teams end in team 0
+    const auto over_teams = [&](F (&s)[kVecs]) {
+        if (R::kTeams == 1)
+            return;
+        __syncthreads();
+        if (team > 0) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+                for (int e = 0; e < R::V; ++e)
+                    lds[(((team - 1) * kVecs + v) * R::V + e) * kTeam + t] = s[v][e];
+        }
+        __syncthreads();
+        if (team == 0) {
+            for (int o = 0; o < R::kTeams - 1; ++o)
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+                    for (int e = 0; e < R::V; ++e)
+                        s[v][e] += lds[((o * kVecs + v) * R::V + e) * kTeam + t];
+        }
+    };
+    const auto write = [&](float* p, const F (&s)[kVecs]) {
+        if (R::kTeams > 1 && team > 0)
+            return;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+            for (int e = 0; e < R::V; ++e) {
+                const uint32_t c = R::col(v, t) + e;
+                if (c < a.d)
+                    p[c] = s[v][e];
+            }
+    };
+
+    for (size_t gate = g_lo; gate < g_hi; ++gate) {
+        size_t lo = gate * a.rows_per_gate, hi = lo + a.rows_per_gate;
+        if (g.strips_per_gate > 1) {
+            const size_t s = strip - gate * g.strips_per_gate, n = a.rows_per_gate;
+            hi = lo + n * (s + 1) / g.strips_per_gate;
+            lo = lo + n * s / g.strips_per_gate;
+        }
+        F fg[kVecs], sum_gate[kVecs];
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            fg[v] = R::columns(a.gate ? a.gate + gate * a.d : nullptr, R::col(v, t), a.d);
+            sum_gate[v] = F{};
+        }
+        for (size_t row = lo + team; row < hi; row += R::kTeams) {
+            const float rz = a.pre ? g.rstd_pre[row] : 0.0f, ry = a.post ? g.rstd_post[row] : 1.0f;
+            F zn[kVecs], yn[kVecs], e[kVecs], m[kVecs];
+            float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                const uint32_t c = R::col(v, t);
+                yn[v] = R::wide(R::load_raw(y + row * a.d, c, a.d)) * ry;
+                e[v] = dz ? R::wide(R::load_raw(dz + row * a.d, c, a.d)) : F{};
+                m[v] = F{} + 1.0f;
+                if (a.drop.threshold) {
+                    m[v] = R::mask(a.drop, key, uint64_t(row) * a.d + c);
+#pragma unroll
+                    for (int k = 0; k < R::V; ++k)  // a dropped y takes no part, whatever it holds
+                        yn[v][k] = m[v][k] == 0.0f && !a.post ? 0.0f : yn[v][k];
+                }
+                if (a.pre) {
+                    zn[v] = R::wide(R::load_raw(z + row * a.d, c, a.d)) * rz;
+                    const F h = R::wide(R::load_raw(dh + row * a.d, c, a.d));
+                    sum_pre[v] += h * zn[v];
+                    const F p = h * pre[v], q = fg[v] * m[v] * post[v] * yn[v];
+                    e[v] += p * rz;
+#pragma unroll
+                    for (int k = 0; k < R::V; ++k) {
+                        s[0] += p[k] * zn[v][k];
+                        s[1] += q[k] * e[v][k];
+                        s[2] += q[k] * zn[v][k];
+                    }
+                } else {
+                    zn[v] = F{};
+                    const F q = fg[v] * m[v] * post[v] * yn[v];
+#pragma unroll
+                    for (int k = 0; k < R::V; ++k)
+                        s[1] += q[k] * e[v][k];
+                }
+            }
+            TeamSum<kTeam, 3>::run(s, lds, half);
+            const float c1 = rz * (s[0] * a.inv_d);
+            const float c2 = a.post ? (s[1] - c1 * s[2]) * a.inv_d : 0.0f;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                const uint32_t c = R::col(v, t);
+                const F whole = e[v] - zn[v] * c1;
+                R::store(dx + row * a.d, c, a.d, whole * a.scale);
+                const F wm = whole * m[v], wy = wm * yn[v];
+                sum_gate[v] += wy * post[v];
+                sum_post[v] += wy * fg[v];
+                R::store(dy + row * a.d, c, a.d, (wm * fg[v] * post[v] - yn[v] * c2) * ry);
+            }
+        }
+        if (g.gate_out) {
+            over_teams(sum_gate);
+            write(g.gate_out + (g.strips_per_gate > 1 ? strip : gate) * a.d, sum_gate);
+        }
+    }
+    if (g.part_post) {
+        over_teams(sum_post);
+        write(g.part_post + strip * a.d, sum_post);
+    }
+    if (g.part_pre) {
+        over_teams(sum_pre);
+        write(g.part_pre + strip * a.d, sum_pre);
+    }
+}
+
+// out[k][c] = sum over the `count` partial rows of k, in a fixed order: 16
+// threads a column take every 16th row, and their sums are added in order.
+constexpr int kSumCols = 64, kSumRows = 16;
+
+struct PartSum {
+    const float* part;
+    float* out;
+    uint32_t count;  // partial rows of one output row
+    uint32_t rows;   // output rows
+};
+
+__global__ __launch_bounds__(kSumCols* kSumRows) void sum_parts_kernel(PartSum a, PartSum b, PartSum c, uint32_t d)
+{
+    __shared__ float lds[kSumRows][kSumCols];
+    const uint32_t col = blockIdx.x * kSumCols + threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
+    for (uint32_t row = blockIdx.y; row < a.rows + b.rows + c.rows; row += gridDim.y) {
+        uint32_t k = row;
+        PartSum p = a;
+        if (k >= a.rows) {
+            k -= a.rows;
+            p = b;
+            if (k >= b.rows) {
+                k -= b.rows;
+                p = c;
+            }
+        }
+        float s = 0.0f;
+        if (col < d)
+            for (uint32_t i = r; i < p.count; i += kSumRows)
+                s += p.part[(size_t(k) * p.count + i) * d + col];
+        lds[r][threadIdx.x % kSumCols] = s;
+        __syncthreads();
+        if (r == 0 && col < d) {
+            for (int i = 1; i < kSumRows; ++i)
+                s += lds[i][threadIdx.x];
+            p.out[size_t(k) * d + col] = s;
+        }
+        __syncthreads();
+    }
+}
+
+// ---- host side --------------------------------------------------------------------
+
+// Calls f(team, vecs) with the smallest team that holds a row of `vecs`
+// vectors, as integral constants.
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+template <typename F>
+void with_team(size_t vecs, F f)
+{
+    if (vecs <= 64)
+        f(Int<64>(), Int<1>());
+    else if (vecs <= 128)
+        f(Int<64>(), Int<2>());
+    else if (vecs <= 256)
+        f(Int<256>(), Int<1>());
+    else if (vecs <= 512)
+        f(Int<256>(), Int<2>());
+    else if (vecs <= 1024)
+        f(Int<512>(), Int<2>());
+    else if (vecs <= 2048)
+        f(Int<1024>(), Int<2>());
+    else
+        f(Int<1024>(), Int<4>());
+}
+
+// Teams of one launch: waves for a few rounds of every compute unit.
+constexpr size_t kForwardWaves = 256 * 16;
+
+// Strips of the backward launch, each of which leaves a partial row: two
+// workgroups a compute unit.
+constexpr size_t kGradStrips = 512;
+
+struct GradStrips {
+    size_t strips, per_gate, gates_per;
+};
+
+GradStrips grad_strips(size_t rows, size_t gates)
+{
+    GradStrips s{};
+    const size_t rows_per_gate = rows / gates;
+    if (gates >= kGradStrips / 2) {
+        s.per_gate = 1;
+        s.gates_per = ceil_div(gates, kGradStrips);
+        s.strips = ceil_div(gates, s.gates_per);
+    } else {
+        // at least four rows a strip
+        s.per_gate = std::max<size_t>(1, std::min(kGradStrips / gates, rows_per_gate / 4));
+        s.gates_per = 1;
+        s.strips = gates * s.per_gate;
+    }
+    return s;
+}
+
+struct GradRoom {
+    size_t post, pre, gate, total;
+};
+
+GradRoom grad_room(size_t d, const GradStrips& s)
+{
+    GradRoom r{};
+    const size_t part = (s.strips * d * 4 + 255) & ~size_t(255);
+    r.post = 0;
+    r.pre = part;
+    r.gate = 2 * part;
+    r.total = (s.per_gate > 1 ? 3 : 2) * part;
+    return r;
+}
+
+int check_shape(const char* what, size_t rows, size_t d, size_t gates, int dtype, double p, const uint64_t* step)
+{
+    if (!dtype_bytes(dtype))
+        return fail(GC_EINVAL, std::string(what) + ": unknown dtype");
+    if (d == 0)
+        return fail(GC_EINVAL, std::string(what) + ": a row must hold at least one value");
+    if (d > kMaxNormD || rows > (size_t(1) << 40))
+        return fail(GC_EUNSUPPORTED, std::string(what) + ": rows of more than 16384 values, or over 2^40 rows");
+    if (gates == 0 || gates > (size_t(1) << 31) || (rows && rows % gates))
+        return fail(GC_EINVAL, std::string(what) + ": the gate's rows must divide the rows");
+    if (!dropout_p_ok(p))
+        return fail(GC_EINVAL, std::string(what) + ": p must lie in [0, 1]");
+    if (!aligned_to(step, 8))
+        return fail(GC_EINVAL, std::string(what) + ": step must be 8-byte aligned");
+    return GC_OK;
+}
+
+NormArgs norm_args(size_t rows, size_t d, const float* post, const float* gate, size_t gates, const float* pre,
+                   float scale, float eps, double p, uint64_t seed, uint32_t worker, const uint64_t* step)
+{
+    NormArgs a{};
+    a.post = post;
+    a.gate = gate;
+    a.pre = pre;
+    a.rows = rows;
+    a.rows_per_gate = rows / gates;
+    a.d = uint32_t(d);
+    a.scale = scale;
+    a.eps = eps;
+    a.inv_d = float(1.0 / double(d));
+    a.drop = dropout_args(p, seed, worker, step);
+    return a;
+}
+
+}  // namespace
+}  // namespace gcq
+
+using namespace gcq;
+
+GCQ_API int norm_residual(const void* x, const void* y, int dtype, size_t rows, size_t d, const float* post_gain,
+                          const float* gate, size_t gates, const float* pre_gain, float residual_scale, float eps,
+                          double p, uint64_t seed, uint32_t worker, const uint64_t* step, void* z, void* h,
+                          float* rstd_post, float* rstd_pre, hipStream_t stream)
+{
+    clear_error();
+    if (int rc = check_shape("norm_residual", rows, d, gates, dtype, p, step))
+        return rc;
+    if (!(eps >= 0.0f))
+        return fail(GC_EINVAL, "norm_residual: eps must not be negative");
+    if (rows == 0)
+        return GC_OK;
+    const size_t b = dtype_bytes(dtype);
+    if (!x || !y || !z || (pre_gain && (!h || !rstd_pre)) || (post_gain && !rstd_post))
+        return fail(GC_EINVAL, "norm_residual: a buffer is NULL");
+    if (!aligned_to(x, b) || !aligned_to(y, b) || !aligned_to(z, b) || !aligned_to(h, b) || !aligned4(post_gain) ||
+        !aligned4(gate) || !aligned4(pre_gain) || !aligned4(rstd_post) || !aligned4(rstd_pre))
+        return fail(GC_EINVAL, "norm_residual: a buffer is misaligned");
+    const NormArgs a = norm_args(rows, d, post_gain, gate, gates, pre_gain, residual_scale, eps, p, seed, worker, step);
+    with_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        const bool aligned = d * b % 16 == 0 && aligned16(x) && aligned16(y) && aligned16(z) && aligned16(h);
+        with_team(ceil_div(d, kVec<T>), [&](auto team, auto vecs) {
+            constexpr int kTeam = decltype(team)::value, kVecs = decltype(vecs)::value;
+            constexpr int kWg = kTeam < 256 ? 256 : kTeam;
+            const size_t teams = std::min(rows, kForwardWaves / (kTeam / kWave));
+            const dim3 grid(unsigned(ceil_div(teams, kWg / kTeam)));
+            const auto launch = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, grid, dim3(kWg), 0, stream, static_cast<const T*>(x),
+                                   static_cast<const T*>(y), a, static_cast<T*>(z), static_cast<T*>(h), rstd_post,
+                                   rstd_pre, teams);
+            };
+            if (aligned)
+                launch(norm_residual_kernel<T, kTeam, kVecs, true>);
+            else
+                launch(norm_residual_kernel<T, kTeam, kVecs, false>);
+        });
+        return 0;
+    });
+    return check_launch("norm_residual");
+}
+
+GCQ_API int norm_residual_grad(const void* z, const void* y, int dtype, size_t rows, size_t d,
+                               const float* post_gain, const float* gate, size_t gates, const float* pre_gain,
+                               float residual_scale, double p, uint64_t seed, uint32_t worker, const uint64_t* step,
+                               const float* rstd_post, const float* rstd_pre, const void* dz, const void* dh, void* dx,
+                               void* dy, float* dpost_gain, float* dgate, float* dpre_gain, void* ws, size_t* ws_bytes,
+                               hipStream_t stream)
+{
+    clear_error();
+    if (int rc = check_shape("norm_residual_grad", rows, d, gates, dtype, p, step))
+        return rc;
+    if (!ws_bytes)
+        return fail(GC_EINVAL, "norm_residual_grad: ws_bytes is NULL");
+    const GradStrips s = rows ? grad_strips(rows, gates) : GradStrips{};
+    const GradRoom room = grad_room(d, s);
+    if (!ws) {
+        *ws_bytes = room.total;
+        return GC_OK;
+    }
+    const size_t b = dtype_bytes(dtype);
+    if ((dpost_gain && !post_gain) || (dgate && !gate) || (dpre_gain && !pre_gain))
+        return fail(GC_EINVAL, "norm_residual_grad: a gradient of a gain or gate that is NULL");
+    if (rows && (!z || !y || !dx || !dy || (!dz && !dh) || (pre_gain ? !dh || !rstd_pre : dh != nullptr) ||
+                 (post_gain && !rstd_post)))
+        return fail(GC_EINVAL, "norm_residual_grad: a buffer is NULL (or dh is given without pre_gain)");
+    if (!aligned_to(z, b) || !aligned_to(y, b) || !aligned_to(dz, b) || !aligned_to(dh, b) || !aligned_to(dx, b) ||
+        !aligned_to(dy, b) || !aligned4(post_gain) || !aligned4(gate) || !aligned4(pre_gain) ||
+        !aligned4(rstd_post) || !aligned4(rstd_pre) || !aligned4(dpost_gain) || !aligned4(dgate) ||
+        !aligned4(dpre_gain))
+        return fail(GC_EINVAL, "norm_residual_grad: a buffer is misaligned");
+    if (!aligned16(ws) || *ws_bytes < room.total)
+        return fail(GC_EINVAL, "norm_residual_grad: workspace too small or not 16-byte aligned");
+    char* w = static_cast<char*>(ws);
+    PartSum sums[3] = {};
+    int n = 0;
+    const auto add = [&](float* out, size_t off, size_t count, size_t out_rows) {
+        sums[n++] = PartSum{reinterpret_cast<const float*>(w + off), out, uint32_t(count), uint32_t(out_rows)};
+    };
+    if (dpost_gain)
+        add(dpost_gain, room.post, s.strips, 1);
+    if (dpre_gain)
+        add(dpre_gain, room.pre, s.strips, 1);
+    if (dgate && (rows == 0 || s.per_gate > 1))
+        add(dgate, room.gate, rows ? s.per_gate : 0, gates);
+    if (rows) {
+        const NormArgs a = norm_args(rows, d, post_gain, gate, gates, pre_gain, residual_scale, 0.0f, p, seed, worker,
+                                     step);
+        NormGradArgs g{};
+        g.rstd_post = rstd_post;
+        g.rstd_pre = rstd_pre;
+        g.part_post = dpost_gain ? reinterpret_cast<float*>(w + room.post) : nullptr;
+        g.part_pre = dpre_gain ? reinterpret_cast<float*>(w + room.pre) : nullptr;
+        g.gate_out = !dgate ? nullptr : s.per_gate > 1 ? reinterpret_cast<float*>(w + room.gate) : dgate;
+        g.strips = s.strips;
+        g.strips_per_gate = s.per_gate;
+        g.gates_per_strip = s.gates_per;
+        with_dtype(dtype, [&](auto t) {
+            using T = decltype(t);
+            const bool aligned = d * b % 16 == 0 && aligned16(z) && aligned16(y) && aligned16(dz) && aligned16(dh) &&
+                                 aligned16(dx) && aligned16(dy);
+            with_team(ceil_div(d, kVec<T>), [&](auto team, auto vecs) {
+                constexpr int kTeam = decltype(team)::value, kVecs = decltype(vecs)::value;
+                const auto launch = [&](auto kernel) {
+                    hipLaunchKernelGGL(kernel, dim3(unsigned(s.strips)), dim3(kTeam < 256 ? 256 : kTeam), 0, stream,
+                                       static_cast<const T*>(z), static_cast<const T*>(y), static_cast<const T*>(dz),
+                                       static_cast<const T*>(dh), a, g, static_cast<T*>(dx), static_cast<T*>(dy));
+                };
+                if (aligned)
+                    launch(norm_residual_grad_kernel<T, kTeam, kVecs, true>);
+                else
+                    launch(norm_residual_grad_kernel<T, kTeam, kVecs, false>);
+            });
+            return 0;
+        });
+        if (int rc = check_launch("norm_residual_grad"))
+            return rc;
+    }
+    uint32_t out_rows = 0;
+    for (const PartSum& p : sums)
+        out_rows += p.rows;
+    if (out_rows)
+        hipLaunchKernelGGL(sum_parts_kernel, dim3(unsigned(ceil_div(d, kSumCols)), std::min(out_rows, 65535u)),
+                           dim3(kSumCols * kSumRows), 0, stream, sums[0], sums[1], sums[2], uint32_t(d));
+    return check_launch("norm_residual_grad (sums)");
+}

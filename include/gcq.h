@@ -335,6 +335,51 @@ int dropout_backward(const void* grad_out, size_t n, int dtype, double p,
                      uint64_t seed, uint32_t worker, uint64_t offset,
                      const uint64_t* step, void* grad_in, hipStream_t stream);
 
+/* ---- the norms around a block, its gate and residual scale ------------------ */
+
+/* For each row of d values:
+ *   u = y * rstd(y) * post_gain     (post_gain NULL: u = y)
+ *   z = residual_scale * x + gate * drop(u)   (gate NULL: 1)
+ *   h = z * rstd(z) * pre_gain      (pre_gain NULL: no h)
+ *   rstd(v) = 1 / sqrt(mean(v^2) + eps)
+ * with the mask of dropout() at offset 0 over the rows x d values (p = 0: no
+ * dropout). Everything between is fp32; h is that of the z before its
+ * rounding.
+ *   x, y, z, h  [rows, d] of `dtype`, rows contiguous; z may be x or y, h
+ *               may be the other one
+ *   post_gain, pre_gain  [d] fp32, or NULL
+ *   gate        [gates, d] fp32, or NULL; `gates` divides rows, and row r
+ *               takes gate row r / (rows / gates)
+ *   rstd_post, rstd_pre  [rows] fp32 out, for the gradient; needed where the
+ *               gain is given
+ *   d 1 .. 16384, eps >= 0, p 0 .. 1; seed, worker, step as in dropout() */
+int norm_residual(const void* x, const void* y, int dtype, size_t rows, size_t d,
+                  const float* post_gain, const float* gate, size_t gates,
+                  const float* pre_gain, float residual_scale, float eps, double p,
+                  uint64_t seed, uint32_t worker, const uint64_t* step, void* z,
+                  void* h, float* rstd_post, float* rstd_pre, hipStream_t stream);
+
+/* The gradient of norm_residual: dz, dh are those of z (what reaches it other
+ * than through h) and h.
+ *   z, y        the outputs z and inputs y of the forward call; the rest of
+ *               its arguments and its rstd_post, rstd_pre
+ *   dz, dh      [rows, d] of `dtype`. dh is needed with pre_gain and not
+ *               allowed without it; dz may be NULL (zero) where dh is given
+ *   dx, dy      [rows, d] of `dtype` out; each may be dz, dh, z or y itself
+ *   dpost_gain, dpre_gain  [d], dgate [gates, d] fp32 out, or NULL: not
+ *               computed. fp32 sums over the rows in a fixed order.
+ *   ws          16-byte-aligned workspace; ws == NULL: *ws_bytes = its size
+ *               for (rows, d, gates), else *ws_bytes must be at least that.
+ * rows may be 0: the gains' gradients are then zero. */
+int norm_residual_grad(const void* z, const void* y, int dtype, size_t rows, size_t d,
+                       const float* post_gain, const float* gate, size_t gates,
+                       const float* pre_gain, float residual_scale, double p,
+                       uint64_t seed, uint32_t worker, const uint64_t* step,
+                       const float* rstd_post, const float* rstd_pre, const void* dz,
+                       const void* dh, void* dx, void* dy, float* dpost_gain,
+                       float* dgate, float* dpre_gain, void* ws, size_t* ws_bytes,
+                       hipStream_t stream);
+
 /* ---- softmax cross entropy of a linear layer over a large vocabulary ------- */
 
 /* For tokens n < N, with logits l_nv = <hidden[n], weight[v]> over v < V:
