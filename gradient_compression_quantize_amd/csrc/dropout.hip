@@ -40,7 +40,7 @@ __global__ __launch_bounds__(kThreads) void dropout_vec_kernel(const T* x, const
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const size_t c = c0 + u * kThreads;
-                if (a.threshold) {
+                if (a.some) {
 #pragma unroll
                     for (int s = 0; s < V / 4; ++s) {
                         const U4 w = dropout_words(a, key, offset4 + c * (V / 4) + s);
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(kThreads) void dropout_vec_kernel(const T* x, const
             // the last tile, a value at a time
             for (size_t i = tile * (kThreads * kUnroll * V) + threadIdx.x; i < n; i += kThreads) {
                 float v = float(x[i]);
-                if (a.threshold)
+                if (a.some)
                     v = dropout_apply(a, dropout_word(a, key, offset4 * 4 + i), v);
                 if (kResidual)
                     v += float(residual[i]);
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(kThreads) void dropout_slot_kernel(const T* x, cons
     const size_t nslots = (n + head + 3) >> 2;
     for (size_t q = size_t(blockIdx.x) * kThreads + threadIdx.x; q < nslots;
          q += size_t(gridDim.x) * kThreads) {
-        const U4 w = a.threshold ? dropout_words(a, key, (offset >> 2) + q) : U4{0, 0, 0, 0};
+        const U4 w = a.some ? dropout_words(a, key, (offset >> 2) + q) : U4{0, 0, 0, 0};
         const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kThreads) void dropout_slot_kernel(const T* x, cons
             if (j >= head && j - head < n) {
                 const size_t i = j - head;
                 float v = float(x[i]);
-                if (a.threshold)
+                if (a.some)
                     v = dropout_apply(a, words[k], v);
                 if (kResidual)
                     v += float(residual[i]);

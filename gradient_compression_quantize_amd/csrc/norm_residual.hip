@@ -28,6 +28,11 @@ namespace {
 
 constexpr size_t kMaxNormD = 16384;
 
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
 struct NormArgs {
     const float *post, *gate, *pre;  // NULL: 1 and no norm, 1, no h
     size_t rows, rows_per_gate;
@@ -39,7 +44,8 @@ struct NormArgs {
 // ---- a row in the registers of a team -----------------------------------------
 
 // Vector v of team lane t is v * kTeam + t; kAligned: every row starts on 16
-// bytes (otherwise the loads and stores are aligned to the element alone).
+// bytes and holds whole vectors (otherwise the loads and stores are aligned
+// to the element alone, and a row's last values go one at a time).
 template <typename T, int kTeam, int kVecs, bool kAligned>
 struct Row {
     static constexpr int V = kVec<T>;
@@ -53,11 +59,10 @@ struct Row {
 
     static __device__ __forceinline__ Raw load_raw(const T* row, uint32_t c, uint32_t d)
     {
-        if (c + V <= d) {
-            if (kAligned)
-                return *reinterpret_cast<const Raw*>(row + c);
+        if (kAligned)
+            return c < d ? *reinterpret_cast<const Raw*>(row + c) : Raw{};
+        if (c + V <= d)
             return *reinterpret_cast<const RawAny*>(row + c);
-        }
         Raw r = {};
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -78,17 +83,31 @@ struct Row {
     static __device__ __forceinline__ void store(T* row, uint32_t c, uint32_t d, F x)
     {
         const Raw r = __builtin_convertvector(x, Raw);
-        if (c + V <= d) {
-            if (kAligned)
+        if (kAligned) {
+            if (c < d)
                 *reinterpret_cast<Raw*>(row + c) = r;
-            else
-                *reinterpret_cast<RawAny*>(row + c) = r;
+            return;
+        }
+        if (c + V <= d) {
+            *reinterpret_cast<RawAny*>(row + c) = r;
             return;
         }
 #pragma unroll
         for (int e = 0; e < V; ++e)
             if (c + e < d)
                 row[c + e] = r[e];
+    }
+
+    // x where bit e of `bits` is set, else 0 (whatever x holds).
+    static __device__ __forceinline__ float keep(uint32_t bits, int e, float x)
+    {
+        return u2f(f2u(x) & uint32_t(int32_t(bits << (31 - e)) >> 31));
+    }
+
+    // Which team of the workgroup this is, for every lane of a wave the same.
+    static __device__ __forceinline__ int team()
+    {
+        return kTeams == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kTeam);
     }
 
     // fp32 values of columns: 1 where there is no array.
@@ -101,11 +120,11 @@ struct Row {
         return f;
     }
 
-    // 0 or 1 / (1 - p) for the values i .. i + V - 1 of the mask; i mod 4 is
-    // the same for a whole row.
-    static __device__ __forceinline__ F mask(const DropoutArgs& a, uint64_t key, uint64_t i)
+    // Whether the values i .. i + V - 1 of the mask are kept, a bit each; i mod
+    // 4 is the same for a whole row.
+    static __device__ __forceinline__ uint32_t mask(const DropoutArgs& a, uint64_t key, uint64_t i)
     {
-        const uint32_t phase = __builtin_amdgcn_readfirstlane(uint32_t(i) & 3);
+        const uint32_t phase = kAligned ? 0 : __builtin_amdgcn_readfirstlane(uint32_t(i) & 3);
         uint32_t w[V + 4];
 #pragma unroll
         for (int s = 0; s < V / 4; ++s) {
@@ -124,13 +143,28 @@ struct Row {
             for (int e = 0; e < V; ++e)
                 w[e] = phase == 1 ? w[e + 1] : phase == 2 ? w[e + 2] : w[e + 3];
         }
-        F f;
+        uint32_t bits = 0;
 #pragma unroll
         for (int e = 0; e < V; ++e)
-            f[e] = dropout_keeps(a, w[e]) ? a.scale : 0.0f;
-        return f;
+            bits |= w[e] >= a.cut ? 1u << e : 0u;
+        return bits;
     }
 };
+
+// Sum over a wave, in every lane: four DPP steps within each row of 16 lanes
+// (quad_perm xor 1 and xor 2, row_half_mirror, row_mirror), then the rows.
+__device__ __forceinline__ float wave_sum(float x)
+{
+    const auto step = [](float v, auto ctrl) {
+        return v + u2f(uint32_t(__builtin_amdgcn_update_dpp(0, int(f2u(v)), decltype(ctrl)::value, 0xF, 0xF, true)));
+    };
+    x = step(x, Int<0xB1>());
+    x = step(x, Int<0x4E>());
+    x = step(x, Int<0x141>());
+    x = step(x, Int<0x140>());
+    const auto row = [x](int lane) { return u2f(uint32_t(__builtin_amdgcn_readlane(int(f2u(x)), lane))); };
+    return (row(0) + row(16)) + (row(32) + row(48));
+}
 
 // Sums over a team; every lane gets them. Teams of several waves are whole
 // workgroups and exchange through LDS, alternating between two halves so that
@@ -143,9 +177,7 @@ struct TeamSum {
     {
 #pragma unroll
         for (int k = 0; k < kCount; ++k)
-#pragma unroll
-            for (int off = kWave / 2; off > 0; off >>= 1)
-                x[k] += __shfl_xor(x[k], off);
+            x[k] = wave_sum(x[k]);
         if (kWaves == 1)
             return;
         float* at = lds + half * (kWaves * kCount);
@@ -169,9 +201,9 @@ struct TeamSum {
 // ---- forward --------------------------------------------------------------------
 //
 // Outputs may be the inputs' own buffers: a thread writes only the values that
-// it alone has read before.
+// it alone has read before. kAll: every optional argument is there.
 
-template <typename T, int kTeam, int kVecs, bool kAligned>
+template <typename T, int kTeam, int kVecs, bool kAligned, bool kAll>
 __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_kernel(
     const T* x, const T* y, NormArgs a, T* z, T* h, float* rstd_post, float* rstd_pre, size_t teams)
 {
@@ -179,8 +211,9 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_kerne
     using F = typename R::F;
     __shared__ float lds[2 * (kTeam / kWave)];
     int half = 0;
+    const bool has_post = kAll || a.post, has_pre = kAll || a.pre;
     const int t = threadIdx.x % kTeam;
-    const size_t team = size_t(blockIdx.x) * R::kTeams + threadIdx.x / kTeam;
+    const size_t team = size_t(blockIdx.x) * R::kTeams + R::team();
     if (team >= teams)
         return;  // only teams of one wave share a workgroup
     const size_t lo = a.rows * team / teams, hi = a.rows * (team + 1) / teams;
@@ -216,13 +249,13 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_kerne
             R::load(ry, y, row + 1, a.d, t);
         }
         float rp = 1.0f;
-        if (a.post) {
+        if (has_post) {
             float s[1] = {0.0f};
 #pragma unroll
             for (int v = 0; v < kVecs; ++v)
 #pragma unroll
                 for (int e = 0; e < R::V; ++e)
-                    s[0] += fy[v][e] * fy[v][e];
+                    s[0] = __builtin_fmaf(fy[v][e], fy[v][e], s[0]);
             TeamSum<kTeam, 1>::run(s, lds, half);
             rp = 1.0f / sqrtf(s[0] * a.inv_d + a.eps);
             if (t == 0)
@@ -233,19 +266,20 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_kerne
         for (int v = 0; v < kVecs; ++v) {
             const uint32_t c = R::col(v, t);
             F b = fy[v] * rp * w[v];
-            if (a.drop.threshold) {
-                const F m = R::mask(a.drop, key, uint64_t(row) * a.d + c);
+            if (a.drop.some) {
+                const uint32_t kept = R::mask(a.drop, key, uint64_t(row) * a.d + c);
 #pragma unroll
                 for (int e = 0; e < R::V; ++e)  // 0 where dropped, whatever y holds
-                    b[e] = m[e] == 0.0f ? 0.0f : b[e] * m[e];
+                    b[e] = R::keep(kept, e, b[e] * a.drop.scale);
             }
-            fx[v] = fx[v] * a.scale + b;
 #pragma unroll
-            for (int e = 0; e < R::V; ++e)
-                s[0] += fx[v][e] * fx[v][e];
+            for (int e = 0; e < R::V; ++e) {
+                fx[v][e] = __builtin_fmaf(fx[v][e], a.scale, b[e]);
+                s[0] = __builtin_fmaf(fx[v][e], fx[v][e], s[0]);
+            }
             R::store(z + row * a.d, c, a.d, fx[v]);
         }
-        if (a.pre) {
+        if (has_pre) {
             TeamSum<kTeam, 1>::run(s, lds, half);
             const float rz = 1.0f / sqrtf(s[0] * a.inv_d + a.eps);
             if (t == 0)
@@ -270,8 +304,8 @@ struct NormGradArgs {
 
 // One workgroup for each strip of rows; its teams take the rows in turn. The
 // rows of a strip share a gate, or the strip holds whole gates.
-template <typename T, int kTeam, int kVecs, bool kAligned>
-__global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_grad_kernel(
+template <typename T, int kTeam, int kVecs, bool kAligned, bool kAll>
+__global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam, kTeam < 1024 ? 2 : 4) void norm_residual_grad_kernel(
     const T* z, const T* y, const T* dz, const T* dh, NormArgs a, NormGradArgs g, T* dx, T* dy)
 {
     using R = Row<T, kTeam, kVecs, kAligned>;
@@ -280,20 +314,20 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_grad_
     constexpr int kLds = R::kTeams > 1 ? (R::kTeams - 1) * kTeam * kVecs * R::V : 2 * 3 * (kTeam / kWave);
     __shared__ float lds[kLds];
     int half = 0;
-    const int t = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
+    const bool has_post = kAll || a.post, has_pre = kAll || a.pre, has_dz = kAll || dz;
+    const int t = threadIdx.x % kTeam, team = R::team();
     const uint64_t key = dropout_key(a.drop);
+    const float factor = a.drop.some ? a.drop.scale : 1.0f;
     const size_t strip = blockIdx.x;
     const size_t gates = a.rows / a.rows_per_gate;
     // gates [g_lo, g_hi) of this strip, and its rows of the first one
     const size_t g_lo = g.strips_per_gate > 1 ? strip / g.strips_per_gate : strip * g.gates_per_strip;
     const size_t g_hi = g.strips_per_gate > 1 ? g_lo + 1 : std::min(g_lo + g.gates_per_strip, gates);
 
-    F post[kVecs], pre[kVecs], sum_post[kVecs], sum_pre[kVecs];
+    F pre[kVecs], sum_pre[kVecs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-        post[v] = R::columns(a.post, R::col(v, t), a.d);
         pre[v] = R::columns(a.pre, R::col(v, t), a.d);
-        sum_post[v] = F{};
         sum_pre[v] = F{};
     }
     // teams of one wave: sums over the workgroup's teams end in team 0
@@ -318,7 +352,9 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_grad_
                         s[v][e] += lds[((o * kVecs + v) * R::V + e) * kTeam + t];
         }
     };
-    const auto write = [&](float* p, const F (&s)[kVecs]) {
+    // s times r and the columns of f (1 for NULL), onto what this thread wrote there
+    // before if `more`
+    const auto write = [&](float* p, const F (&s)[kVecs], float r, const float* f, bool more) {
         if (R::kTeams > 1 && team > 0)
             return;
 #pragma unroll
@@ -327,7 +363,7 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_grad_
             for (int e = 0; e < R::V; ++e) {
                 const uint32_t c = R::col(v, t) + e;
                 if (c < a.d)
-                    p[c] = s[v][e];
+                    p[c] = __builtin_fmaf(s[v][e] * r, f ? f[c] : 1.0f, more ? p[c] : 0.0f);
             }
     };
 
@@ -338,74 +374,103 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_grad_
             hi = lo + n * (s + 1) / g.strips_per_gate;
             lo = lo + n * s / g.strips_per_gate;
         }
-        F fg[kVecs], sum_gate[kVecs];
+        // the gate, the post gain and 1 / (1 - p) enter as one factor w; with
+        // A = sum of t kept yhat over the rows of a gate, dgate = A post / (1 -
+        // p), and dpost is the sum of A gate / (1 - p) over the gates
+        F w[kVecs], sum[kVecs];
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
-            fg[v] = R::columns(a.gate ? a.gate + gate * a.d : nullptr, R::col(v, t), a.d);
-            sum_gate[v] = F{};
+            const uint32_t c = R::col(v, t);
+            w[v] = R::columns(a.gate ? a.gate + gate * a.d : nullptr, c, a.d) * R::columns(a.post, c, a.d) * factor;
+            sum[v] = F{};
         }
+        typename R::Raw next_y[kVecs], next_dz[kVecs], next_z[kVecs], next_dh[kVecs];
+        float next_rz = 0.0f, next_ry = 1.0f;
+        const auto fetch = [&](size_t row) {
+            R::load(next_y, y, row, a.d, t);
+            if (has_dz)
+                R::load(next_dz, dz, row, a.d, t);
+            if (has_pre) {
+                R::load(next_z, z, row, a.d, t);
+                R::load(next_dh, dh, row, a.d, t);
+                next_rz = g.rstd_pre[row];
+            }
+            if (has_post)
+                next_ry = g.rstd_post[row];
+        };
+        // the next row's loads run under this row's arithmetic, where the
+        // registers hold both (a workgroup of 1024 threads has 128 a lane)
+        constexpr bool kAhead = kTeam < 1024;
+        if (kAhead && lo + team < hi)
+            fetch(lo + team);
         for (size_t row = lo + team; row < hi; row += R::kTeams) {
-            const float rz = a.pre ? g.rstd_pre[row] : 0.0f, ry = a.post ? g.rstd_post[row] : 1.0f;
-            F zn[kVecs], yn[kVecs], e[kVecs], m[kVecs];
+            if (!kAhead)
+                fetch(row);
+            const float rz = next_rz, ry = next_ry;
+            F zn[kVecs], yn[kVecs], e[kVecs], p[kVecs];
+            uint32_t kept[kVecs];
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                yn[v] = R::wide(next_y[v]);
+                e[v] = has_dz ? R::wide(next_dz[v]) : F{};
+                zn[v] = has_pre ? R::wide(next_z[v]) : F{};
+                p[v] = has_pre ? R::wide(next_dh[v]) : F{};
+            }
+            if (kAhead && row + R::kTeams < hi)
+                fetch(row + R::kTeams);
             float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) {
                 const uint32_t c = R::col(v, t);
-                yn[v] = R::wide(R::load_raw(y + row * a.d, c, a.d)) * ry;
-                e[v] = dz ? R::wide(R::load_raw(dz + row * a.d, c, a.d)) : F{};
-                m[v] = F{} + 1.0f;
-                if (a.drop.threshold) {
-                    m[v] = R::mask(a.drop, key, uint64_t(row) * a.d + c);
+                yn[v] *= ry;
+                kept[v] = ~0u;
+                if (a.drop.some) {
+                    kept[v] = R::mask(a.drop, key, uint64_t(row) * a.d + c);
+                    if (!has_post) {  // a dropped y takes no part, whatever it holds
 #pragma unroll
-                    for (int k = 0; k < R::V; ++k)  // a dropped y takes no part, whatever it holds
-                        yn[v][k] = m[v][k] == 0.0f && !a.post ? 0.0f : yn[v][k];
-                }
-                if (a.pre) {
-                    zn[v] = R::wide(R::load_raw(z + row * a.d, c, a.d)) * rz;
-                    const F h = R::wide(R::load_raw(dh + row * a.d, c, a.d));
-                    sum_pre[v] += h * zn[v];
-                    const F p = h * pre[v], q = fg[v] * m[v] * post[v] * yn[v];
-                    e[v] += p * rz;
-#pragma unroll
-                    for (int k = 0; k < R::V; ++k) {
-                        s[0] += p[k] * zn[v][k];
-                        s[1] += q[k] * e[v][k];
-                        s[2] += q[k] * zn[v][k];
+                        for (int k = 0; k < R::V; ++k)
+                            yn[v][k] = R::keep(kept[v], k, yn[v][k]);
                     }
-                } else {
-                    zn[v] = F{};
-                    const F q = fg[v] * m[v] * post[v] * yn[v];
+                }
+                zn[v] *= rz;
 #pragma unroll
-                    for (int k = 0; k < R::V; ++k)
-                        s[1] += q[k] * e[v][k];
+                for (int k = 0; k < R::V; ++k) {
+                    sum_pre[v][k] = __builtin_fmaf(p[v][k], zn[v][k], sum_pre[v][k]);
+                    const float gp = p[v][k] * pre[v][k];
+                    const float q = w[v][k] * R::keep(kept[v], k, yn[v][k]);
+                    e[v][k] = __builtin_fmaf(gp, rz, e[v][k]);
+                    s[0] = __builtin_fmaf(gp, zn[v][k], s[0]);
+                    s[1] = __builtin_fmaf(q, e[v][k], s[1]);
+                    s[2] = __builtin_fmaf(q, zn[v][k], s[2]);
                 }
             }
             TeamSum<kTeam, 3>::run(s, lds, half);
             const float c1 = rz * (s[0] * a.inv_d);
-            const float c2 = a.post ? (s[1] - c1 * s[2]) * a.inv_d : 0.0f;
+            const float c2 = has_post ? ry * ((s[1] - c1 * s[2]) * a.inv_d) : 0.0f;
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) {
                 const uint32_t c = R::col(v, t);
-                const F whole = e[v] - zn[v] * c1;
-                R::store(dx + row * a.d, c, a.d, whole * a.scale);
-                const F wm = whole * m[v], wy = wm * yn[v];
-                sum_gate[v] += wy * post[v];
-                sum_post[v] += wy * fg[v];
-                R::store(dy + row * a.d, c, a.d, (wm * fg[v] * post[v] - yn[v] * c2) * ry);
+                F out;
+#pragma unroll
+                for (int k = 0; k < R::V; ++k) {
+                    e[v][k] = __builtin_fmaf(-c1, zn[v][k], e[v][k]);
+                    const float wm = R::keep(kept[v], k, e[v][k]);
+                    sum[v][k] = __builtin_fmaf(wm, yn[v][k], sum[v][k]);
+                    out[k] = __builtin_fmaf(-c2, yn[v][k], wm * w[v][k] * ry);
+                }
+                R::store(dx + row * a.d, c, a.d, e[v] * a.scale);
+                R::store(dy + row * a.d, c, a.d, out);
             }
         }
-        if (g.gate_out) {
-            over_teams(sum_gate);
-            write(g.gate_out + (g.strips_per_gate > 1 ? strip : gate) * a.d, sum_gate);
-        }
-    }
-    if (g.part_post) {
-        over_teams(sum_post);
-        write(g.part_post + strip * a.d, sum_post);
+        over_teams(sum);
+        if (g.part_post)
+            write(g.part_post + strip * a.d, sum, factor, a.gate ? a.gate + gate * a.d : nullptr, gate > g_lo);
+        if (g.gate_out)
+            write(g.gate_out + (g.strips_per_gate > 1 ? strip : gate) * a.d, sum, factor, a.post, false);
     }
     if (g.part_pre) {
         over_teams(sum_pre);
-        write(g.part_pre + strip * a.d, sum_pre);
+        write(g.part_pre + strip * a.d, sum_pre, 1.0f, nullptr, false);
     }
 }
 
@@ -452,38 +517,36 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void sum_parts_kernel(PartSum a
 
 // ---- host side --------------------------------------------------------------------
 
-// Calls f(team, vecs) with the smallest team that holds a row of `vecs`
-// vectors, as integral constants.
-template <int N>
-struct Int {
-    static constexpr int value = N;
-};
-
-template <typename F>
-void with_team(size_t vecs, F f)
+// Calls f(team, vecs), as integral constants, with the smallest team that
+// holds a row of d values.
+template <typename T, typename F>
+void with_team(size_t d, F f)
 {
+    // at most 16 values a lane
+    constexpr int M = 16 / kVec<T>;
+    const size_t vecs = ceil_div(d, kVec<T>);
     if (vecs <= 64)
         f(Int<64>(), Int<1>());
     else if (vecs <= 128)
         f(Int<64>(), Int<2>());
-    else if (vecs <= 256)
-        f(Int<256>(), Int<1>());
-    else if (vecs <= 512)
-        f(Int<256>(), Int<2>());
-    else if (vecs <= 1024)
-        f(Int<512>(), Int<2>());
-    else if (vecs <= 2048)
-        f(Int<1024>(), Int<2>());
+    else if (vecs <= 64 * M)
+        f(Int<64>(), Int<M>());
+    else if (vecs <= 128 * M)
+        f(Int<256>(), Int<M / 2>());
+    else if (vecs <= 256 * M)
+        f(Int<256>(), Int<M>());
+    else if (vecs <= 512 * M)
+        f(Int<512>(), Int<M>());
     else
-        f(Int<1024>(), Int<4>());
+        f(Int<1024>(), Int<M>());
 }
 
 // Teams of one launch: waves for a few rounds of every compute unit.
-constexpr size_t kForwardWaves = 256 * 16;
+constexpr size_t kForwardWaves = 256 * 8;
 
 // Strips of the backward launch, each of which leaves a partial row: two
 // workgroups a compute unit.
-constexpr size_t kGradStrips = 512;
+constexpr size_t kGradStrips = 256;
 
 struct GradStrips {
     size_t strips, per_gate, gates_per;
@@ -582,7 +645,7 @@ GCQ_API int norm_residual(const void* x, const void* y, int dtype, size_t rows, 
     with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const bool aligned = d * b % 16 == 0 && aligned16(x) && aligned16(y) && aligned16(z) && aligned16(h);
-        with_team(ceil_div(d, kVec<T>), [&](auto team, auto vecs) {
+        with_team<T>(d, [&](auto team, auto vecs) {
             constexpr int kTeam = decltype(team)::value, kVecs = decltype(vecs)::value;
             constexpr int kWg = kTeam < 256 ? 256 : kTeam;
             const size_t teams = std::min(rows, kForwardWaves / (kTeam / kWave));
@@ -592,10 +655,12 @@ GCQ_API int norm_residual(const void* x, const void* y, int dtype, size_t rows, 
                                    static_cast<const T*>(y), a, static_cast<T*>(z), static_cast<T*>(h), rstd_post,
                                    rstd_pre, teams);
             };
-            if (aligned)
-                launch(norm_residual_kernel<T, kTeam, kVecs, true>);
+            if (aligned && post_gain && pre_gain)
+                launch(norm_residual_kernel<T, kTeam, kVecs, true, true>);
+            else if (aligned)
+                launch(norm_residual_kernel<T, kTeam, kVecs, true, false>);
             else
-                launch(norm_residual_kernel<T, kTeam, kVecs, false>);
+                launch(norm_residual_kernel<T, kTeam, kVecs, false, false>);
         });
         return 0;
     });
@@ -661,17 +726,19 @@ GCQ_API int norm_residual_grad(const void* z, const void* y, int dtype, size_t r
             using T = decltype(t);
             const bool aligned = d * b % 16 == 0 && aligned16(z) && aligned16(y) && aligned16(dz) && aligned16(dh) &&
                                  aligned16(dx) && aligned16(dy);
-            with_team(ceil_div(d, kVec<T>), [&](auto team, auto vecs) {
+            with_team<T>(d, [&](auto team, auto vecs) {
                 constexpr int kTeam = decltype(team)::value, kVecs = decltype(vecs)::value;
                 const auto launch = [&](auto kernel) {
                     hipLaunchKernelGGL(kernel, dim3(unsigned(s.strips)), dim3(kTeam < 256 ? 256 : kTeam), 0, stream,
                                        static_cast<const T*>(z), static_cast<const T*>(y), static_cast<const T*>(dz),
                                        static_cast<const T*>(dh), a, g, static_cast<T*>(dx), static_cast<T*>(dy));
                 };
-                if (aligned)
-                    launch(norm_residual_grad_kernel<T, kTeam, kVecs, true>);
+                if (aligned && post_gain && pre_gain && dz)
+                    launch(norm_residual_grad_kernel<T, kTeam, kVecs, true, true>);
+                else if (aligned)
+                    launch(norm_residual_grad_kernel<T, kTeam, kVecs, true, false>);
                 else
-                    launch(norm_residual_grad_kernel<T, kTeam, kVecs, false>);
+                    launch(norm_residual_grad_kernel<T, kTeam, kVecs, false, false>);
             });
             return 0;
         });
