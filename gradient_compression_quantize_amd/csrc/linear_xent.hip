@@ -128,11 +128,11 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
 {
     using L = LogitTile<TA, TB, WA, WB>;
     using P = typename L::Product;
-    __shared__ bf16_t la0[TA * kStageK], la1[TA * kStageK], lb0[TB * kStageK], lb1[TB * kStageK];
+    GCQ_TILE_BUFFERS(lds, TA, TB);
     uint32_t ta, tb;
     tile_of(xcd_contiguous(blockIdx.x, gridDim.x), sh.tiles_a, sh.tiles_b, ta, tb);
     typename P::Acc acc;
-    P::run(weight, hidden, sh, ta * TA, tb * TB, 0, sh.stages * sh.segments, la0, la1, lb0, lb1, acc);
+    P::run(weight, hidden, sh, ta * TA, tb * TB, 0, sh.turns * sh.segments, lds, acc);
 
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -232,11 +232,11 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
 {
     using L = LogitTile<TA, TB, WA, WB>;
     using P = typename L::Product;
-    __shared__ bf16_t la0[TA * kStageK], la1[TA * kStageK], lb0[TB * kStageK], lb1[TB * kStageK];
+    GCQ_TILE_BUFFERS(lds, TA, TB);
     uint32_t ta, tb;
     tile_of(xcd_contiguous(blockIdx.x, gridDim.x), sh.tiles_a, sh.tiles_b, ta, tb);
     typename P::Acc acc;
-    P::run(weight, hidden, sh, ta * TA, tb * TB, 0, sh.stages * sh.segments, la0, la1, lb0, lb1, acc);
+    P::run(weight, hidden, sh, ta * TA, tb * TB, 0, sh.turns * sh.segments, lds, acc);
 
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -244,10 +244,12 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
     const uint32_t a_wave = ta * TA + wa * L::kRowsA, b_wave = tb * TB + wb * L::kRowsB;
 
     // this wave's part of the staging buffers: kRowsB tokens x kRowsA values
-    constexpr int kPart = L::kRowsA * L::kRowsB, kPerBuffer = TA * kStageK / kPart;
-    static_assert(TA == TB || P::kWaves <= 2 * kPerBuffer, "the parts fit the buffers");
-    const int at = wave / kPerBuffer;
-    bf16_t* part = (at == 0 ? la0 : at == 1 ? la1 : at == 2 ? lb0 : lb1) + (wave % kPerBuffer) * kPart;
+    constexpr int kPart = L::kRowsA * L::kRowsB;
+    static_assert(TA == TB && P::kWaves == 2 * kBuffers && kPart <= TA * kStageK, "a buffer for each wave");
+    bf16_t* part = lds.a[0];
+#pragma unroll
+    for (int k = 1; k < 2 * kBuffers; ++k)
+        part = wave == k ? (k < kBuffers ? lds.a[k] : lds.b[k - kBuffers]) : part;
     constexpr int kChunks = L::kRowsA / 8;
 
 #pragma unroll
@@ -326,15 +328,15 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void product_kernel(MatOperand A,
                                                                   ProductShape sh, ProductOut<T> out)
 {
     using P = TileProduct<true, kBK, TA, TB, WA, WB>;
-    __shared__ bf16_t la0[TA * kStageK], la1[TA * kStageK], lb0[TB * kStageK], lb1[TB * kStageK];
+    GCQ_TILE_BUFFERS(lds, TA, TB);
     const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x);
     const uint32_t tiles = sh.tiles_a * sh.tiles_b, split = id / tiles;
     uint32_t ta, tb;
     tile_of(id - split * tiles, sh.tiles_a, sh.tiles_b, ta, tb);
-    const uint64_t all = uint64_t(sh.stages) * sh.segments;
+    const uint64_t all = uint64_t(sh.turns) * sh.segments;
     typename P::Acc acc;
     P::run(A, B, sh, ta * TA, tb * TB, uint32_t(all * split / sh.splits),
-           uint32_t(all * (split + 1) / sh.splits), la0, la1, lb0, lb1, acc);
+           uint32_t(all * (split + 1) / sh.splits), lds, acc);
 
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -434,10 +436,10 @@ int check_sizes(const char* what, size_t N, size_t V, size_t D, int dtype)
 }
 
 // Whether the product can read the matrix where it is: exact in bf16, rows
-// aligned for 16-byte loads, whole stages.
+// aligned for 16-byte loads, whole turns.
 bool direct_ok(const void* p, size_t D, int dtype)
 {
-    return dtype == GC_BF16 && D % kStageK == 0 && aligned16(p);
+    return dtype == GC_BF16 && D % kTurnK == 0 && aligned16(p);
 }
 
 // bf16 planes that hold a value of the type exactly (fp32 to 2^-24).
@@ -454,7 +456,7 @@ PlaneRoom plane_room(Carver& c, size_t rows, size_t D, int dtype)
 {
     PlaneRoom r{};
     r.rows = rows;
-    r.d = round_up(D, kStageK);
+    r.d = round_up(D, kTurnK);
     r.planes = planes_of(dtype);
     r.off = c.take(r.planes * rows * r.d * 2);
     return r;
@@ -549,11 +551,11 @@ struct GradLayout {
     uint32_t h_splits, w_splits;
 };
 
-// Splits of a product of `tiles` tiles over `stages` stages: enough to give
-// every compute unit a tile, at least 8 stages each.
-uint32_t splits_for(size_t tiles, size_t stages)
+// Splits of a product of `tiles` tiles over `turns` turns: enough to give
+// every compute unit a tile, at least 4 turns each.
+uint32_t splits_for(size_t tiles, size_t turns)
 {
-    return uint32_t(std::max<size_t>(1, std::min(kCus / std::max<size_t>(tiles, 1), stages / 8)));
+    return uint32_t(std::max<size_t>(1, std::min(kCus / std::max<size_t>(tiles, 1), turns / 4)));
 }
 
 ProductShape grad_shape(int planes_a, int out_dtype)
@@ -568,7 +570,7 @@ GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, in
     GradLayout L{};
     Carver c;
     L.weight = plane_room(c, V, D, dtype);
-    L.n_pad = round_up(N, kStageK);
+    L.n_pad = round_up(N, kTurnK);
     L.hidden = plane_room(c, L.n_pad, D, dtype);
     L.d4 = round_up(D, 4);
     L.g_planes = std::max(g_planes(dh_dtype), g_planes(dw_dtype));
@@ -578,8 +580,8 @@ GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, in
     L.g = c.take(L.g_planes * L.n_pad * L.piece * 2);
     const size_t ta = ceil_div(D, kTile);
     L.h_splits = splits_for(ceil_div(N, kTile) * ta,
-                            L.piece / kStageK * grad_shape(L.weight.planes, dh_dtype).segments);
-    L.w_splits = splits_for(L.piece / kTile * ta, L.n_pad / kStageK * grad_shape(L.hidden.planes, dw_dtype).segments);
+                            L.piece / kTurnK * grad_shape(L.weight.planes, dh_dtype).segments);
+    L.w_splits = splits_for(L.piece / kTile * ta, L.n_pad / kTurnK * grad_shape(L.hidden.planes, dw_dtype).segments);
     L.h_slab = c.take(L.h_splits > 1 || L.pieces > 1 ? L.h_splits * N * L.d4 * 4 : 0);
     L.w_slab = c.take(L.w_splits > 1 ? L.w_splits * L.piece * L.d4 * 4 : 0);
     L.total = c.used;
@@ -670,7 +672,7 @@ GCQ_API int linear_xent_loss(const void* hidden, const void* weight, int dtype, 
     const MatOperand ho = make_operand(hidden, N, D, dtype, L.hidden, w, !direct_ok(hidden, D, dtype), nullptr,
                                        0, 0, stream);
     ProductShape sh{};
-    sh.stages = uint32_t(round_up(D, kStageK) / kStageK);
+    sh.turns = uint32_t(round_up(D, kTurnK) / kTurnK);
     set_pairs(sh, L.weight.planes, L.hidden.planes, kFullLimit);
     sh.tiles_a = uint32_t(ceil_div(V, L.cfg.ta));
     sh.tiles_b = uint32_t(ceil_div(N, L.cfg.tb));
@@ -744,7 +746,7 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
         wp.plane0 += v0 * wo.ld;
         wp.extent = uint32_t(vp);
         ProductShape sh{};
-        sh.stages = uint32_t(round_up(D, kStageK) / kStageK);
+        sh.turns = uint32_t(round_up(D, kTurnK) / kTurnK);
         set_pairs(sh, L.weight.planes, L.hidden.planes, kFullLimit);
         sh.tiles_a = uint32_t(ceil_div(vp, kTile));
         sh.tiles_b = uint32_t(ceil_div(L.n_pad, kTile));
@@ -766,7 +768,7 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
             A.krows = uint32_t(vp);
             B.extent = uint32_t(N);
             ProductShape ps = grad_shape(L.weight.planes, dhidden_dtype);
-            ps.stages = uint32_t(ceil_div(vp, kStageK));
+            ps.turns = uint32_t(ceil_div(vp, kTurnK));
             ps.tiles_a = uint32_t(ceil_div(D, kTile));
             ps.tiles_b = uint32_t(ceil_div(N, kTile));
             ps.splits = L.h_splits;
@@ -783,7 +785,7 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
             A.krows = B.krows = uint32_t(L.n_pad);
             B.extent = uint32_t(L.piece);
             ProductShape ps = grad_shape(L.hidden.planes, dweight_dtype);
-            ps.stages = uint32_t(L.n_pad / kStageK);
+            ps.turns = uint32_t(L.n_pad / kTurnK);
             ps.tiles_a = uint32_t(ceil_div(D, kTile));
             ps.tiles_b = uint32_t(ceil_div(vp, kTile));
             ps.splits = L.w_splits;

@@ -16,12 +16,14 @@
 // planes with i + j up to a limit: what a limit of 2 drops is 2^-24 of a term,
 // what a limit of 1 drops 2^-16.
 //
-// A workgroup of kWavesA x kWavesB waves owns a tile of kTA x kTB outputs. A
-// stage is 64 values of k of both operands, moved straight into LDS
-// (buffer_load ... lds, 16 bytes a lane) while the stage before it is
-// multiplied. LDS holds 16-byte chunks permuted by an XOR of the row, which
-// the loads apply to their global addresses (LDS-direct loads write lane after
-// lane) and the fragment reads to their LDS addresses.
+// A workgroup of WA x WB waves owns a tile of TA x TB outputs. k advances in
+// stages of 32 values of both operands, moved straight into LDS
+// (buffer_load ... lds, 16 bytes a lane) by way of four buffers: while stage s
+// is multiplied, s + 1 is there (its first fragments are read under the last
+// products of s), s + 2 is on its way and s + 3 is asked for. LDS holds 16-byte
+// chunks permuted by an XOR of the row, which the loads apply to their global
+// addresses (LDS-direct loads write lane after lane) and the fragment reads to
+// their LDS addresses.
 #pragma once
 
 #include "values.h"
@@ -33,7 +35,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kStageK = 64;
+constexpr int kStageK = 32;
+constexpr int kBuffers = 4;
+
+// k is padded to whole turns of the four buffers.
+constexpr int kTurnK = kBuffers * kStageK;
 
 struct MatOperand {
     const bf16_t* plane0;
@@ -45,7 +51,7 @@ struct MatOperand {
 };
 
 struct ProductShape {
-    uint32_t stages;    // of one segment: ceil(k / 64)
+    uint32_t turns;     // of one segment: ceil(k / 128)
     uint32_t segments;  // pairs of planes: 1 .. 6
     uint32_t pair_a, pair_b;  // the planes of segment s: two bits each, at bit 2 s
     uint32_t tiles_a, tiles_b, splits;
@@ -66,18 +72,20 @@ inline void set_pairs(ProductShape& sh, int planes_a, int planes_b, int limit)
 // What one lane and wave move of an operand's stage, T rows (or columns) wide.
 template <bool kKRows, int T, int kWaves>
 struct StageLoader {
-    static constexpr int kLoads = T / 8 / kWaves;  // 1 KB wave loads
+    static constexpr int kLoads = T / 16 / kWaves;  // 1 KB wave loads
     static_assert(kLoads >= 1, "every wave moves at least one load");
-    static constexpr int kChunks = T / 8;                 // by k: 16-byte chunks of a row
-    static constexpr int kRowsPerLoad = 1024 / (2 * T);   // by k
+    static constexpr int kChunks = T / 8;                // by k: 16-byte chunks of a row
+    static constexpr int kRowsPerLoad = 1024 / (2 * T);  // by k
     uint32_t off[kLoads];  // by rows: byte offset of each load; by k: of its columns alone
     uint32_t row;          // by k: the first load's row
     int wave;
 
-    // XOR on the chunk index of LDS row `row` (see the file comment).
+    // XOR on the chunk index of LDS row `row`. By rows (64 bytes each) the 8
+    // rows of a fragment that are read together cover all banks; by k the 4
+    // rows that 16 lanes read together do.
     static __device__ __forceinline__ uint32_t swizzle(uint32_t row)
     {
-        return kKRows ? 2 * (row & 3) : row & 7;
+        return kKRows ? 2 * (row & 3) : (row >> 1) & 3;
     }
 
     __device__ __forceinline__ void init(const MatOperand& m, uint32_t first, int wave_, int lane)
@@ -90,28 +98,33 @@ struct StageLoader {
                 const uint32_t chunk = (lane % kChunks) ^ swizzle(row + j * kRowsPerLoad);
                 off[j] = min(first + chunk * 8, m.extent - 8) * 2;
             } else {
-                const uint32_t r = (wave * kLoads + j) * 8 + lane / 8;
-                const uint32_t chunk = (lane & 7) ^ swizzle(r);
+                const uint32_t r = (wave * kLoads + j) * 16 + lane / 4;
+                const uint32_t chunk = (lane & 3) ^ swizzle(r);
                 off[j] = min(first + r, m.extent - 1) * m.ld * 2 + chunk * 16;
             }
         }
     }
 
-    // Enqueues the stage from k0 on of plane p into lds.
-    __device__ __forceinline__ void load(const MatOperand& m, const bf16_t* p, uint32_t k0, bf16_t* lds) const
+    // Where the stage from k0 on of plane p starts, as a descriptor of `bytes`
+    // bytes: of none, its loads fetch nothing.
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage(const MatOperand& m, const bf16_t* p, uint32_t k0,
+                                                                   uint32_t bytes)
     {
-        const bf16_t* base = p + (kKRows ? size_t(k0) * m.ld : size_t(k0));
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16_t*>(base), 0, 0xFFFFFFFFu,
-                                                            0x00020000);
-        const uint32_t last = m.krows - 1 - k0;  // by k: the last row of the stage that may be read
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            // rows of a stage and the bytes of a row fit 24 bits
-            const uint32_t o =
-                kKRows ? __umul24(min(row + j * kRowsPerLoad, last), m.ld * 2) + off[j] : off[j];
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + j) * 512), 16, o, 0, 0, 0);
-        }
+        // (by k: not past the last row)
+        const bf16_t* base = p + (kKRows ? size_t(min(k0, m.krows - 1)) * m.ld : size_t(k0));
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16_t*>(base), 0, bytes, 0x00020000);
+    }
+
+    // Enqueues load j of the stage into lds.
+    __device__ __forceinline__ void load(const MatOperand& m, __amdgpu_buffer_rsrc_t at, uint32_t k0, int j,
+                                         bf16_t* lds) const
+    {
+        // by k: the last row of the stage that may be read; rows of a stage
+        // and the bytes of a row fit 24 bits
+        const uint32_t last = m.krows - 1 - min(k0, m.krows - 1);
+        const uint32_t o = kKRows ? __umul24(min(row + j * kRowsPerLoad, last), m.ld * 2) + off[j] : off[j];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            at, (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + j) * 512), 16, o, 0, 0, 0);
     }
 };
 
@@ -130,7 +143,7 @@ struct FragmentReader {
             base = row * (2 * T) + (((col >> 3) ^ (2 * (row & 3))) << 4) + ((col & 4) << 1);
         } else {
             const uint32_t row = first + (lane & 31);
-            base = row * 128 + (((lane >> 5) ^ (row & 7)) << 4);
+            base = row * (2 * kStageK) + (((lane >> 5) ^ ((row >> 1) & 3)) << 4);
         }
     }
 
@@ -139,7 +152,7 @@ struct FragmentReader {
     {
         if (kKRows) {
             typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-            // chunk + 4 f under the XOR of bits 1 and 2: bit 2 of 4 f meets it, the rest adds
+            // 4 f chunks on: the XOR reaches bit 2 of the chunk, which 4 f meets too
             const char* p = reinterpret_cast<const char*>(lds) + (base ^ (uint32_t(f) << 6)) + kk * 16 * (2 * T);
             union {
                 s16x4 h[2];
@@ -149,15 +162,27 @@ struct FragmentReader {
             u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * (2 * T)));
             return u.v;
         }
-        const char* p = reinterpret_cast<const char*>(lds) + (base ^ (uint32_t(kk) << 5)) + f * (32 * 128);
+        const char* p = reinterpret_cast<const char*>(lds) + (base ^ (uint32_t(kk) << 5)) + f * (32 * 2 * kStageK);
         return *reinterpret_cast<const bf16x8*>(p);
     }
 };
 
+// The LDS of a tile, as variables of their own, so that the compiler knows
+// which loads a fragment read has to wait for.
+struct TileBuffers {
+    bf16_t *a[kBuffers], *b[kBuffers];
+};
+
+#define GCQ_TILE_BUFFERS(name, TA, TB)                                                                       \
+    __shared__ bf16_t name##_a0[(TA) * kStageK], name##_a1[(TA) * kStageK], name##_a2[(TA) * kStageK],       \
+        name##_a3[(TA) * kStageK], name##_b0[(TB) * kStageK], name##_b1[(TB) * kStageK],                     \
+        name##_b2[(TB) * kStageK], name##_b3[(TB) * kStageK];                                                \
+    const TileBuffers name = {{name##_a0, name##_a1, name##_a2, name##_a3},                                  \
+                              {name##_b0, name##_b1, name##_b2, name##_b3}}
+
 template <bool kAK, bool kBK, int TA, int TB, int WA, int WB>
 struct TileProduct {
     static constexpr int kWaves = WA * WB;
-    static constexpr int kThreads = kWaves * kWave;
     static constexpr int RA = TA / WA / 32, RB = TB / WB / 32;  // 32 x 32 products of a wave
     using LoadA = StageLoader<kAK, TA, kWaves>;
     using LoadB = StageLoader<kBK, TB, kWaves>;
@@ -166,13 +191,11 @@ struct TileProduct {
         f32x16 v[RA][RB];
     };
 
-    // Multiplies stages [s0, s1) of the tile at (a0, b0). The four buffers
-    // are LDS variables of their own, so that the compiler knows which loads
-    // a fragment read has to wait for.
-    static __device__ __forceinline__ void run(const MatOperand& A, const MatOperand& B,
-                                               const ProductShape& sh, uint32_t a0, uint32_t b0,
-                                               uint32_t s0, uint32_t s1, bf16_t* la0, bf16_t* la1,
-                                               bf16_t* lb0, bf16_t* lb1, Acc& acc)
+    // Multiplies turns [t0, t1) of the tile at (a0, b0). LDS is free for
+    // other use when it returns.
+    static __device__ __forceinline__ void run(const MatOperand& A, const MatOperand& B, const ProductShape& sh,
+                                               uint32_t a0, uint32_t b0, uint32_t t0, uint32_t t1,
+                                               const TileBuffers& lds, Acc& acc)
     {
         const int lane = threadIdx.x & (kWave - 1);
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -190,77 +213,97 @@ struct TileProduct {
 #pragma unroll
             for (int j = 0; j < RB; ++j)
                 acc.v[i][j] = f32x16{};
-
-        // the stage that is fetched next
-        uint32_t seg = s0 / sh.stages, k0 = (s0 - seg * sh.stages) * kStageK;
-        const auto fetch = [&](bf16_t* la, bf16_t* lb) {
-            const uint32_t pa = (sh.pair_a >> (2 * seg)) & 3, pb = (sh.pair_b >> (2 * seg)) & 3;
-            ga.load(A, A.plane0 + pa * A.plane_stride, k0, la);
-            gb.load(B, B.plane0 + pb * B.plane_stride, k0, lb);
-            k0 += kStageK;
-            if (k0 == sh.stages * kStageK) {
-                k0 = 0;
-                ++seg;
-            }
-        };
-        // the fragments of the next 16 values of k are read while these are
-        // multiplied
-        const auto multiply = [&](const bf16_t* la, const bf16_t* lb) {
-            bf16x8 a[2][RA], b[2][RB];
-            const auto read = [&](int kk) {
-#pragma unroll
-                for (int j = 0; j < RB; ++j)
-                    b[kk & 1][j] = fb.read(lb, j, kk);
-#pragma unroll
-                for (int i = 0; i < RA; ++i)
-                    a[kk & 1][i] = fa.read(la, i, kk);
-            };
-            read(0);
-#pragma unroll
-            for (int kk = 0; kk < kStageK / 16; ++kk) {
-                if (kk + 1 < kStageK / 16)
-                    read(kk + 1);
-#pragma unroll
-                for (int i = 0; i < RA; ++i)
-#pragma unroll
-                    for (int j = 0; j < RB; ++j)
-                        acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[kk & 1][i], b[kk & 1][j],
-                                                                              acc.v[i][j], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        };
-        if (s0 >= s1)
+        if (t0 >= t1)
             return;
-        // One barrier a stage: behind it every wave's loads of the stage are in
-        // LDS and every wave is done with the buffers that the next stage's
-        // loads then overwrite.
-        fetch(la0, lb0);
-        uint32_t s = s0;
-        for (; s + 2 <= s1; s += 2) {
-            stage_ready();
-            fetch(la1, lb1);
-            multiply(la0, lb0);
-            stage_ready();
-            if (s + 2 < s1)
-                fetch(la0, lb0);
-            multiply(la1, lb1);
+
+        // the stage that is fetched next: its place in the planes, and how
+        // many are left
+        const uint32_t k_end = sh.turns * kTurnK;
+        uint32_t seg = t0 / sh.turns, k0 = (t0 - seg * sh.turns) * kTurnK, left = (t1 - t0) * kBuffers;
+        struct Fetch {
+            __amdgpu_buffer_rsrc_t a, b;
+            uint32_t k0;
+        };
+        const auto next_stage = [&]() {
+            const uint32_t pa = (sh.pair_a >> (2 * seg)) & 3, pb = (sh.pair_b >> (2 * seg)) & 3;
+            // (readfirstlane keeps what the compiler would select in vector
+            // registers in scalar ones)
+            const uint32_t bytes = __builtin_amdgcn_readfirstlane(left ? 0xFFFFFFFFu : 0u);
+            const Fetch f = {LoadA::stage(A, A.plane0 + pa * A.plane_stride, k0, bytes),
+                             LoadB::stage(B, B.plane0 + pb * B.plane_stride, k0, bytes), k0};
+            left -= bytes & 1;
+            k0 += kStageK;
+            const uint32_t over = __builtin_amdgcn_readfirstlane(k0 == k_end ? 1u : 0u);
+            seg += over;
+            k0 -= over * k_end;
+            return f;
+        };
+        constexpr int kLoads = LoadA::kLoads + LoadB::kLoads;
+        const auto load = [&](const Fetch& f, int j, int buffer) {
+            if (j < LoadA::kLoads)
+                ga.load(A, f.a, f.k0, j, lds.a[buffer]);
+            else if (j < kLoads)
+                gb.load(B, f.b, f.k0, j - LoadA::kLoads, lds.b[buffer]);
+        };
+
+#pragma unroll
+        for (int s = 0; s < kBuffers - 1; ++s) {
+            const Fetch f = next_stage();
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                load(f, j, s);
         }
-        stage_ready();
-        if (s < s1) {
-            multiply(la0, lb0);
-            workgroup_sync();
+        wait_loads<2 * kLoads>();
+        bf16x8 a[2][RA], b[2][RB];
+#pragma unroll
+        for (int j = 0; j < RB; ++j)
+            b[0][j] = fb.read(lds.b[0], j, 0);
+#pragma unroll
+        for (int i = 0; i < RA; ++i)
+            a[0][i] = fa.read(lds.a[0], i, 0);
+
+        for (uint32_t t = t0; t < t1; ++t) {
+#pragma unroll
+            for (int s = 0; s < kBuffers; ++s) {
+                // behind the barrier stage s + 1 is in LDS for everybody, and
+                // nobody reads the buffer of s - 1 any more, which s + 3 takes
+                wait_loads<kLoads>();
+                const Fetch f = next_stage();
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const int from = kk == 0 ? s : (s + 1) % kBuffers;
+                    // each row of products runs over the reads of a fragment
+                    // of the next 16 k and one load
+#pragma unroll
+                    for (int i = 0; i < (RA > RB ? RA : RB); ++i) {
+                        if (i < RB)
+                            b[kk ^ 1][i] = fb.read(lds.b[from], i, kk ^ 1);
+                        if (i < RA)
+                            a[kk ^ 1][i] = fa.read(lds.a[from], i, kk ^ 1);
+                        constexpr int kSteps = 2 * (RA > RB ? RA : RB), kEach = (kLoads + kSteps - 1) / kSteps;
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e)
+                            load(f, (kk * (RA > RB ? RA : RB) + i) * kEach + e, (s + kBuffers - 1) % kBuffers);
+                        if (i < RA) {
+#pragma unroll
+                            for (int j = 0; j < RB; ++j)
+                                acc.v[i][j] =
+                                    __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[kk][i], b[kk][j], acc.v[i][j], 0, 0, 0);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
         }
+        wait_loads<0>();
     }
 
-    static __device__ __forceinline__ void stage_ready()
+    // Waits until all but the last N loads of this wave are in LDS, then for
+    // every wave of the workgroup to get there.
+    template <int N>
+    static __device__ __forceinline__ void wait_loads()
     {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        workgroup_sync();
-    }
-
-    static __device__ __forceinline__ void workgroup_sync()
-    {
-        asm volatile("" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     }
