@@ -80,12 +80,13 @@ struct StageLoader {
     uint32_t row;          // by k: the first load's row
     int wave;
 
-    // XOR on the chunk index of LDS row `row`. By rows (64 bytes each) the 8
-    // rows of a fragment that are read together cover all banks; by k the 4
-    // rows that 16 lanes read together do.
+    // XOR on the chunk index of LDS row `row`, so that what is read in one
+    // clock covers the 64 banks (256 bytes): by rows (64 bytes each) the same
+    // chunk of 16 rows, by k 64 bytes of 4 rows. SQ_LDS_BANK_CONFLICT is zero;
+    // covering 32 banks alone left it at half of SQ_LDS_IDX_ACTIVE.
     static __device__ __forceinline__ uint32_t swizzle(uint32_t row)
     {
-        return kKRows ? 2 * (row & 3) : (row >> 1) & 3;
+        return kKRows ? 4 * (row & 3) : (row >> 2) & 3;
     }
 
     __device__ __forceinline__ void init(const MatOperand& m, uint32_t first, int wave_, int lane)
@@ -140,10 +141,10 @@ struct FragmentReader {
             const uint32_t g = lane >> 4, j = lane & 15;
             const uint32_t row = 8 * (g >> 1) + (j >> 2);
             const uint32_t col = first + 16 * (g & 1) + 4 * (j & 3);
-            base = row * (2 * T) + (((col >> 3) ^ (2 * (row & 3))) << 4) + ((col & 4) << 1);
+            base = row * (2 * T) + (((col >> 3) ^ StageLoader<true, T, 1>::swizzle(row)) << 4) + ((col & 4) << 1);
         } else {
             const uint32_t row = first + (lane & 31);
-            base = row * (2 * kStageK) + (((lane >> 5) ^ ((row >> 1) & 3)) << 4);
+            base = row * (2 * kStageK) + (((lane >> 5) ^ StageLoader<false, T, 1>::swizzle(row)) << 4);
         }
     }
 
@@ -152,7 +153,7 @@ struct FragmentReader {
     {
         if (kKRows) {
             typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-            // 4 f chunks on: the XOR reaches bit 2 of the chunk, which 4 f meets too
+            // 4 f chunks on: the XOR reaches bits 2 and 3 of the chunk, which 4 f meets too
             const char* p = reinterpret_cast<const char*>(lds) + (base ^ (uint32_t(f) << 6)) + kk * 16 * (2 * T);
             union {
                 s16x4 h[2];
