@@ -142,35 +142,49 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
     for (int j = 0; j < P::RB; ++j) {
         const uint32_t n = tb * TB + wb * L::kRowsB + j * 32 + acc_col(lane);
         const int64_t t = n < N ? target[n] : -1;
-        // the target's place in this lane's part, if it is there
+        // the target's place in this wave's part, if it is there: it hardly
+        // ever is, and only the last tile reaches past the vocabulary
         const uint32_t at = t >= 0 && t < int64_t(V) ? uint32_t(t) - a_wave : 0xFFFFFFFFu;
-        const uint32_t left = V > a_wave ? V - a_wave : 0;
-        float top = -INFINITY, mine = 0.0f;
-        bool found = false;
+        if (__any(at < uint32_t(L::kRowsA))) {
+            float mine = 0.0f;
+            bool found = false;
 #pragma unroll
-        for (int i = 0; i < P::RA; ++i)
+            for (int i = 0; i < P::RA; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t v = i * 32 + acc_row(e, lane);
-                if (v >= left)
-                    acc.v[i][j][e] = -INFINITY;
-                if (v == at) {
-                    mine = acc.v[i][j][e];
-                    found = true;
-                }
-                top = fmaxf(top, acc.v[i][j][e]);
-            }
-        if (found)
-            target_logit[n] = mine;
-        top = fmaxf(top, __shfl_xor(top, 32));
-        float sum = 0.0f;
-        // a part that holds no logit above -inf adds nothing
-        const float ref = top == -INFINITY ? 0.0f : top;
+                for (int e = 0; e < 16; ++e)
+                    if (i * 32 + acc_row(e, lane) == at) {
+                        mine = acc.v[i][j][e];
+                        found = true;
+                    }
+            if (found)
+                target_logit[n] = mine;
+        }
+        if (a_wave + L::kRowsA > V) {
+            const uint32_t left = V > a_wave ? V - a_wave : 0;
+#pragma unroll
+            for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (i * 32 + acc_row(e, lane) >= left)
+                        acc.v[i][j][e] = -INFINITY;
+        }
+        float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < P::RA; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                sum += __builtin_amdgcn_exp2f((acc.v[i][j][e] - ref) * kLog2e);
+                top = fmaxf(top, acc.v[i][j][e]);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // exp(l - top) = 2^(l log2 e - top log2 e); a part that holds no logit
+        // above -inf adds nothing
+        const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
+        float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                sums[e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][e], kLog2e, -ref));
+        float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
         sum += __shfl_xor(sum, 32);
         if (lane < 32 && n < N)
             parts[size_t(n) * nparts + ta * WA + wa] = LossPart{top, sum};
@@ -256,23 +270,53 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
     for (int j = 0; j < P::RB; ++j) {
         const uint32_t n = b_wave + j * 32 + acc_col(lane);
         bool live = n < N;
-        uint32_t t = 0;
+        uint32_t at = 0xFFFFFFFFu;  // the target's place in this wave's part
         float z = 0.0f, d = 0.0f;
         if (live) {
             const int64_t tn = target[n];
             live = tn != ignore && tn >= 0 && tn < int64_t(V);
-            t = uint32_t(tn);
-            z = lse[n];
-            d = dloss[n];
+            at = live ? uint32_t(tn) - (v0 + a_wave) : at;
+            z = live ? lse[n] : 0.0f;
+            d = live ? dloss[n] : 0.0f;
+        }
+        // p. Rounded to bf16 at the end, it takes one rounding of (l - lse)
+        // log2 e: 2^-24 of it, some 1e-6 of p
+        const float zl = z * kLog2e;
+#pragma unroll
+        for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc.v[i][j][e] = kPlanes == 1
+                                     ? __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][e], kLog2e, -zl))
+                                     : exp_neg(acc.v[i][j][e] - z);
+        if (__any(at < uint32_t(L::kRowsA))) {
+#pragma unroll
+            for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc.v[i][j][e] -= i * 32 + acc_row(e, lane) == at ? 1.0f : 0.0f;
+        }
+        // a row without a target holds zeros, whatever its logits were
+        if (__any(!live)) {
+#pragma unroll
+            for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc.v[i][j][e] = live ? acc.v[i][j][e] : 0.0f;
+        }
+        if (v0 + a_wave + L::kRowsA > V) {
+            const uint32_t left = V > v0 + a_wave ? V - (v0 + a_wave) : 0;
+#pragma unroll
+            for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc.v[i][j][e] = i * 32 + acc_row(e, lane) >= left ? 0.0f : acc.v[i][j][e];
         }
 #pragma unroll
         for (int i = 0; i < P::RA; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t v = v0 + a_wave + i * 32 + acc_row(e, lane);
-                const float p = exp_neg(acc.v[i][j][e] - z) - (v == t ? 1.0f : 0.0f);
-                acc.v[i][j][e] = live && v < V ? d * p : 0.0f;
-            }
+            for (int e = 0; e < 16; ++e)
+                acc.v[i][j][e] *= d;
     }
 #pragma unroll
     for (int plane = 0; plane < kPlanes; ++plane) {
