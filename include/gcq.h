@@ -408,7 +408,7 @@ int linear_xent_loss(const void* hidden, const void* weight, int dtype, size_t N
  *   dhidden[n] = sum_v G_nv weight[v],   dweight[v] = sum_n G_nv hidden[n].
  * A row without a target adds nothing, whatever hidden[n], lse[n] and
  * dloss[n] hold there. G is formed piece by piece of the vocabulary (about
- * 256 MB of the workspace); sums are fp32 in a fixed order.
+ * 512 MB of the workspace); sums are fp32 in a fixed order.
  *   lse, dloss  [N] fp32 (lse as linear_xent_loss gives it)
  *   dhidden     [N, D] of dhidden_dtype, or NULL: not computed
  *   dweight     [V, D] of dweight_dtype, or NULL: not computed
