@@ -36,81 +36,165 @@ __device__ __forceinline__ float exp_neg(float x)
     return r == 0.0f ? 0.0f : __builtin_fmaf(r, lo * kLn2, r);
 }
 
-// ---- operands as bf16 planes ------------------------------------------------
-
-constexpr int kMaxPlanes = 3;
-
-// The next plane of x: its bf16 rounding, which is taken off x (exactly). A
-// finite x never becomes infinite; an infinity or NaN stays in the first
-// plane alone.
-__device__ __forceinline__ bf16_t next_plane(float& x)
+// Whether row n has a target among the rows of the vocabulary.
+__device__ __forceinline__ bool has_target(const int64_t* target, size_t n, int64_t ignore, size_t V)
 {
-    const float top = 0x1.FEp127f;  // largest bf16
-    if (!(fabsf(x) <= std::numeric_limits<float>::max())) {
-        const bf16_t h = bf16_t(x);
-        x = 0.0f;
-        return h;
-    }
-    const bf16_t h = bf16_t(fminf(fmaxf(x, -top), top));
-    x -= float(h);
-    return h;
+    const int64_t t = target[n];
+    return t != ignore && t >= 0 && size_t(t) < V;
 }
 
-constexpr int kPlaneThreads = 256;
+// ---- operands as planes --------------------------------------------------------
 
-// src [rows][d] -> kPlanes planes [rows_out][d_out] (d_out a multiple of 8),
-// one behind the other, zeros behind the last column and row and in the rows
-// whose target is no row of the vocabulary (`target` not NULL): what such
-// rows hold, NaN included, reaches nothing.
-template <typename T, int kPlanes>
-__global__ __launch_bounds__(kPlaneThreads) void planes_kernel(
-    const T* __restrict__ src, size_t rows, size_t d, bf16_t* __restrict__ out, size_t rows_out, size_t d_out,
-    const int64_t* __restrict__ target, int64_t ignore, size_t V)
+constexpr int kRowThreads = 256, kRowWaves = kRowThreads / kWave;
+
+// A row's values c .. c + 7 (zeros behind d), whatever the alignment.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, size_t c, size_t d, float (&v)[8])
 {
-    const size_t chunks = d_out / 8, total = rows_out * chunks;
-    const bool vec = (d & 7) == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
-    for (size_t q = size_t(blockIdx.x) * kPlaneThreads + threadIdx.x; q < total;
-         q += size_t(gridDim.x) * kPlaneThreads) {
-        const size_t row = q / chunks, c = (q - row * chunks) * 8;
-        bool live = row < rows;
-        if (live && target) {
-            const int64_t t = target[row];
-            live = t != ignore && t >= 0 && size_t(t) < V;
-        }
-        float v[8] = {};
-        if (live && c < d) {
-            const T* p = src + row * d + c;
-            if (vec) {
+    typedef T Vec __attribute__((ext_vector_type(8)));
+    typedef Vec VecAny __attribute__((aligned(sizeof(T))));
+    if (c + 8 <= d) {
+        const auto x = __builtin_convertvector(*reinterpret_cast<const VecAny*>(row + c), vec_of<float, 8>);
 #pragma unroll
-                for (int k = 0; k < 8; k += kVec<T>) {
-                    const vec_f32<T> x = load_vec(p + k);
+        for (int k = 0; k < 8; ++k)
+            v[k] = x[k];
+        return;
+    }
 #pragma unroll
-                    for (int e = 0; e < kVec<T>; ++e)
-                        v[k + e] = x[e];
-                }
-            } else {
+    for (int k = 0; k < 8; ++k)
+        v[k] = c + k < d ? float(row[c + k]) : 0.0f;
+}
+
+// What the scale of a matrix goes by: the largest finite |x| of its rows (of
+// those with a target, if `target` is not NULL), a maximum for each workgroup.
+constexpr unsigned kMaxParts = 1024;
+
+struct MaxOf {
+    const void* src;
+    size_t rows, d;
+    const int64_t* target;
+    float* parts;  // [kMaxParts]
+};
+
+__device__ __forceinline__ float workgroup_max(float m)
+{
+    __shared__ float lds[kRowWaves];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (c + k < d)
-                        v[k] = float(p[k]);
-            }
-        }
-#pragma unroll
-        for (int plane = 0; plane < kPlanes; ++plane) {
-            bf16x8 h;
+    for (int off = kWave / 2; off > 0; off >>= 1)
+        m = fmaxf(m, __shfl_xor(m, off));
+    if ((threadIdx.x & (kWave - 1)) == 0)
+        lds[threadIdx.x / kWave] = m;
+    __syncthreads();
+    m = lds[0];
+    for (int w = 1; w < kRowWaves; ++w)
+        m = fmaxf(m, lds[w]);
+    return m;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kRowThreads) void largest_kernel(MaxOf a, int64_t ignore, size_t V)
+{
+    const T* src = static_cast<const T*>(a.src);
+    const int lane = threadIdx.x & (kWave - 1);
+    float m = 0.0f;
+    for (size_t r = size_t(blockIdx.x) * kRowWaves + threadIdx.x / kWave; r < a.rows; r += size_t(gridDim.x) * kRowWaves) {
+        if (a.target && !has_target(a.target, r, ignore, V))
+            continue;
+        const T* row = src + r * a.d;
+#pragma unroll 2
+        for (size_t c = lane * 8; c < a.d; c += kWave * 8) {
+            float v[8];
+            load8(row, c, a.d, v);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                h[k] = next_plane(v[k]);
-            *reinterpret_cast<bf16x8*>(out + plane * (rows_out * d_out) + row * d_out + c) = h;
+                m = fabsf(v[k]) <= std::numeric_limits<float>::max() ? fmaxf(m, fabsf(v[k])) : m;
         }
     }
+    m = workgroup_max(m);
+    if (threadIdx.x == 0)
+        a.parts[blockIdx.x] = m;
+}
+
+// The exponent that brings the largest value to [2^14, 2^15): called by whole
+// workgroups.
+__device__ __forceinline__ int exponent_of(const float* parts)
+{
+    float m = 0.0f;
+#pragma unroll
+    for (unsigned k = 0; k < kMaxParts; k += kRowThreads)
+        m = fmaxf(m, parts[k + threadIdx.x]);
+    m = workgroup_max(m);
+    return m > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(m) : 0;
+}
+
+// The exponent alone, where the values are written later (G).
+__global__ __launch_bounds__(kRowThreads) void exponent_kernel(const float* parts, int* exponent)
+{
+    const int k = exponent_of(parts);
+    if (threadIdx.x == 0)
+        *exponent = k;
+}
+
+// src [rows][d] -> kPlanes planes [rows_out][d_out] (d_out a multiple of 8),
+// one behind the other, of bf16 as it is (kF16 = false) or of fp16, scaled
+// where `parts` is not NULL; zeros behind the last column and row, and in the
+// rows that have no target if `target` is not NULL: what such rows hold, NaN
+// included, reaches nothing. One wave a row.
+template <typename T, bool kF16, int kPlanes>
+__global__ __launch_bounds__(kRowThreads) void planes_kernel(const T* __restrict__ src, size_t rows, size_t d,
+                                                             uint16_t* __restrict__ out, size_t rows_out, size_t d_out,
+                                                             const int64_t* __restrict__ target, int64_t ignore,
+                                                             size_t V, const float* __restrict__ parts,
+                                                             int* __restrict__ exponent)
+{
+    int scale = 0;
+    if (kF16 && parts) {
+        scale = exponent_of(parts);
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            *exponent = scale;
+    }
+    const int lane = threadIdx.x & (kWave - 1);
+    for (size_t r = size_t(blockIdx.x) * kRowWaves + threadIdx.x / kWave; r < rows_out;
+         r += size_t(gridDim.x) * kRowWaves) {
+        const bool live = r < rows && (!target || has_target(target, r, ignore, V));
+#pragma unroll 2
+        for (size_t c = lane * 8; c < d_out; c += kWave * 8) {
+            float v[8] = {};
+            if (live)
+                load8(src + r * d, c, d, v);
+#pragma unroll
+            for (int plane = 0; plane < kPlanes; ++plane) {
+                s16x8 w;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (!kF16) {
+                        w[k] = __builtin_bit_cast(short, bf16_t(v[k]));
+                        continue;
+                    }
+                    if (plane == 0)
+                        v[k] = __builtin_amdgcn_ldexpf(v[k], scale);
+                    const f16_t h = f16_t(v[k]);
+                    w[k] = __builtin_bit_cast(short, h);
+                    // an infinity or NaN stays in the first plane alone
+                    v[k] = fabsf(float(h)) <= 65504.0f ? (v[k] - float(h)) * 0x1p11f : 0.0f;
+                }
+                *reinterpret_cast<s16x8*>(out + plane * (rows_out * d_out) + r * d_out + c) = w;
+            }
+        }
+    }
+}
+
+// What sums of products of scaled operands are multiplied by, as an exponent.
+__device__ __forceinline__ int unscale(const MatOperand& a, const MatOperand& b)
+{
+    return -((a.exponent ? *a.exponent : 0) + (b.exponent ? *b.exponent : 0));
 }
 
 // ---- tiles of the logits -------------------------------------------------------
 
-template <int TA, int TB, int WA, int WB>
+template <bool kF16, int TA, int TB, int WA, int WB>
 struct LogitTile {
-    using Product = TileProduct<false, false, TA, TB, WA, WB>;
+    using Product = TileProduct<kF16, false, false, TA, TB, WA, WB>;
     static constexpr int kRowsA = TA / WA, kRowsB = TB / WB;  // of one wave
 };
 
@@ -120,13 +204,13 @@ struct LossPart {
 
 // Vocabulary tile x token tile. A wave's part of a token's row is kRowsA
 // logits, half of them in each half of the wave.
-template <int TA, int TB, int WA, int WB>
+template <bool kF16, int TA, int TB, int WA, int WB>
 __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
     MatOperand weight, MatOperand hidden, ProductShape sh, uint32_t N, uint32_t V,
     const int64_t* __restrict__ target, LossPart* __restrict__ parts, uint32_t nparts,
     float* __restrict__ target_logit)
 {
-    using L = LogitTile<TA, TB, WA, WB>;
+    using L = LogitTile<kF16, TA, TB, WA, WB>;
     using P = typename L::Product;
     GCQ_TILE_BUFFERS(lds, TA, TB);
     uint32_t ta, tb;
@@ -142,6 +226,14 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
     for (int j = 0; j < P::RB; ++j) {
         const uint32_t n = tb * TB + wb * L::kRowsB + j * 32 + acc_col(lane);
         const int64_t t = n < N ? target[n] : -1;
+        if (kF16) {
+            const int back = unscale(weight, hidden);
+#pragma unroll
+            for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc.v[i][j][e] = __builtin_amdgcn_ldexpf(acc.v[i][j][e], back);
+        }
         // the target's place in this wave's part, if it is there: it hardly
         // ever is, and only the last tile reaches past the vocabulary
         const uint32_t at = t >= 0 && t < int64_t(V) ? uint32_t(t) - a_wave : 0xFFFFFFFFu;
@@ -233,18 +325,20 @@ __global__ __launch_bounds__(kJoinThreads) void loss_join_kernel(
 // (zeros from N on, and behind the vocabulary). Each wave turns its part of
 // the tile into rows of G through LDS, so that the stores are whole rows.
 struct GradOut {
-    bf16_t* plane0;  // [rows_out][ld]
+    uint16_t* plane0;  // [rows_out][ld]
     size_t plane_stride;
     uint32_t ld, rows_out;
+    const int* exponent;  // fp16 planes hold G times 2^exponent
 };
 
-template <int TA, int TB, int WA, int WB, int kPlanes>
+// One plane of bf16, or kPlanes of fp16.
+template <bool kF16, int TA, int TB, int WA, int WB, int kPlanes>
 __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
     MatOperand weight, MatOperand hidden, ProductShape sh, uint32_t N, uint32_t v0, uint32_t V,
     const int64_t* __restrict__ target, int64_t ignore, const float* __restrict__ lse,
     const float* __restrict__ dloss, GradOut out)
 {
-    using L = LogitTile<TA, TB, WA, WB>;
+    using L = LogitTile<kF16, TA, TB, WA, WB>;
     using P = typename L::Product;
     GCQ_TILE_BUFFERS(lds, TA, TB);
     uint32_t ta, tb;
@@ -257,9 +351,11 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
     const int wa = wave % WA, wb = wave / WA;
     const uint32_t a_wave = ta * TA + wa * L::kRowsA, b_wave = tb * TB + wb * L::kRowsB;
 
+    const int back = kF16 ? unscale(weight, hidden) : 0, up = kF16 ? *out.exponent : 0;
+
     // this wave's buffer, for its turn of values into rows
     static_assert(TA == TB && P::kWaves == 2 * kBuffers, "a buffer for each wave");
-    bf16_t* part = lds.a[0];
+    uint16_t* part = lds.a[0];
 #pragma unroll
     for (int k = 1; k < 2 * kBuffers; ++k)
         part = wave == k ? (k < kBuffers ? lds.a[k] : lds.b[k - kBuffers]) : part;
@@ -277,16 +373,16 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
             z = live ? lse[n] : 0.0f;
             d = live ? dloss[n] : 0.0f;
         }
-        // p. Rounded to bf16 at the end, it takes one rounding of (l - lse)
+        // p. In one plane in the end, it takes one rounding of (l - lse)
         // log2 e: 2^-24 of it, some 1e-6 of p
         const float zl = z * kLog2e;
 #pragma unroll
         for (int i = 0; i < P::RA; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                acc.v[i][j][e] = kPlanes == 1
-                                     ? __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][e], kLog2e, -zl))
-                                     : exp_neg(acc.v[i][j][e] - z);
+            for (int e = 0; e < 16; ++e) {
+                const float l = kF16 ? __builtin_amdgcn_ldexpf(acc.v[i][j][e], back) : acc.v[i][j][e];
+                acc.v[i][j][e] = kPlanes == 1 ? __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2e, -zl)) : exp_neg(l - z);
+            }
         if (__any(at < uint32_t(L::kRowsA))) {
 #pragma unroll
             for (int i = 0; i < P::RA; ++i)
@@ -314,10 +410,10 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
         for (int i = 0; i < P::RA; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                acc.v[i][j][e] *= d;
+                acc.v[i][j][e] = kF16 ? __builtin_amdgcn_ldexpf(acc.v[i][j][e] * d, up) : acc.v[i][j][e] * d;
     }
     // kIs x 32 values of 32 tokens at a time, all planes of them
-    constexpr int kIs = kPlanes == 3 ? 2 : P::RA, kCols = kIs * 32, kChunks = kCols / 8;
+    constexpr int kIs = P::RA, kCols = kIs * 32, kChunks = kCols / 8;
     constexpr int kPlanePart = 32 * kCols;
     static_assert(kPlanes * kPlanePart <= TA * kStageK && P::RA % kIs == 0, "the planes fit a buffer");
 #pragma unroll
@@ -329,22 +425,26 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
             for (int i = 0; i < kIs; ++i)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
                     float x[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         x[e] = acc.v[i0 + i][j][q * 4 + e];
                     const int col = i * 32 + 8 * q + 4 * (lane >> 5);
-                    bf16_t* to = part + row * kCols + ((col >> 3) ^ (row & (kChunks - 1))) * 8 + (col & 4);
+                    uint16_t* to = part + row * kCols + ((col >> 3) ^ (row & (kChunks - 1))) * 8 + (col & 4);
 #pragma unroll
                     for (int plane = 0; plane < kPlanes; ++plane) {
-                        bf16x4 w;
+                        s16x4 w;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            w[e] = bf16_t(x[e]);
-                            x[e] -= float(w[e]);
+                            if (!kF16) {
+                                w[e] = __builtin_bit_cast(short, bf16_t(x[e]));
+                                continue;
+                            }
+                            const f16_t h = f16_t(x[e]);
+                            w[e] = __builtin_bit_cast(short, h);
+                            x[e] = (x[e] - float(h)) * 0x1p11f;
                         }
-                        *reinterpret_cast<bf16x4*>(to + plane * kPlanePart) = w;
+                        *reinterpret_cast<s16x4*>(to + plane * kPlanePart) = w;
                     }
                 }
             wave_lds_sync();
@@ -355,10 +455,10 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
                 for (int r = 0; r < 32; r += kRows) {
                     const int from = r + lane / kChunks, chunk = lane % kChunks;
                     const uint32_t n = b_wave + j * 32 + from;
-                    const bf16x8 w = *reinterpret_cast<const bf16x8*>(
+                    const s16x8 w = *reinterpret_cast<const s16x8*>(
                         part + plane * kPlanePart + from * kCols + ((chunk ^ (from & (kChunks - 1))) << 3));
                     if (n < out.rows_out)
-                        *reinterpret_cast<bf16x8*>(out.plane0 + plane * out.plane_stride + size_t(n) * out.ld +
+                        *reinterpret_cast<s16x8*>(out.plane0 + plane * out.plane_stride + size_t(n) * out.ld +
                                                    a_wave + i0 * 32 + chunk * 8) = w;
                 }
             wave_lds_sync();
@@ -377,11 +477,11 @@ struct ProductOut {
     bool add;                 // onto what is there
 };
 
-template <bool kBK, int TA, int TB, int WA, int WB, typename T>
+template <bool kF16, bool kBK, int TA, int TB, int WA, int WB, typename T>
 __global__ __launch_bounds__(WA* WB* kWave, 2) void product_kernel(MatOperand A, MatOperand B,
                                                                   ProductShape sh, ProductOut<T> out)
 {
-    using P = TileProduct<true, kBK, TA, TB, WA, WB>;
+    using P = TileProduct<kF16, true, kBK, TA, TB, WA, WB>;
     GCQ_TILE_BUFFERS(lds, TA, TB);
     const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x);
     const uint32_t tiles = sh.tiles_a * sh.tiles_b, split = id / tiles;
@@ -395,6 +495,7 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void product_kernel(MatOperand A,
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wa = wave % WA, wb = wave / WA;
+    const int back = kF16 ? unscale(A, B) : 0;
     T* p = out.p + split * out.split_stride;
 #pragma unroll
     for (int j = 0; j < P::RB; ++j) {
@@ -410,7 +511,7 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void product_kernel(MatOperand A,
                 vec_of<float, 4> w;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    w[e] = acc.v[i][j][q * 4 + e];
+                    w[e] = kF16 ? __builtin_amdgcn_ldexpf(acc.v[i][j][q * 4 + e], back) : acc.v[i][j][q * 4 + e];
                 if (out.vec && a + 4 <= out.na) {
                     auto* o4 = reinterpret_cast<vec_of<T, 4>*>(o);
                     if (out.add)
@@ -489,30 +590,43 @@ int check_sizes(const char* what, size_t N, size_t V, size_t D, int dtype)
     return GC_OK;
 }
 
-// Whether the product can read the matrix where it is: exact in bf16, rows
-// aligned for 16-byte loads, whole turns.
-bool direct_ok(const void* p, size_t D, int dtype)
+// How a call computes. bf16 operands are multiplied as they are where no more
+// is asked than 16 bits of a gradient; everything else in fp16: fp16 inputs as
+// they are, others scaled by a power of two, fp32 ones in two planes. (fp16
+// holds a bf16 value exactly down to 2^-29 of the largest one of the matrix.)
+struct Mode {
+    bool f16;       // matrix products in fp16
+    bool scaled;    // inputs scaled, from copies
+    int planes;     // of the inputs
+};
+
+Mode mode_of(int dtype, bool wide)
 {
-    return dtype == GC_BF16 && D % kTurnK == 0 && aligned16(p);
+    if (dtype == GC_BF16 && !wide)
+        return Mode{false, false, 1};
+    return Mode{true, dtype != GC_F16, dtype == GC_F32 ? 2 : 1};
 }
 
-// bf16 planes that hold a value of the type exactly (fp32 to 2^-24).
-int planes_of(int dtype) { return dtype == GC_BF16 ? 1 : dtype == GC_F16 ? 2 : 3; }
+// Whether the product can read the matrix where it is: rows aligned for
+// 16-byte loads, whole turns.
+bool direct_ok(const void* p, size_t D, const Mode& m) { return !m.scaled && D % kTurnK == 0 && aligned16(p); }
 
 // An operand's planes: the matrix itself, or copies in the workspace, which
 // has room for them whatever the address.
 struct PlaneRoom {
-    size_t rows, d, off;
+    size_t rows, d, off, parts, exponent;
     int planes;
 };
 
-PlaneRoom plane_room(Carver& c, size_t rows, size_t D, int dtype)
+PlaneRoom plane_room(Carver& c, size_t rows, size_t D, const Mode& m)
 {
     PlaneRoom r{};
     r.rows = rows;
     r.d = round_up(D, kTurnK);
-    r.planes = planes_of(dtype);
+    r.planes = m.planes;
     r.off = c.take(r.planes * rows * r.d * 2);
+    r.parts = c.take(kMaxParts * sizeof(float));
+    r.exponent = c.take(sizeof(int));
     return r;
 }
 
@@ -521,41 +635,56 @@ unsigned stride_grid(size_t items, size_t per)
     return unsigned(std::max<size_t>(1, std::min(ceil_div(items, per), max_grid_blocks())));
 }
 
-// Lays out src as planes (or takes it as it is) and describes it as an
-// operand by rows; `rows_valid` of its rows may be read.
-MatOperand make_operand(const void* src, size_t rows, size_t D, int dtype, const PlaneRoom& room, char* ws,
-                        bool copy, const int64_t* target, int64_t ignore, size_t V, hipStream_t stream)
+// Launches the maxima of src.
+template <typename T>
+void launch_largest(const T* src, size_t rows, size_t d, const int64_t* target, int64_t ignore, size_t V, float* parts,
+                    hipStream_t stream)
+{
+    hipLaunchKernelGGL(largest_kernel<T>, dim3(kMaxParts), dim3(kRowThreads), 0, stream,
+                       MaxOf{src, rows, d, target, parts}, ignore, V);
+}
+
+// Describes src as an operand by rows, laid out as planes in the workspace
+// unless it can be read as it is. Of rows without a target (`target` not NULL)
+// the scale takes no notice, and with `drop` they become zeros.
+MatOperand make_operand(const void* src, size_t rows, size_t D, int dtype, const Mode& mode, const PlaneRoom& room,
+                        char* ws, const int64_t* target, bool drop, int64_t ignore, size_t V, hipStream_t stream)
 {
     MatOperand m{};
-    if (!copy) {
-        m.plane0 = static_cast<const bf16_t*>(src);
+    if (!drop && direct_ok(src, D, mode)) {
+        m.plane0 = static_cast<const uint16_t*>(src);
         m.ld = uint32_t(D);
         m.extent = uint32_t(rows);
         return m;
     }
-    bf16_t* out = reinterpret_cast<bf16_t*>(ws + room.off);
+    uint16_t* out = reinterpret_cast<uint16_t*>(ws + room.off);
+    float* parts = mode.scaled ? reinterpret_cast<float*>(ws + room.parts) : nullptr;
+    int* exponent = mode.scaled ? reinterpret_cast<int*>(ws + room.exponent) : nullptr;
     with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        constexpr int kPlanes = sizeof(T) == 4 ? 3 : std::is_same_v<T, f16_t> ? 2 : 1;
-        hipLaunchKernelGGL((planes_kernel<T, kPlanes>), dim3(stride_grid(room.rows * (room.d / 8), kPlaneThreads)),
-                           dim3(kPlaneThreads), 0, stream, static_cast<const T*>(src), rows, D, out, room.rows,
-                           room.d, target, ignore, V);
+        const T* p = static_cast<const T*>(src);
+        if (parts)
+            launch_largest(p, rows, D, target, ignore, V, parts, stream);
+        const auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3(unsigned(std::min<size_t>(ceil_div(room.rows, kRowWaves), 256 * 8))),
+                               dim3(kRowThreads), 0, stream, p, rows, D, out, room.rows, room.d,
+                               drop ? target : nullptr, ignore, V, parts, exponent);
+        };
+        if constexpr (sizeof(T) == 4)
+            launch(planes_kernel<T, true, 2>);
+        else if (mode.f16)
+            launch(planes_kernel<T, true, 1>);
+        else
+            launch(planes_kernel<T, false, 1>);
         return 0;
     });
     m.plane0 = out;
     m.plane_stride = room.rows * room.d;
     m.ld = uint32_t(room.d);
     m.extent = uint32_t(room.rows);
+    m.exponent = exponent;
     return m;
 }
-
-// Products that feed fp32 results run to 2^-24 of a term, those of a 16-bit
-// result to 2^-16 (fp16) or 2^-8 (bf16): see g_planes.
-constexpr int kFullLimit = kMaxPlanes - 1;
-
-// Planes of G for a gradient of the type: one more rounding of the size of
-// the gradient's own for bf16, none that shows for the others.
-int g_planes(int dtype) { return dtype == GC_BF16 ? 1 : dtype == GC_F16 ? 2 : 3; }
 
 // ---- loss
 
@@ -569,6 +698,7 @@ LossConfig loss_config(size_t N)
 }
 
 struct LossLayout {
+    Mode mode;
     LossConfig cfg;
     PlaneRoom weight, hidden;
     size_t parts, target_logit, nparts, total;
@@ -578,9 +708,10 @@ LossLayout loss_layout(size_t N, size_t V, size_t D, int dtype)
 {
     LossLayout L{};
     Carver c;
+    L.mode = mode_of(dtype, dtype != GC_BF16);
     L.cfg = loss_config(N);
-    L.weight = plane_room(c, V, D, dtype);
-    L.hidden = plane_room(c, N, D, dtype);
+    L.weight = plane_room(c, V, D, L.mode);
+    L.hidden = plane_room(c, N, D, L.mode);
     L.nparts = ceil_div(V, L.cfg.ta) * L.cfg.wa;
     L.parts = c.take(N * L.nparts * sizeof(LossPart));
     L.target_logit = c.take(N * 4);
@@ -601,10 +732,11 @@ constexpr int kTile = 256;
 constexpr size_t kCus = 256;
 
 struct GradLayout {
+    Mode mode;
     PlaneRoom weight, hidden;
     size_t n_pad, piece, pieces;  // rows of G, vocabulary of one piece
     int g_planes;
-    size_t g, h_slab, w_slab, total;
+    size_t g, g_parts, g_exponent, h_slab, w_slab, total;
     size_t d4;  // row length of the slabs
     uint32_t h_splits, w_splits;
 };
@@ -616,10 +748,14 @@ uint32_t splits_for(size_t tiles, size_t turns)
     return uint32_t(std::max<size_t>(1, std::min(kCus / std::max<size_t>(tiles, 1), turns / 4)));
 }
 
+// Planes of G for a gradient of the type: one, rounded to the 16 bits that the
+// gradient is rounded to as well, or two.
+int g_planes(int dtype) { return dtype == GC_F32 ? 2 : 1; }
+
 ProductShape grad_shape(int planes_a, int out_dtype)
 {
     ProductShape sh{};
-    set_pairs(sh, planes_a, g_planes(out_dtype), g_planes(out_dtype) - 1);
+    set_pairs(sh, planes_a, g_planes(out_dtype));
     return sh;
 }
 
@@ -627,15 +763,18 @@ GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, in
 {
     GradLayout L{};
     Carver c;
-    L.weight = plane_room(c, V, D, dtype);
+    L.mode = mode_of(dtype, dh_dtype == GC_F32 || dw_dtype == GC_F32);
+    L.weight = plane_room(c, V, D, L.mode);
     L.n_pad = round_up(N, kTurnK);
-    L.hidden = plane_room(c, L.n_pad, D, dtype);
+    L.hidden = plane_room(c, L.n_pad, D, L.mode);
     L.d4 = round_up(D, 4);
     L.g_planes = std::max(g_planes(dh_dtype), g_planes(dw_dtype));
     const size_t columns = kPieceBytes / (L.n_pad * 2 * L.g_planes) / kTile * kTile;
     L.piece = std::min(std::max<size_t>(columns, kTile), round_up(V, kTile));
     L.pieces = ceil_div(V, L.piece);
     L.g = c.take(L.g_planes * L.n_pad * L.piece * 2);
+    L.g_parts = c.take(kMaxParts * sizeof(float));
+    L.g_exponent = c.take(sizeof(int));
     const size_t ta = ceil_div(D, kTile);
     L.h_splits = splits_for(ceil_div(N, kTile) * ta,
                             L.piece / kTurnK * grad_shape(L.weight.planes, dh_dtype).segments);
@@ -646,18 +785,21 @@ GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, in
     return L;
 }
 
-// A product into `out` of type T (or into the slab, when there is one).
+// A product into `out` of type T.
 template <bool kBK, typename T>
-void launch_product(const MatOperand& A, const MatOperand& B, ProductShape sh, const ProductOut<T>& out,
+void launch_product(const MatOperand& A, const MatOperand& B, ProductShape sh, const ProductOut<T>& out, bool f16,
                     hipStream_t stream)
 {
-    hipLaunchKernelGGL((product_kernel<kBK, kTile, kTile, 2, 4, T>),
-                       dim3(sh.tiles_a * sh.tiles_b * sh.splits), dim3(8 * kWave), 0, stream, A, B, sh, out);
+    const dim3 grid(sh.tiles_a * sh.tiles_b * sh.splits), block(8 * kWave);
+    if (f16)
+        hipLaunchKernelGGL((product_kernel<true, kBK, kTile, kTile, 2, 4, T>), grid, block, 0, stream, A, B, sh, out);
+    else if constexpr (!std::is_same_v<T, f16_t>)
+        hipLaunchKernelGGL((product_kernel<false, kBK, kTile, kTile, 2, 4, T>), grid, block, 0, stream, A, B, sh, out);
 }
 
 template <bool kBK>
 void launch_product_any(const MatOperand& A, const MatOperand& B, const ProductShape& sh, void* out, int dtype,
-                        size_t nb, size_t D, hipStream_t stream)
+                        size_t nb, size_t D, bool f16, hipStream_t stream)
 {
     with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
@@ -667,7 +809,7 @@ void launch_product_any(const MatOperand& A, const MatOperand& B, const ProductS
         o.na = uint32_t(D);
         o.nb = uint32_t(nb);
         o.vec = D % 4 == 0 && aligned_to(out, 4 * sizeof(T));
-        launch_product<kBK, T>(A, B, sh, o, stream);
+        launch_product<kBK, T>(A, B, sh, o, f16, stream);
         return 0;
     });
 }
@@ -725,25 +867,29 @@ GCQ_API int linear_xent_loss(const void* hidden, const void* weight, int dtype, 
     if (!aligned16(ws) || *ws_bytes < L.total)
         return fail(GC_EINVAL, "linear_xent_loss: workspace too small or not 16-byte aligned");
     char* w = static_cast<char*>(ws);
-    const MatOperand wo = make_operand(weight, V, D, dtype, L.weight, w, !direct_ok(weight, D, dtype), nullptr,
-                                       0, 0, stream);
-    const MatOperand ho = make_operand(hidden, N, D, dtype, L.hidden, w, !direct_ok(hidden, D, dtype), nullptr,
-                                       0, 0, stream);
+    const MatOperand wo = make_operand(weight, V, D, dtype, L.mode, L.weight, w, nullptr, false, 0, V, stream);
+    const MatOperand ho = make_operand(hidden, N, D, dtype, L.mode, L.hidden, w, target, false, ignore_index, V, stream);
     ProductShape sh{};
     sh.turns = uint32_t(round_up(D, kTurnK) / kTurnK);
-    set_pairs(sh, L.weight.planes, L.hidden.planes, kFullLimit);
+    set_pairs(sh, L.weight.planes, L.hidden.planes);
     sh.tiles_a = uint32_t(ceil_div(V, L.cfg.ta));
     sh.tiles_b = uint32_t(ceil_div(N, L.cfg.tb));
     sh.splits = 1;
     LossPart* parts = reinterpret_cast<LossPart*>(w + L.parts);
     float* tl = reinterpret_cast<float*>(w + L.target_logit);
     const dim3 grid(sh.tiles_a * sh.tiles_b);
-    if (L.cfg.ta == 64)
-        hipLaunchKernelGGL((loss_tiles_kernel<64, 32, 2, 1>), grid, dim3(2 * kWave), 0, stream, wo, ho, sh,
-                           uint32_t(N), uint32_t(V), target, parts, uint32_t(L.nparts), tl);
+    const auto tiles = [&](auto kernel, int waves) {
+        hipLaunchKernelGGL(kernel, grid, dim3(waves * kWave), 0, stream, wo, ho, sh, uint32_t(N), uint32_t(V), target,
+                           parts, uint32_t(L.nparts), tl);
+    };
+    if (L.cfg.ta == 64 && L.mode.f16)
+        tiles(loss_tiles_kernel<true, 64, 32, 2, 1>, 2);
+    else if (L.cfg.ta == 64)
+        tiles(loss_tiles_kernel<false, 64, 32, 2, 1>, 2);
+    else if (L.mode.f16)
+        tiles(loss_tiles_kernel<true, 256, 256, 2, 4>, 8);
     else
-        hipLaunchKernelGGL((loss_tiles_kernel<256, 256, 2, 4>), grid, dim3(8 * kWave), 0, stream, wo, ho, sh,
-                           uint32_t(N), uint32_t(V), target, parts, uint32_t(L.nparts), tl);
+        tiles(loss_tiles_kernel<false, 256, 256, 2, 4>, 8);
     hipLaunchKernelGGL(loss_join_kernel, dim3(stride_grid(N, kJoinThreads / kWave)), dim3(kJoinThreads), 0,
                        stream, parts, uint32_t(L.nparts), tl, target, ignore_index, uint32_t(N), uint32_t(V),
                        loss, lse);
@@ -784,13 +930,19 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
         return GC_OK;
 
     char* w = static_cast<char*>(ws);
-    const MatOperand wo = make_operand(weight, V, D, dtype, L.weight, w, !direct_ok(weight, D, dtype), nullptr,
-                                       0, 0, stream);
+    const MatOperand wo = make_operand(weight, V, D, dtype, L.mode, L.weight, w, nullptr, false, 0, V, stream);
     // always a copy: rows without a target become zeros
-    const MatOperand ho = make_operand(hidden, N, D, dtype, L.hidden, w, true, target, ignore_index, V, stream);
+    const MatOperand ho = make_operand(hidden, N, D, dtype, L.mode, L.hidden, w, target, true, ignore_index, V, stream);
     GradOut g{};
     MatOperand go{};
-    go.plane0 = g.plane0 = reinterpret_cast<bf16_t*>(w + L.g);
+    if (L.mode.f16) {
+        float* parts = reinterpret_cast<float*>(w + L.g_parts);
+        int* exponent = reinterpret_cast<int*>(w + L.g_exponent);
+        launch_largest(dloss, N, 1, target, ignore_index, V, parts, stream);
+        hipLaunchKernelGGL(exponent_kernel, dim3(1), dim3(kRowThreads), 0, stream, parts, exponent);
+        go.exponent = g.exponent = exponent;
+    }
+    go.plane0 = g.plane0 = reinterpret_cast<uint16_t*>(w + L.g);
     go.plane_stride = g.plane_stride = L.n_pad * L.piece;
     go.ld = g.ld = uint32_t(L.piece);
     g.rows_out = uint32_t(L.n_pad);
@@ -805,7 +957,7 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
         wp.extent = uint32_t(vp);
         ProductShape sh{};
         sh.turns = uint32_t(round_up(D, kTurnK) / kTurnK);
-        set_pairs(sh, L.weight.planes, L.hidden.planes, kFullLimit);
+        set_pairs(sh, L.weight.planes, L.hidden.planes);
         sh.tiles_a = uint32_t(ceil_div(vp, kTile));
         sh.tiles_b = uint32_t(ceil_div(L.n_pad, kTile));
         sh.splits = 1;
@@ -814,12 +966,12 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
             hipLaunchKernelGGL(kernel, grid, block, 0, stream, wp, ho, sh, uint32_t(N), uint32_t(v0), uint32_t(V),
                                target, ignore_index, lse, dloss, g);
         };
-        if (L.g_planes == 1)
-            logits(logit_grad_kernel<kTile, kTile, 2, 4, 1>);
-        else if (L.g_planes == 2)
-            logits(logit_grad_kernel<kTile, kTile, 2, 4, 2>);
+        if (!L.mode.f16)
+            logits(logit_grad_kernel<false, kTile, kTile, 2, 4, 1>);
+        else if (L.g_planes == 1)
+            logits(logit_grad_kernel<true, kTile, kTile, 2, 4, 1>);
         else
-            logits(logit_grad_kernel<kTile, kTile, 2, 4, 3>);
+            logits(logit_grad_kernel<true, kTile, kTile, 2, 4, 2>);
         if (dhidden) {
             MatOperand A = wp, B = go;
             A.extent = uint32_t(wo.ld);
@@ -831,10 +983,10 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
             ps.tiles_b = uint32_t(ceil_div(N, kTile));
             ps.splits = L.h_splits;
             if (h_direct) {
-                launch_product_any<false>(A, B, ps, dhidden, dhidden_dtype, N, D, stream);
+                launch_product_any<false>(A, B, ps, dhidden, dhidden_dtype, N, D, L.mode.f16, stream);
             } else {
                 ProductOut<float> o{h_slab, L.d4, N * L.d4, uint32_t(L.d4), uint32_t(N), true, v0 > 0};
-                launch_product<false, float>(A, B, ps, o, stream);
+                launch_product<false, float>(A, B, ps, o, L.mode.f16, stream);
             }
         }
         if (dweight) {
@@ -849,10 +1001,10 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
             ps.splits = L.w_splits;
             char* out = static_cast<char*>(dweight) + v0 * D * dtype_bytes(dweight_dtype);
             if (L.w_splits == 1) {
-                launch_product_any<true>(A, B, ps, out, dweight_dtype, vp, D, stream);
+                launch_product_any<true>(A, B, ps, out, dweight_dtype, vp, D, L.mode.f16, stream);
             } else {
                 ProductOut<float> o{w_slab, L.d4, L.piece * L.d4, uint32_t(L.d4), uint32_t(vp), true, false};
-                launch_product<true, float>(A, B, ps, o, stream);
+                launch_product<true, float>(A, B, ps, o, L.mode.f16, stream);
                 launch_sum(w_slab, L.d4, L.piece * L.d4, L.w_splits, vp, D, out, dweight_dtype, stream);
             }
         }

@@ -1,7 +1,8 @@
-// mfma_product.h -- the tiled bf16 matrix product under linear_xent.hip.
+// mfma_product.h -- the tiled matrix product under linear_xent.hip.
 //
-// out[b][a] = sum over segments, sum over k of A(a, k) * B(b, k), fp32 sums in
-// the matrix cores. An operand is a matrix of bf16 in one of two layouts:
+// out[b][a] = sum over segments, sum over k of A(a, k) * B(b, k), 16-bit
+// factors, fp32 sums in the matrix cores. An operand is a matrix of bf16 or
+// fp16 in one of two layouts:
 //   by rows (kKRows = false): row a holds its k values contiguously;
 //   by k    (kKRows = true):  row k holds the values of all a contiguously.
 // The second is read out of LDS with the transposing load (ds_read_b64_tr_b16:
@@ -9,12 +10,14 @@
 // and lane i receives column i of the 4 rows), so that no operand is ever
 // transposed in memory.
 //
-// Precision: an operand of more than 8 significant bits is held as up to three
-// planes of bf16, x = p0 + p1 + p2, each the rounding of what the ones before
-// left (at most 2^-8 of it, so 2^-8, 2^-16 and 2^-24 of x after one, two and
-// three). A product then runs over segments, one for each pair (i, j) of
-// planes with i + j up to a limit: what a limit of 2 drops is 2^-24 of a term,
-// what a limit of 1 drops 2^-16.
+// Precision: an operand of more than 11 significant bits is held as two planes
+// of fp16, x = p0 + 2^-11 p1, p0 the rounding of x (off by at most 2^-11 of it)
+// and p1 that of the rest times 2^11: together they are within 2^-22 of x, as
+// long as x is within 2^-29 of the largest value (the caller scales that to
+// about 2^15), and within 2^-37 of the largest value below. A product then
+// runs over segments, one for each pair of planes: first those of one p1,
+// whose sum is then multiplied by 2^-11, then p0 p0. The pair of two p1, at
+// most 2^-22 of a term, is left out.
 //
 // A workgroup of WA x WB waves owns a tile of TA x TB outputs. k advances in
 // stages of 32 values of both operands, moved straight into LDS
@@ -32,8 +35,10 @@ namespace gcq {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStageK = 32;
 constexpr int kBuffers = 4;
@@ -42,31 +47,38 @@ constexpr int kBuffers = 4;
 constexpr int kTurnK = kBuffers * kStageK;
 
 struct MatOperand {
-    const bf16_t* plane0;
+    const uint16_t* plane0;
     size_t plane_stride;  // values from plane to plane
     uint32_t ld;          // values from row to row: a multiple of 8
     uint32_t extent;  // by rows: rows that may be read; by k: columns that may be read (a multiple of 8)
-    uint32_t krows;   // by k: rows that may be read (a last stage past them reads the last one again,
-                      // against zeros of the other operand)
+    uint32_t krows;   // by k: rows that may be read (what lies past them reads the last one again, against
+                      // zeros of the other operand)
+    const int* exponent;  // values are held times 2^exponent; NULL: 0
 };
 
 struct ProductShape {
     uint32_t turns;     // of one segment: ceil(k / 128)
-    uint32_t segments;  // pairs of planes: 1 .. 6
+    uint32_t segments;  // pairs of planes: 1 .. 3
     uint32_t pair_a, pair_b;  // the planes of segment s: two bits each, at bit 2 s
+    uint32_t fold;      // segments whose sum is multiplied by 2^-11: the first so many
     uint32_t tiles_a, tiles_b, splits;
 };
 
-// The pairs (i, j) of planes with i + j <= limit.
-inline void set_pairs(ProductShape& sh, int planes_a, int planes_b, int limit)
+// The pairs (0, 1), (1, 0), (0, 0) of planes, as far as they exist.
+inline void set_pairs(ProductShape& sh, int planes_a, int planes_b)
 {
     sh.segments = sh.pair_a = sh.pair_b = 0;
-    for (int i = 0; i < planes_a; ++i)
-        for (int j = 0; j < planes_b && i + j <= limit; ++j) {
-            sh.pair_a |= uint32_t(i) << (2 * sh.segments);
-            sh.pair_b |= uint32_t(j) << (2 * sh.segments);
-            ++sh.segments;
-        }
+    const auto add = [&](uint32_t i, uint32_t j) {
+        sh.pair_a |= i << (2 * sh.segments);
+        sh.pair_b |= j << (2 * sh.segments);
+        ++sh.segments;
+    };
+    if (planes_b == 2)
+        add(0, 1);
+    if (planes_a == 2)
+        add(1, 0);
+    sh.fold = sh.segments;
+    add(0, 0);
 }
 
 // What one lane and wave move of an operand's stage, T rows (or columns) wide.
@@ -108,17 +120,17 @@ struct StageLoader {
 
     // Where the stage from k0 on of plane p starts, as a descriptor of `bytes`
     // bytes: of none, its loads fetch nothing.
-    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage(const MatOperand& m, const bf16_t* p, uint32_t k0,
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage(const MatOperand& m, const uint16_t* p, uint32_t k0,
                                                                    uint32_t bytes)
     {
         // (by k: not past the last row)
-        const bf16_t* base = p + (kKRows ? size_t(min(k0, m.krows - 1)) * m.ld : size_t(k0));
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16_t*>(base), 0, bytes, 0x00020000);
+        const uint16_t* base = p + (kKRows ? size_t(min(k0, m.krows - 1)) * m.ld : size_t(k0));
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, bytes, 0x00020000);
     }
 
     // Enqueues load j of the stage into lds.
     __device__ __forceinline__ void load(const MatOperand& m, __amdgpu_buffer_rsrc_t at, uint32_t k0, int j,
-                                         bf16_t* lds) const
+                                         uint16_t* lds) const
     {
         // by k: the last row of the stage that may be read; rows of a stage
         // and the bytes of a row fit 24 bits
@@ -149,7 +161,7 @@ struct FragmentReader {
     }
 
     // Fragment f (32 f rows on), k values 16 kk on.
-    __device__ __forceinline__ bf16x8 read(const bf16_t* lds, int f, int kk) const
+    __device__ __forceinline__ s16x8 read(const uint16_t* lds, int f, int kk) const
     {
         if (kKRows) {
             typedef __attribute__((address_space(3))) s16x4* lds_ptr;
@@ -157,31 +169,32 @@ struct FragmentReader {
             const char* p = reinterpret_cast<const char*>(lds) + (base ^ (uint32_t(f) << 6)) + kk * 16 * (2 * T);
             union {
                 s16x4 h[2];
-                bf16x8 v;
+                s16x8 v;
             } u;
             u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p));
             u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * (2 * T)));
             return u.v;
         }
         const char* p = reinterpret_cast<const char*>(lds) + (base ^ (uint32_t(kk) << 5)) + f * (32 * 2 * kStageK);
-        return *reinterpret_cast<const bf16x8*>(p);
+        return *reinterpret_cast<const s16x8*>(p);
     }
 };
 
 // The LDS of a tile, as variables of their own, so that the compiler knows
 // which loads a fragment read has to wait for.
 struct TileBuffers {
-    bf16_t *a[kBuffers], *b[kBuffers];
+    uint16_t *a[kBuffers], *b[kBuffers];
 };
 
 #define GCQ_TILE_BUFFERS(name, TA, TB)                                                                       \
-    __shared__ bf16_t name##_a0[(TA) * kStageK], name##_a1[(TA) * kStageK], name##_a2[(TA) * kStageK],       \
+    __shared__ uint16_t name##_a0[(TA) * kStageK], name##_a1[(TA) * kStageK], name##_a2[(TA) * kStageK],       \
         name##_a3[(TA) * kStageK], name##_b0[(TB) * kStageK], name##_b1[(TB) * kStageK],                     \
         name##_b2[(TB) * kStageK], name##_b3[(TB) * kStageK];                                                \
     const TileBuffers name = {{name##_a0, name##_a1, name##_a2, name##_a3},                                  \
                               {name##_b0, name##_b1, name##_b2, name##_b3}}
 
-template <bool kAK, bool kBK, int TA, int TB, int WA, int WB>
+// kF16: fp16 operands, else bf16.
+template <bool kF16, bool kAK, bool kBK, int TA, int TB, int WA, int WB>
 struct TileProduct {
     static constexpr int kWaves = WA * WB;
     static constexpr int RA = TA / WA / 32, RB = TB / WB / 32;  // 32 x 32 products of a wave
@@ -255,7 +268,7 @@ struct TileProduct {
                 load(f, j, s);
         }
         wait_loads<2 * kLoads>();
-        bf16x8 a[2][RA], b[2][RB];
+        s16x8 a[2][RA], b[2][RB];
 #pragma unroll
         for (int j = 0; j < RB; ++j)
             b[0][j] = fb.read(lds.b[0], j, 0);
@@ -263,7 +276,10 @@ struct TileProduct {
         for (int i = 0; i < RA; ++i)
             a[0][i] = fa.read(lds.a[0], i, 0);
 
+        const uint32_t fold = sh.fold * sh.turns;
         for (uint32_t t = t0; t < t1; ++t) {
+            if (t == fold && t > t0)
+                scale(acc);
 #pragma unroll
             for (int s = 0; s < kBuffers; ++s) {
                 // behind the barrier stage s + 1 is in LDS for everybody, and
@@ -288,15 +304,36 @@ struct TileProduct {
                         if (i < RA) {
 #pragma unroll
                             for (int j = 0; j < RB; ++j)
-                                acc.v[i][j] =
-                                    __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[kk][i], b[kk][j], acc.v[i][j], 0, 0, 0);
+                                acc.v[i][j] = multiply(a[kk][i], b[kk][j], acc.v[i][j]);
                         }
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
         }
+        if (t1 <= fold)
+            scale(acc);
         wait_loads<0>();
+    }
+
+    static __device__ __forceinline__ f32x16 multiply(s16x8 a, s16x8 b, f32x16 c)
+    {
+        if constexpr (kF16)
+            return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b),
+                                                          c, 0, 0, 0);
+        else
+            return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                           __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+
+    // The sum of the segments of a second plane, in the first one's units.
+    static __device__ __forceinline__ void scale(Acc& acc)
+    {
+#pragma unroll
+        for (int i = 0; i < RA; ++i)
+#pragma unroll
+            for (int j = 0; j < RB; ++j)
+                acc.v[i][j] *= 0x1p-11f;
     }
 
     // Waits until all but the last N loads of this wave are in LDS, then for

@@ -387,12 +387,13 @@ int norm_residual_grad(const void* z, const void* y, int dtype, size_t rows, siz
  *   loss[n] = lse[n] - l_n,target[n];  0 where target[n] == ignore_index; NaN
  *             where target[n] is neither that nor a row of the vocabulary
  * The logits are never kept: tiles of the product end in a running maximum
- * and sum of their part of the vocabulary. bf16 inputs are multiplied as they
- * are; fp16 and fp32 ones as two and three bf16 planes, which hold an fp16
- * value exactly and an fp32 value to 2^-24 (four and six products). Sums are
- * fp32.
+ * and sum of their part of the vocabulary. bf16 and fp16 inputs are
+ * multiplied as they are; an fp32 value x as two fp16 values that hold it to
+ * 2^-22 of x or 2^-37 of the largest finite one of its matrix (of hidden: of
+ * the rows that have a target), whichever is more. Sums are fp32.
  *   hidden  [N, D], weight [V, D] of `dtype`, rows contiguous
- *   target  [N] int64;  loss, lse [N] fp32 (lse is written for every row)
+ *   target  [N] int64;  loss, lse [N] fp32 (lse is written for every row; of
+ *           fp32 inputs only rows that have a target get one to rely on)
  *   ws      16-byte-aligned workspace; ws == NULL: *ws_bytes is set to the
  *           size needed for (N, V, D, dtype) and nothing is enqueued.
  *           Otherwise *ws_bytes is its size and must be at least that.
@@ -413,8 +414,10 @@ int linear_xent_loss(const void* hidden, const void* weight, int dtype, size_t N
  *   dhidden     [N, D] of dhidden_dtype, or NULL: not computed
  *   dweight     [V, D] of dweight_dtype, or NULL: not computed
  *   a gradient's type is the inputs' or fp32, and says how exactly it is
- *   computed: for a bf16 gradient G is rounded to bf16 on its way into the
- *   product, for an fp16 one to 16, for an fp32 one to 24 bits. An fp32
+ *   computed. G is rounded to the 16 bits of a gradient of 16 bits on its way
+ *   into the product; for an fp32 one it is held to 2^-22 of itself or 2^-37
+ *   of the largest |dloss|, whichever is more, and inputs of fp32 as in
+ *   linear_xent_loss (bf16 ones are exact to 2^-39 of their largest). An fp32
  *   dweight is what compress_2bit and qsgd_maxnorm_quantize take.
  *   ws          as in linear_xent_loss. The query asks by the types alone.
  * N may be 0: dweight is then zero. */

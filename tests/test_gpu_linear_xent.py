@@ -1,15 +1,18 @@
 """linear_xent_loss and linear_xent_grad against the formulas in 64 bits.
 
-Tolerances. A plane of bf16 leaves at most half a step, 2^-8 of what it
-rounds: k planes leave 2^-8k. A logit is a sum of D products in fp32 sums: at
-most (D + 2) fp32 half steps of the terms' magnitudes; bf16 and fp16 factors
-are exact, of fp32 ones the products drop at most 4 * 2^-24 of each term (two
-planes' rests, and the pairs (1, 2) and (2, 1)). lse and loss follow, plus the
+Tolerances. A logit is a sum of D products in fp32 sums: at most (D + 2) fp32
+half steps of the terms' magnitudes. bf16 and fp16 factors are exact; an fp32
+one is two fp16 planes, the second scaled by 2^11: each rounding leaves 2^-11,
+so 2^-22 of the value is left of each factor and the left-out pair of second
+planes is 2^-22 of the term, 3 * 2^-22 together. lse and loss follow, plus the
 sums' own steps. A gradient is a sum of products whose factor G is off by the
-logit's error and exp's steps times p, plus the rounding of G to the planes of
-the gradient's type; products of several planes drop pairs beyond the limit
-(2^-16 for fp16: two such pairs and the rest of a plane; 2^-24 for fp32); then
-the fp32 sums, and one rounding to the gradient's type."""
+logit's error and exp's steps times p, plus the rounding of G: 2^-8 (bf16 all
+through), 2^-11 (any other gradient of 16 bits) or 2^-22 (fp32); the other
+factor is exact, or two planes for fp32 inputs (3 * 2^-22 of a term with G's
+own); then the fp32 sums, and one rounding to the gradient's type. Values far
+below the largest of a matrix: planes of G stop at 2^-24-11 of their units,
+2^-49 where the largest is 2^14 or more, one plane at 2^-24 of them, 2^-38;
+inputs scaled the same way, of two planes at 2^-49, of bf16 at 2^-38."""
 import math
 
 import pytest
@@ -23,7 +26,6 @@ gu = pytest.importorskip("gpu_util")
 
 TYPES = [torch.float32, torch.bfloat16, torch.float16]
 IGNORE = -100
-PLANES = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
 
 
 def inputs(N, V, D, t, seed=0, ignore=0.2, scale=2.0):
@@ -41,8 +43,9 @@ def logits64(h, w):
     l = h.double() @ w.double().t()
     D = h.shape[1]
     mag = h.double().abs() @ w.double().abs().t()
-    each = (D + 2) * po.F32 + (4.1 * po.F32 if h.dtype == torch.float32 else 0.0)
-    return l, mag.max(dim=1).values * each
+    each = (D + 2) * po.F32 + (3.1 * 2.0 ** -22 if h.dtype == torch.float32 else 0.0)
+    floor = 2.0 ** -36 * D * float(h.abs().max()) * float(w.abs().max())
+    return l, mag.max(dim=1).values * each + floor
 
 
 def plain_loss(h, w, y):
@@ -85,7 +88,7 @@ def test_loss(gcq, size, t):
     check_loss(*run_loss(gcq, h, w, y), ref, ref_lse, e)
 
 
-def plain_grad(h, w, y, lse, d, out):
+def plain_grad(h, w, y, lse, d, out, other):
     """Gradients in 64 bits, and bounds of their errors before the outputs'
     own rounding."""
     l, e = logits64(h, w)
@@ -98,14 +101,21 @@ def plain_grad(h, w, y, lse, d, out):
     ad = torch.where(has, d.double().abs(), 0.0)[:, None]
     # G: the logit's error and exp's own steps times p, one step of p - 1, the
     # planes' rounding of the whole
-    eg = ad * p * (e[:, None] + 16 * po.F32) + g.abs() * 2.0 ** -(8 * PLANES[out]) + ad * 2 * po.F32
-    ah, aw = h.double().abs(), w.double().abs()
-    drop = 0.0 if h.dtype == torch.bfloat16 else 4.1 * 2.0 ** -(8 * PLANES[out])
+    top = float(ad.max())
+    if out == torch.float32:
+        rounding = g.abs() * 2.0 ** -22 + top * 2.0 ** -36
+    elif h.dtype == out == other == torch.bfloat16:
+        rounding = g.abs() * 2.0 ** -8
+    else:
+        rounding = g.abs() * 2.0 ** -11 + top * 2.0 ** -38
+    eg = ad * p * (e[:, None] + 16 * po.F32) + rounding + ad * 2 * po.F32
+    drop = 3.1 * 2.0 ** -22 if h.dtype == torch.float32 else 0.0
 
     def product(a, ea, b, k):
         # k terms summed in fp32, operands in planes
         mag = a.abs() @ b.abs()
-        return a @ b, ea @ b.abs() + mag * ((k + 2) * po.F32 + drop)
+        floor = 2.0 ** -38 * float(b.abs().max()) * a.abs().sum(1, keepdim=True)
+        return a @ b, ea @ b.abs() + mag * ((k + 2) * po.F32 + drop) + floor
     hz = torch.where(has[:, None], h.double(), 0.0)
     return product(g, eg, w.double(), w.shape[0]) + product(g.t(), eg.t(), hz, h.shape[0])
 
@@ -140,8 +150,8 @@ def test_grad(gcq, size, types):
     h, w, y, d = inputs(*size, t, seed=sum(size) + 1)
     lse = plain_loss(h, w, y)[1].float()
     dh, dw = run_grad(gcq, h, w, y, lse, d, th, tw)
-    rh, eh, _, _ = plain_grad(h, w, y, lse, d, th)
-    _, _, rw, ew = plain_grad(h, w, y, lse, d, tw)
+    rh, eh, _, _ = plain_grad(h, w, y, lse, d, th, tw)
+    _, _, rw, ew = plain_grad(h, w, y, lse, d, tw, th)
     check_grad(dh, rh, eh)
     check_grad(dw, rw, ew)
 
@@ -150,8 +160,11 @@ def test_grad_alone_of_each(gcq):
     announce("linear_xent_grad of one operand")
     h, w, y, d = inputs(70, 500, 96, torch.bfloat16)
     lse = plain_loss(h, w, y)[1].float()
-    both = run_grad(gcq, h, w, y, lse, d, torch.bfloat16, torch.float32)
-    dh, none = run_grad(gcq, h, w, y, lse, d, torch.bfloat16, torch.float32, skip="w")
-    assert none is None and torch.equal(dh, both[0])
-    none, dw = run_grad(gcq, h, w, y, lse, d, torch.bfloat16, torch.float32, skip="h")
-    assert none is None and torch.equal(dw, both[1])
+    # a gradient left out counts as one of the inputs' type
+    for tw in (torch.bfloat16, torch.float32):
+        both = run_grad(gcq, h, w, y, lse, d, torch.bfloat16, tw)
+        if tw == torch.bfloat16:
+            dh, none = run_grad(gcq, h, w, y, lse, d, torch.bfloat16, tw, skip="w")
+            assert none is None and torch.equal(dh, both[0])
+        none, dw = run_grad(gcq, h, w, y, lse, d, torch.bfloat16, tw, skip="h")
+        assert none is None and torch.equal(dw, both[1])
