@@ -533,28 +533,40 @@ def grandk_mn_step(grads: Sequence, K: int, seed: int, s: int, idx, dense, ws, s
 
 # ---- training operators -------------------------------------------------------
 
-_dtypes = None
+_dtypes = {}
 
 
 def _dtype(t, what: str) -> int:
     """gc_dtype of a tensor of activations."""
-    global _dtypes
-    if _dtypes is None:
-        torch = _torch()
-        _dtypes = {torch.float32: GC_F32, torch.bfloat16: GC_BF16, torch.float16: GC_F16}
     code = _dtypes.get(t.dtype)
+    if code is None:
+        torch = _torch()
+        _dtypes.update({torch.float32: GC_F32, torch.bfloat16: GC_BF16, torch.float16: GC_F16})
+        code = _dtypes.get(t.dtype)
     if code is None:
         raise TypeError(f"{what}: expected float32, bfloat16 or float16, got {t.dtype}")
     return code
 
 
-def _step(step) -> ctypes.c_void_p:
+def _at(t, dtype, what: str, cur):
+    """Device address of a tensor (see _ptr), or None of None."""
+    return None if t is None else _ptr(t, dtype, what, cur)
+
+
+def _ws(ws, what: str):
+    """The size of a workspace; one of no bytes would read as a query."""
+    if ws.numel() == 0:
+        raise ValueError(f"{what}: ws too small")
+    return _sz(ws.numel())
+
+
+def _step(step, cur):
     """A device counter added to the seed: an int64 tensor of one element."""
     if step is None:
-        return _vp(None)
+        return None
     if step.numel() != 1:
         raise ValueError("step must hold one element")
-    return _dev(step, _torch().int64, "step")
+    return _ptr(step, _torch().int64, "step", cur)
 
 
 def _u64(v: int) -> int:
@@ -580,9 +592,10 @@ def dropout(x, p: float, seed: int, worker: int, out, residual=None, offset: int
     n = x.numel()
     if out.numel() != n or (residual is not None and residual.numel() != n):
         raise ValueError("dropout: x, out and residual differ in size")
-    _check(load().dropout(_dev(x, x.dtype, "x"), _dev(residual, x.dtype, "residual"), n,
+    cur = _current_device()
+    _check(load().dropout(_at(x, x.dtype, "x", cur), _at(residual, x.dtype, "residual", cur), n,
                           _dtype(x, "x"), float(p), _u64(seed), _worker(worker), _offset(offset),
-                          _step(step), _dev(out, x.dtype, "out"), _stream(stream)))
+                          _step(step, cur), _at(out, x.dtype, "out", cur), _stream(stream)))
 
 
 def dropout_backward(grad_out, p: float, seed: int, worker: int, grad_in, offset: int = 0,
@@ -590,10 +603,11 @@ def dropout_backward(grad_out, p: float, seed: int, worker: int, grad_in, offset
     n = grad_out.numel()
     if grad_in.numel() != n:
         raise ValueError("dropout_backward: grad_out and grad_in differ in size")
-    _check(load().dropout_backward(_dev(grad_out, grad_out.dtype, "grad_out"), n,
+    cur = _current_device()
+    _check(load().dropout_backward(_at(grad_out, grad_out.dtype, "grad_out", cur), n,
                                    _dtype(grad_out, "grad_out"), float(p), _u64(seed),
-                                   _worker(worker), _offset(offset), _step(step),
-                                   _dev(grad_in, grad_out.dtype, "grad_in"), _stream(stream)))
+                                   _worker(worker), _offset(offset), _step(step, cur),
+                                   _at(grad_in, grad_out.dtype, "grad_in", cur), _stream(stream)))
 
 
 def _norm_shape(y, what: str, same, gate, columns, per_row):
@@ -627,12 +641,13 @@ def norm_residual(x, y, z, h=None, post_gain=None, gate=None, pre_gain=None,
     rows, d, gates = _norm_shape(y, "norm_residual", (x, z, h), gate, (post_gain, pre_gain),
                                  (rstd_post, rstd_pre))
     f32 = torch.float32
+    cur = _current_device()
     _check(load().norm_residual(
-        _dev(x, y.dtype, "x"), _dev(y, y.dtype, "y"), _dtype(y, "y"), rows, d,
-        _dev(post_gain, f32, "post_gain"), _dev(gate, f32, "gate"), gates,
-        _dev(pre_gain, f32, "pre_gain"), float(residual_scale), float(eps), float(p), _u64(seed),
-        _worker(worker), _step(step), _dev(z, y.dtype, "z"), _dev(h, y.dtype, "h"),
-        _dev(rstd_post, f32, "rstd_post"), _dev(rstd_pre, f32, "rstd_pre"), _stream(stream)))
+        _at(x, y.dtype, "x", cur), _at(y, y.dtype, "y", cur), _dtype(y, "y"), rows, d,
+        _at(post_gain, f32, "post_gain", cur), _at(gate, f32, "gate", cur), gates,
+        _at(pre_gain, f32, "pre_gain", cur), float(residual_scale), float(eps), float(p), _u64(seed),
+        _worker(worker), _step(step, cur), _at(z, y.dtype, "z", cur), _at(h, y.dtype, "h", cur),
+        _at(rstd_post, f32, "rstd_post", cur), _at(rstd_pre, f32, "rstd_pre", cur), _stream(stream)))
 
 
 def norm_residual_grad_ws_bytes(rows: int, d: int, gates: int = 1) -> int:
@@ -657,15 +672,16 @@ def norm_residual_grad(z, y, dx, dy, ws, dz=None, dh=None, post_gain=None, gate=
     if dgate is not None and (gate is None or dgate.numel() != gate.numel()):
         raise ValueError("norm_residual_grad: dgate differs from gate in size")
     f32 = torch.float32
-    size = _sz(ws.numel())
+    size = _ws(ws, "norm_residual_grad")
+    cur = _current_device()
     _check(load().norm_residual_grad(
-        _dev(z, y.dtype, "z"), _dev(y, y.dtype, "y"), _dtype(y, "y"), rows, d,
-        _dev(post_gain, f32, "post_gain"), _dev(gate, f32, "gate"), gates,
-        _dev(pre_gain, f32, "pre_gain"), float(residual_scale), float(p), _u64(seed),
-        _worker(worker), _step(step), _dev(rstd_post, f32, "rstd_post"),
-        _dev(rstd_pre, f32, "rstd_pre"), _dev(dz, y.dtype, "dz"), _dev(dh, y.dtype, "dh"),
-        _dev(dx, y.dtype, "dx"), _dev(dy, y.dtype, "dy"), _dev(dpost_gain, f32, "dpost_gain"),
-        _dev(dgate, f32, "dgate"), _dev(dpre_gain, f32, "dpre_gain"), _dev(ws, torch.uint8, "ws"),
+        _at(z, y.dtype, "z", cur), _at(y, y.dtype, "y", cur), _dtype(y, "y"), rows, d,
+        _at(post_gain, f32, "post_gain", cur), _at(gate, f32, "gate", cur), gates,
+        _at(pre_gain, f32, "pre_gain", cur), float(residual_scale), float(p), _u64(seed),
+        _worker(worker), _step(step, cur), _at(rstd_post, f32, "rstd_post", cur),
+        _at(rstd_pre, f32, "rstd_pre", cur), _at(dz, y.dtype, "dz", cur), _at(dh, y.dtype, "dh", cur),
+        _at(dx, y.dtype, "dx", cur), _at(dy, y.dtype, "dy", cur), _at(dpost_gain, f32, "dpost_gain", cur),
+        _at(dgate, f32, "dgate", cur), _at(dpre_gain, f32, "dpre_gain", cur), _at(ws, torch.uint8, "ws", cur),
         ctypes.byref(size), _stream(stream)))
 
 
@@ -715,12 +731,13 @@ def linear_xent_loss(hidden, weight, target, loss, lse, ws, ignore_index: int = 
     N, V, D = _xent_sizes(hidden, weight, "linear_xent_loss")
     if target.numel() != N or loss.numel() != N or lse.numel() != N:
         raise ValueError("linear_xent_loss: target, loss and lse must hold one value a token")
-    size = _sz(ws.numel())
+    size = _ws(ws, "linear_xent_loss")
+    cur = _current_device()
     _check(load().linear_xent_loss(
-        _dev(hidden, hidden.dtype, "hidden"), _dev(weight, hidden.dtype, "weight"),
-        _dtype(hidden, "hidden"), N, V, D, _dev(target, torch.int64, "target"), int(ignore_index),
-        _dev(loss, torch.float32, "loss"), _dev(lse, torch.float32, "lse"),
-        _dev(ws, torch.uint8, "ws"), ctypes.byref(size), _stream(stream)))
+        _at(hidden, hidden.dtype, "hidden", cur), _at(weight, hidden.dtype, "weight", cur),
+        _dtype(hidden, "hidden"), N, V, D, _at(target, torch.int64, "target", cur), int(ignore_index),
+        _at(loss, torch.float32, "loss", cur), _at(lse, torch.float32, "lse", cur),
+        _at(ws, torch.uint8, "ws", cur), ctypes.byref(size), _stream(stream)))
 
 
 def linear_xent_grad(hidden, weight, target, lse, dloss, dhidden, dweight, ws,
@@ -740,11 +757,12 @@ def linear_xent_grad(hidden, weight, target, lse, dloss, dhidden, dweight, ws,
     code = _dtype(hidden, "hidden")
     h_code = code if dhidden is None else _dtype(dhidden, "dhidden")
     w_code = code if dweight is None else _dtype(dweight, "dweight")
-    size = _sz(ws.numel())
+    size = _ws(ws, "linear_xent_grad")
+    cur = _current_device()
     _check(load().linear_xent_grad(
-        _dev(hidden, hidden.dtype, "hidden"), _dev(weight, hidden.dtype, "weight"), code, N, V, D,
-        _dev(target, torch.int64, "target"), int(ignore_index), _dev(lse, torch.float32, "lse"),
-        _dev(dloss, torch.float32, "dloss"),
-        _dev(dhidden, None if dhidden is None else dhidden.dtype, "dhidden"), h_code,
-        _dev(dweight, None if dweight is None else dweight.dtype, "dweight"), w_code,
-        _dev(ws, torch.uint8, "ws"), ctypes.byref(size), _stream(stream)))
+        _at(hidden, hidden.dtype, "hidden", cur), _at(weight, hidden.dtype, "weight", cur), code, N, V, D,
+        _at(target, torch.int64, "target", cur), int(ignore_index), _at(lse, torch.float32, "lse", cur),
+        _at(dloss, torch.float32, "dloss", cur),
+        _at(dhidden, None if dhidden is None else dhidden.dtype, "dhidden", cur), h_code,
+        _at(dweight, None if dweight is None else dweight.dtype, "dweight", cur), w_code,
+        _at(ws, torch.uint8, "ws", cur), ctypes.byref(size), _stream(stream)))

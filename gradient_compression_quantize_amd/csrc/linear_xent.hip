@@ -692,9 +692,16 @@ struct LossConfig {
     int ta, tb, wa;
 };
 
+// Tiles of 256 x 256 read the least and need some rounds of 256 of them; few
+// tokens take smaller ones, which fill the chip with tiles of the vocabulary
+// alone and leave less of a tile empty. V = 30522, D = 768, us:
+//   tokens        1     32     64    128    256    512
+//   128 x 64   14.5   16.5   16.2
+//   128 x 128                19.4   19.1   25.6   39.8
+//   256 x 256  24.7   25.1   21.6   21.0   27.2   31.1
 LossConfig loss_config(size_t N)
 {
-    return N <= 32 ? LossConfig{64, 32, 2} : LossConfig{256, 256, 2};
+    return N <= 64 ? LossConfig{128, 64, 2} : N <= 256 ? LossConfig{128, 128, 2} : LossConfig{256, 256, 2};
 }
 
 struct LossLayout {
@@ -741,8 +748,11 @@ struct GradLayout {
     uint32_t h_splits, w_splits;
 };
 
-// Splits of a product of `tiles` tiles over `turns` turns: enough to give
-// every compute unit a tile, at least 4 turns each.
+// Splits of a product of `tiles` tiles over `turns` turns: as many as find a
+// compute unit each, at least 4 turns long. Filling several rounds of 256
+// tiles with more of them cost more in partial results than it gave: 8192 x
+// 30522 x 768 with an fp32 gradient (192 tiles of 128 turns into 16384 x 768)
+// took 1974 us with 4 splits, 1884 with 1.
 uint32_t splits_for(size_t tiles, size_t turns)
 {
     return uint32_t(std::max<size_t>(1, std::min(kCus / std::max<size_t>(tiles, 1), turns / 4)));
@@ -778,7 +788,8 @@ GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, in
     const size_t ta = ceil_div(D, kTile);
     L.h_splits = splits_for(ceil_div(N, kTile) * ta,
                             L.piece / kTurnK * grad_shape(L.weight.planes, dh_dtype).segments);
-    L.w_splits = splits_for(L.piece / kTile * ta, L.n_pad / kTurnK * grad_shape(L.hidden.planes, dw_dtype).segments);
+    L.w_splits = splits_for(L.piece / kTile * ta,
+                            L.n_pad / kTurnK * grad_shape(L.hidden.planes, dw_dtype).segments);
     L.h_slab = c.take(L.h_splits > 1 || L.pieces > 1 ? L.h_splits * N * L.d4 * 4 : 0);
     L.w_slab = c.take(L.w_splits > 1 ? L.w_splits * L.piece * L.d4 * 4 : 0);
     L.total = c.used;
@@ -882,14 +893,19 @@ GCQ_API int linear_xent_loss(const void* hidden, const void* weight, int dtype, 
         hipLaunchKernelGGL(kernel, grid, dim3(waves * kWave), 0, stream, wo, ho, sh, uint32_t(N), uint32_t(V), target,
                            parts, uint32_t(L.nparts), tl);
     };
-    if (L.cfg.ta == 64 && L.mode.f16)
-        tiles(loss_tiles_kernel<true, 64, 32, 2, 1>, 2);
-    else if (L.cfg.ta == 64)
-        tiles(loss_tiles_kernel<false, 64, 32, 2, 1>, 2);
-    else if (L.mode.f16)
-        tiles(loss_tiles_kernel<true, 256, 256, 2, 4>, 8);
+    const auto either = [&](auto f16) {
+        constexpr bool kF16 = decltype(f16)::value;
+        if (L.cfg.tb == 64)
+            tiles(loss_tiles_kernel<kF16, 128, 64, 2, 2>, 4);
+        else if (L.cfg.tb == 128)
+            tiles(loss_tiles_kernel<kF16, 128, 128, 2, 2>, 4);
+        else
+            tiles(loss_tiles_kernel<kF16, 256, 256, 2, 4>, 8);
+    };
+    if (L.mode.f16)
+        either(std::true_type());
     else
-        tiles(loss_tiles_kernel<false, 256, 256, 2, 4>, 8);
+        either(std::false_type());
     hipLaunchKernelGGL(loss_join_kernel, dim3(stride_grid(N, kJoinThreads / kWave)), dim3(kJoinThreads), 0,
                        stream, parts, uint32_t(L.nparts), tl, target, ignore_index, uint32_t(N), uint32_t(V),
                        loss, lse);
@@ -909,7 +925,8 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
     if (!ws_bytes)
         return fail(GC_EINVAL, "linear_xent_grad: ws_bytes is NULL");
     if (!ws) {
-        *ws_bytes = N ? grad_layout(N, V, D, dtype, dhidden_dtype, dweight_dtype).total : 0;
+        // (of no tokens too: a workspace of no bytes would ask again)
+        *ws_bytes = grad_layout(std::max<size_t>(N, 1), V, D, dtype, dhidden_dtype, dweight_dtype).total;
         return GC_OK;
     }
     const size_t b = dtype_bytes(dtype);

@@ -711,7 +711,7 @@ GCQ_API int norm_residual_grad(const void* z, const void* y, int dtype, size_t r
         return fail(GC_EINVAL, "norm_residual_grad: ws_bytes is NULL");
     const GradRoom room = grad_room(rows, d, gates);
     if (!ws) {
-        *ws_bytes = room.total;
+        *ws_bytes = std::max<size_t>(room.total, 256);
         return GC_OK;
     }
     const size_t b = dtype_bytes(dtype);

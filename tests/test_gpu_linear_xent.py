@@ -168,3 +168,260 @@ def test_grad_alone_of_each(gcq):
             assert none is None and torch.equal(dh, both[0])
         none, dw = run_grad(gcq, h, w, y, lse, d, torch.bfloat16, tw, skip="h")
         assert none is None and torch.equal(dw, both[1])
+
+
+def test_no_tokens_and_no_targets(gcq):
+    announce("linear_xent of no tokens, and of none with a target")
+    w = torch.randn(40, 24, device=gu.DEV)
+    e = torch.empty(0, 24, device=gu.DEV)
+    per, none = torch.empty(0, device=gu.DEV), torch.empty(0, dtype=torch.int64, device=gu.DEV)
+    ws = torch.empty(gcq.linear_xent_grad_ws_bytes(0, 40, 24, w.dtype), dtype=torch.uint8, device=gu.DEV)
+    dw = torch.full_like(w, 5.0)
+    gcq.linear_xent_loss(e, w, none, per, per.clone(), ws)
+    gcq.linear_xent_grad(e, w, none, per, per, e.clone(), dw, ws)
+    gu.sync()
+    assert bool((dw == 0).all())
+    with pytest.raises(ValueError, match="ws too small"):
+        gcq.linear_xent_grad(e, w, none, per, per, e.clone(), dw, torch.empty(0, dtype=torch.uint8, device=gu.DEV))
+    for t in TYPES:
+        h, w, y, d = inputs(37, 130, 65, t)
+        y[:] = IGNORE
+        loss, lse = run_loss(gcq, h, w, y)
+        assert bool((loss == 0).all())
+        dh, dw = run_grad(gcq, h, w, y, lse, d, torch.float32, t)
+        assert bool((dh == 0).all()) and bool((dw == 0).all())
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+def test_rows_without_a_target_reach_nothing(gcq, t):
+    """NaN, infinities and huge values in the hidden states, lse and dloss of
+    padded rows; targets outside the vocabulary; an ignore_index inside it."""
+    announce(f"linear_xent padded rows {t}")
+    h, w, y, d = inputs(300, 513, 130, t, ignore=0.0)
+    pad = torch.arange(300) % 3 == 1
+    out = torch.arange(300) % 7 == 2
+    clean_y = torch.where(pad | out, IGNORE, y)
+    lse = plain_loss(h, w, y)[1].float()
+    want_loss = run_loss(gcq, h, w, clean_y)[0]
+    want = run_grad(gcq, h, w, clean_y, lse, d, t, torch.float32)
+    bad_h, bad_y, bad_lse, bad_d = h.clone(), y.clone(), lse.clone(), d.clone()
+    big = torch.finfo(t).max
+    for k, v in enumerate((float("nan"), float("inf"), -float("inf"), big)):
+        rows = (pad | out).nonzero()[k::4, 0]
+        bad_h[rows] = v
+        bad_lse[rows] = v
+        bad_d[rows] = v
+    bad_y[pad] = IGNORE
+    bad_y[out] = torch.tensor([513, -1, 2 ** 40, -2 ** 62, 514])[torch.arange(int(out.sum())) % 5]
+    bad_y[pad & out] = IGNORE
+    loss, _ = run_loss(gcq, bad_h, w, bad_y)
+    off = out & ~pad
+    assert bool(torch.isnan(loss[off]).all()) and torch.equal(loss[~off], want_loss[~off])
+    got = run_grad(gcq, bad_h, w, bad_y, bad_lse, bad_d, t, torch.float32)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # an ignore_index that is a row of the vocabulary
+    y7 = torch.where(pad, 7, torch.where(y == 7, 8, y))
+    loss7, _ = run_loss(gcq, h, w, y7, ignore=7)
+    ref, ref_lse, e = plain_loss(h, w, torch.where(pad, IGNORE, y7))
+    assert bool((loss7[pad] == 0).all())
+    assert bool(((loss7.double() - ref).abs() <= 2 * e + 200 * po.F32 * (1 + ref_lse.abs()))[~pad].all())
+
+
+def test_confident_and_extreme_logits(gcq):
+    """Targets of probability near 1 and logits of some hundreds: the sums of
+    exponentials neither overflow nor vanish."""
+    announce("linear_xent extreme logits")
+    for t in TYPES:
+        h, w, y, d = inputs(64, 400, 128, t, ignore=0.0, scale=40.0)
+        ref, ref_lse, e = plain_loss(h, w, y)
+        assert float(ref_lse.max()) > 80
+        check_loss(*run_loss(gcq, h, w, y), ref, ref_lse, e)
+        y = (h.double() @ w.double().t()).argmax(dim=1)
+        ref, ref_lse, e = plain_loss(h, w, y)
+        loss, lse = run_loss(gcq, h, w, y)
+        check_loss(loss, lse, ref, ref_lse, e)
+        dh, dw = run_grad(gcq, h, w, y, ref_lse.float(), d, t, torch.float32)
+        # e^x of the logit's error, which reaches some 1e-3 here, grows faster than it
+        rh, eh, _, _ = plain_grad(h, w, y, ref_lse.float(), d, t, torch.float32)
+        _, _, rw, ew = plain_grad(h, w, y, ref_lse.float(), d, torch.float32, t)
+        check_grad(dh, rh, 1.01 * eh)
+        check_grad(dw, rw, 1.01 * ew)
+
+
+def test_scale_of_the_inputs_does_not_matter(gcq):
+    """fp32 inputs scaled by powers of two far outside fp16's range give the
+    same loss bit for bit where the logits are the same."""
+    announce("linear_xent fp32 scales")
+    h, w, y, d = inputs(50, 300, 96, torch.float32)
+    want = run_loss(gcq, h, w, y)
+    lse = want[1]
+    dh, dw = run_grad(gcq, h, w, y, lse, d, torch.float32, torch.float32)
+    for k in (-100, -40, 40, 100):
+        a, b = torch.ldexp(h, torch.tensor(k)), torch.ldexp(w, torch.tensor(-k))
+        got = run_loss(gcq, a, b, y)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), k
+        gh, gw = run_grad(gcq, a, b, y, lse, d, torch.float32, torch.float32)
+        assert torch.equal(torch.ldexp(gh, torch.tensor(k)), dh), k
+        if k < 100:  # (2^100 dh's own values stay finite, and above the subnormal)
+            assert torch.equal(torch.ldexp(gw, torch.tensor(-k)), dw), k
+    gh, gw = run_grad(gcq, h, w, y, lse, torch.ldexp(d, torch.tensor(-60)), torch.float32, torch.float32)
+    assert torch.equal(torch.ldexp(gh, torch.tensor(60)), dh) and torch.equal(torch.ldexp(gw, torch.tensor(60)), dw)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+def test_flat_bucket_views_and_guards(gcq, t):
+    """Inputs and outputs one element into their allocation, as views of a
+    flat bucket are: the same bits, and nothing written beside them."""
+    announce(f"linear_xent misaligned {t}")
+    N, V, D = 70, 301, 128
+    h, w, y, d = inputs(N, V, D, t)
+    lse = plain_loss(h, w, y)[1].float()
+    want = run_grad(gcq, h, w, y, lse, d, t, torch.float32)
+    want_loss = run_loss(gcq, h, w, y)
+    guards = []
+
+    def off(v, dtype=None):
+        buf = torch.full((v.numel() + 40,), 7, dtype=v.dtype if dtype is None else dtype, device=gu.DEV)
+        view = buf[1:1 + v.numel()].view(v.shape)
+        view.copy_(v)
+        guards.append(buf)
+        return view
+    dev = [off(x) for x in (h, w, y, lse, d)]
+    dh, dw = off(torch.zeros(N, D), t), off(torch.zeros(V, D), torch.float32)
+    loss, lse2 = off(torch.zeros(N)), off(torch.zeros(N))
+    size = gcq.linear_xent_grad_ws_bytes(N, V, D, t, t, torch.float32)
+    ws = torch.full((size + 256,), 255, dtype=torch.uint8, device=gu.DEV)
+    gcq.linear_xent_grad(*dev, dh, dw, ws[:size])
+    size2 = gcq.linear_xent_loss_ws_bytes(N, V, D, t)
+    ws2 = torch.full((size2 + 256,), 255, dtype=torch.uint8, device=gu.DEV)
+    gcq.linear_xent_loss(dev[0], dev[1], dev[2], loss, lse2, ws2[:size2])
+    gu.sync()
+    assert torch.equal(dh.cpu(), want[0]) and torch.equal(dw.cpu(), want[1])
+    assert torch.equal(loss.cpu(), want_loss[0]) and torch.equal(lse2.cpu(), want_loss[1])
+    assert bool((ws[size:] == 255).all()) and bool((ws2[size2:] == 255).all())
+    for buf in guards:
+        assert float(buf[0]) == 7 and bool((buf[-39:] == 7).all())
+
+
+@pytest.mark.parametrize("types", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32),
+                                   (torch.float32, torch.float32)], ids=str)
+def test_several_pieces_and_splits(gcq, types):
+    """More tokens x vocabulary than one piece of G holds, a last piece that
+    ends inside a tile, and products split over k: against float64 on the
+    device, sampled rows in full."""
+    t, tw = types
+    N, V, D = 4100, 70_003, 72
+    announce(f"linear_xent_grad in pieces {types}")
+    g = torch.Generator(device=gu.DEV).manual_seed(3)
+    h = torch.randn(N, D, generator=g, device=gu.DEV).to(t)
+    w = (torch.randn(V, D, generator=g, device=gu.DEV) * 2 / D ** 0.5).to(t)
+    y = torch.randint(0, V, (N,), generator=g, device=gu.DEV)
+    y[::9] = IGNORE
+    d = torch.randn(N, generator=g, device=gu.DEV)
+    size = gcq.linear_xent_grad_ws_bytes(N, V, D, t, t, tw)
+    # G, of 2 bytes a plane, is never whole
+    assert size < 2 * (2 if tw == torch.float32 else 1) * N * V
+    loss, lse = torch.empty(N, device=gu.DEV), torch.empty(N, device=gu.DEV)
+    gcq.linear_xent_loss(h, w, y, loss, lse,
+                         torch.empty(gcq.linear_xent_loss_ws_bytes(N, V, D, t), dtype=torch.uint8, device=gu.DEV))
+    dh, dw = torch.empty_like(h), torch.empty(V, D, dtype=tw, device=gu.DEV)
+    gcq.linear_xent_grad(h, w, y, lse, d, dh, dw, torch.empty(size, dtype=torch.uint8, device=gu.DEV))
+    gu.sync()
+    rows = torch.cat([torch.arange(0, N, 311), torch.tensor([N - 1])])
+    ref, ref_lse, e = plain_loss(h[rows].cpu(), w.cpu(), y[rows].cpu())
+    check_loss(loss[rows].cpu(), lse[rows].cpu(), ref, ref_lse, e)
+    rh, eh, _, _ = plain_grad(h[rows].cpu(), w.cpu(), y[rows].cpu(), lse[rows].cpu(), d[rows].cpu(), t, tw)
+    check_grad(dh[rows].cpu(), rh, eh + 2.0 ** -36 * float(d.abs().max()) * w.double().abs().sum(0).cpu())
+    # rows of the vocabulary on both sides of every piece's and tile's end, and targets
+    vocab = torch.unique(torch.cat([torch.arange(0, V, 1021), torch.arange(15_800, V, 256)[::8] + 255, y[y >= 0][:50].cpu(),
+                                    torch.tensor([V - 1])]).clamp(max=V - 1))
+    l64 = h.double() @ w[vocab.to(gu.DEV)].double().t()
+    has = y != IGNORE
+    gm = torch.exp(l64 - lse.double()[:, None]) - (y[:, None] == vocab.to(gu.DEV)[None, :]).double()
+    gm = torch.where(has[:, None], gm * d.double()[:, None], 0.0)
+    ref = gm.t().contiguous() @ torch.where(has[:, None], h.double(), 0.0)
+    # per term: the logit's error (D + 2 steps of its magnitude), exp's steps, G's rounding
+    rel = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -22}[tw if tw == torch.float32 else t]
+    el = ((D + 2) * po.F32 + 3.1 * 2.0 ** -22) * (h.double().abs() @ w[vocab.to(gu.DEV)].double().abs().t()).max() + 16 * po.F32
+    mag = gm.abs().t().contiguous() @ h.double().abs()
+    err = mag * (rel + el + (N + 2) * po.F32 + 3.1 * 2.0 ** -22)
+    check_grad(dw[vocab.to(gu.DEV)].cpu(), ref.cpu(), err.cpu())
+
+
+def test_gradient_against_differences(gcq):
+    """(f(v + e) - f(v - e)) / 2e of the kernels' own loss, fp32."""
+    announce("linear_xent differences")
+    h, w, y, d = inputs(6, 40, 32, torch.float32, seed=8)
+    lse = run_loss(gcq, h, w, y)[1]
+    dh, dw = run_grad(gcq, h, w, y, lse, d, torch.float32, torch.float32)
+
+    def value(k, i, e):
+        a, b = h.clone(), w.clone()
+        (a if k == "h" else b).view(-1)[i] += e
+        return float((run_loss(gcq, a, b, y)[0].double() * d.double()).sum())
+    # noise: 6 losses off by at most 300 F each, times |d| < 4, over 2 e; and
+    # e^2 / 6 times a third derivative below 4 * 6 * 4^3
+    e = 2.0 ** -6
+    allowed = 6 * 4 * 300 * po.F32 / (2 * e) + e * e / 6 * 1536
+    for k, got in (("h", dh), ("w", dw)):
+        for i in (0, 33, 77, got.numel() - 1):
+            diff = (value(k, i, e) - value(k, i, -e)) / (2 * e)
+            assert abs(diff - float(got.view(-1)[i])) <= allowed, (k, i)
+
+
+def test_graph_replays_and_streams(gcq):
+    """Loss and gradient captured once and replayed on new inputs, and the
+    same calls on two streams at once, each with its own workspace."""
+    announce("linear_xent in a HIP graph, and on two streams")
+    N, V, D = 200, 700, 136
+    for t, tw in ((torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)):
+        sets = []
+        for k in range(2):
+            h, w, y, d = [x.to(gu.DEV) for x in inputs(N, V, D, t, seed=k)]
+            sets.append(dict(h=h, w=w, y=y, d=d, loss=torch.empty(N, device=gu.DEV), lse=torch.empty(N, device=gu.DEV),
+                             dh=torch.empty_like(h), dw=torch.empty(V, D, dtype=tw, device=gu.DEV),
+                             ws=torch.empty(max(gcq.linear_xent_loss_ws_bytes(N, V, D, t),
+                                                gcq.linear_xent_grad_ws_bytes(N, V, D, t, t, tw)), dtype=torch.uint8,
+                                            device=gu.DEV)))
+
+        def body(s, stream=None):
+            gcq.linear_xent_loss(s["h"], s["w"], s["y"], s["loss"], s["lse"], s["ws"], stream=stream)
+            gcq.linear_xent_grad(s["h"], s["w"], s["y"], s["lse"], s["d"], s["dh"], s["dw"], s["ws"], stream=stream)
+        s = sets[0]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            body(s)
+        torch.cuda.current_stream().wait_stream(side)
+        gu.sync()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            body(s)
+        for k in range(3):
+            new = inputs(N, V, D, t, seed=10 + k)
+            for name, v in zip("hwyd", new):
+                s[name].copy_(v)
+            for name in ("loss", "lse", "dh", "dw"):
+                s[name].fill_(float("nan"))
+            s["ws"].fill_(255)
+            gu.sync()
+            graph.replay()
+            gu.sync()
+            loss, lse = run_loss(gcq, *new[:3])
+            dh, dw = run_grad(gcq, *new[:3], lse, new[3], t, tw)
+            assert torch.equal(s["loss"].cpu(), loss) and torch.equal(s["lse"].cpu(), lse)
+            assert torch.equal(s["dh"].cpu(), dh) and torch.equal(s["dw"].cpu(), dw)
+        want = []
+        for s in sets:
+            body(s)
+            gu.sync()
+            want.append([s[k].clone() for k in ("loss", "lse", "dh", "dw")])
+        streams = [torch.cuda.Stream() for _ in sets]
+        gu.sync()
+        for _ in range(5):
+            for s, st in zip(sets, streams):
+                body(s, stream=st)
+        gu.sync()
+        for s, ref in zip(sets, want):
+            for k, r in zip(("loss", "lse", "dh", "dw"), ref):
+                assert torch.equal(s[k], r)
