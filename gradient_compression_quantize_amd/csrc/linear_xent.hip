@@ -71,9 +71,17 @@ constexpr unsigned kMaxParts = 1024;
 
 struct MaxOf {
     const void* src;
+    bool f32;  // else of the inputs' type
     size_t rows, d;
     const int64_t* target;
-    float* parts;  // [kMaxParts]
+    float* parts;
+    unsigned nparts;
+};
+
+// A launch takes the maxima of up to three matrices, and lays out up to two
+// and sets an exponent: blockIdx.y says which.
+struct MaxOfAll {
+    MaxOf of[3];
 };
 
 __device__ __forceinline__ float workgroup_max(float m)
@@ -92,12 +100,12 @@ __device__ __forceinline__ float workgroup_max(float m)
 }
 
 template <typename T>
-__global__ __launch_bounds__(kRowThreads) void largest_kernel(MaxOf a, int64_t ignore, size_t V)
+__device__ __forceinline__ void largest(const MaxOf& a, int64_t ignore, size_t V)
 {
     const T* src = static_cast<const T*>(a.src);
     const int lane = threadIdx.x & (kWave - 1);
     float m = 0.0f;
-    for (size_t r = size_t(blockIdx.x) * kRowWaves + threadIdx.x / kWave; r < a.rows; r += size_t(gridDim.x) * kRowWaves) {
+    for (size_t r = size_t(blockIdx.x) * kRowWaves + threadIdx.x / kWave; r < a.rows; r += size_t(a.nparts) * kRowWaves) {
         if (a.target && !has_target(a.target, r, ignore, V))
             continue;
         const T* row = src + r * a.d;
@@ -115,53 +123,67 @@ __global__ __launch_bounds__(kRowThreads) void largest_kernel(MaxOf a, int64_t i
         a.parts[blockIdx.x] = m;
 }
 
-// The exponent that brings the largest value to [2^14, 2^15): called by whole
-// workgroups.
-__device__ __forceinline__ int exponent_of(const float* parts)
+template <typename T>
+__global__ __launch_bounds__(kRowThreads) void largest_kernel(MaxOfAll all, int64_t ignore, size_t V)
 {
-    float m = 0.0f;
-#pragma unroll
-    for (unsigned k = 0; k < kMaxParts; k += kRowThreads)
-        m = fmaxf(m, parts[k + threadIdx.x]);
-    m = workgroup_max(m);
-    return m > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(m) : 0;
+    const MaxOf a = blockIdx.y == 0 ? all.of[0] : blockIdx.y == 1 ? all.of[1] : all.of[2];
+    if (blockIdx.x >= a.nparts)
+        return;
+    if (a.f32)
+        largest<float>(a, ignore, V);
+    else
+        largest<T>(a, ignore, V);
 }
 
-// The exponent alone, where the values are written later (G).
-__global__ __launch_bounds__(kRowThreads) void exponent_kernel(const float* parts, int* exponent)
-{
-    const int k = exponent_of(parts);
-    if (threadIdx.x == 0)
-        *exponent = k;
-}
+// src [rows][d] -> planes [rows_out][d_out] (d_out a multiple of 8), one
+// behind the other, of bf16 as it is or of fp16, scaled where `parts` is not
+// NULL so that the largest value comes to [2^14, 2^15); zeros behind the last
+// column and row, and in the rows that have no target if `target` is not NULL:
+// what such rows hold, NaN included, reaches nothing. One wave a row. Without
+// an `out` only the exponent is set.
+struct PlanesOf {
+    const void* src;
+    size_t rows, d;
+    uint16_t* out;
+    size_t rows_out, d_out;
+    const int64_t* target;
+    const float* parts;
+    unsigned nparts;
+    int* exponent;
+};
 
-// src [rows][d] -> kPlanes planes [rows_out][d_out] (d_out a multiple of 8),
-// one behind the other, of bf16 as it is (kF16 = false) or of fp16, scaled
-// where `parts` is not NULL; zeros behind the last column and row, and in the
-// rows that have no target if `target` is not NULL: what such rows hold, NaN
-// included, reaches nothing. One wave a row.
+struct PlanesOfAll {
+    PlanesOf of[3];
+};
+
 template <typename T, bool kF16, int kPlanes>
-__global__ __launch_bounds__(kRowThreads) void planes_kernel(const T* __restrict__ src, size_t rows, size_t d,
-                                                             uint16_t* __restrict__ out, size_t rows_out, size_t d_out,
-                                                             const int64_t* __restrict__ target, int64_t ignore,
-                                                             size_t V, const float* __restrict__ parts,
-                                                             int* __restrict__ exponent)
+__global__ __launch_bounds__(kRowThreads) void planes_kernel(PlanesOfAll all, int64_t ignore, size_t V)
 {
+    const PlanesOf a = blockIdx.y == 0 ? all.of[0] : blockIdx.y == 1 ? all.of[1] : all.of[2];
+    if (size_t(blockIdx.x) * kRowWaves >= std::max<size_t>(a.out ? a.rows_out : 0, 1))
+        return;
     int scale = 0;
-    if (kF16 && parts) {
-        scale = exponent_of(parts);
+    if (kF16 && a.parts) {
+        float m = 0.0f;
+        for (unsigned k = threadIdx.x; k < a.nparts; k += kRowThreads)
+            m = fmaxf(m, a.parts[k]);
+        m = workgroup_max(m);
+        scale = m > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(m) : 0;
         if (blockIdx.x == 0 && threadIdx.x == 0)
-            *exponent = scale;
+            *a.exponent = scale;
     }
+    if (!a.out)
+        return;
+    const T* src = static_cast<const T*>(a.src);
     const int lane = threadIdx.x & (kWave - 1);
-    for (size_t r = size_t(blockIdx.x) * kRowWaves + threadIdx.x / kWave; r < rows_out;
+    for (size_t r = size_t(blockIdx.x) * kRowWaves + threadIdx.x / kWave; r < a.rows_out;
          r += size_t(gridDim.x) * kRowWaves) {
-        const bool live = r < rows && (!target || has_target(target, r, ignore, V));
+        const bool live = r < a.rows && (!a.target || has_target(a.target, r, ignore, V));
 #pragma unroll 2
-        for (size_t c = lane * 8; c < d_out; c += kWave * 8) {
+        for (size_t c = lane * 8; c < a.d_out; c += kWave * 8) {
             float v[8] = {};
             if (live)
-                load8(src + r * d, c, d, v);
+                load8(src + r * a.d, c, a.d, v);
 #pragma unroll
             for (int plane = 0; plane < kPlanes; ++plane) {
                 s16x8 w;
@@ -178,7 +200,7 @@ __global__ __launch_bounds__(kRowThreads) void planes_kernel(const T* __restrict
                     // an infinity or NaN stays in the first plane alone
                     v[k] = fabsf(float(h)) <= 65504.0f ? (v[k] - float(h)) * 0x1p11f : 0.0f;
                 }
-                *reinterpret_cast<s16x8*>(out + plane * (rows_out * d_out) + r * d_out + c) = w;
+                *reinterpret_cast<s16x8*>(a.out + plane * (a.rows_out * a.d_out) + r * a.d_out + c) = w;
             }
         }
     }
@@ -635,20 +657,63 @@ unsigned stride_grid(size_t items, size_t per)
     return unsigned(std::max<size_t>(1, std::min(ceil_div(items, per), max_grid_blocks())));
 }
 
-// Launches the maxima of src.
-template <typename T>
-void launch_largest(const T* src, size_t rows, size_t d, const int64_t* target, int64_t ignore, size_t V, float* parts,
-                    hipStream_t stream)
-{
-    hipLaunchKernelGGL(largest_kernel<T>, dim3(kMaxParts), dim3(kRowThreads), 0, stream,
-                       MaxOf{src, rows, d, target, parts}, ignore, V);
-}
+// What has to be done before the products, in at most two launches.
+struct Preparation {
+    MaxOfAll max{};
+    PlanesOfAll planes{};
+    int nmax = 0, nplanes = 0;
 
-// Describes src as an operand by rows, laid out as planes in the workspace
-// unless it can be read as it is. Of rows without a target (`target` not NULL)
-// the scale takes no notice, and with `drop` they become zeros.
-MatOperand make_operand(const void* src, size_t rows, size_t D, int dtype, const Mode& mode, const PlaneRoom& room,
-                        char* ws, const int64_t* target, bool drop, int64_t ignore, size_t V, hipStream_t stream)
+    void scale_by(const void* src, bool f32, size_t rows, size_t d, const int64_t* target, float* parts)
+    {
+        max.of[nmax++] = MaxOf{src, f32, rows, d, target, parts,
+                               unsigned(std::min<size_t>(ceil_div(rows, kRowWaves), kMaxParts))};
+    }
+
+    // The exponent of the matrix that scale_by was called for last.
+    void lay_out(PlanesOf p, bool scaled)
+    {
+        if (scaled) {
+            p.parts = max.of[nmax - 1].parts;
+            p.nparts = max.of[nmax - 1].nparts;
+        }
+        planes.of[nplanes++] = p;
+    }
+
+    void launch(int dtype, const Mode& mode, int64_t ignore, size_t V, hipStream_t stream) const
+    {
+        unsigned parts = 0;
+        for (int k = 0; k < nmax; ++k)
+            parts = std::max(parts, max.of[k].nparts);
+        size_t rows = 1;
+        for (int k = 0; k < nplanes; ++k)
+            rows = std::max(rows, planes.of[k].out ? planes.of[k].rows_out : 0);
+        const dim3 grid(unsigned(std::min<size_t>(ceil_div(rows, kRowWaves), 256 * 8)), unsigned(nplanes));
+        with_dtype(dtype, [&](auto t) {
+            using T = decltype(t);
+            if (nmax)
+                hipLaunchKernelGGL(largest_kernel<T>, dim3(parts, unsigned(nmax)), dim3(kRowThreads), 0, stream, max,
+                                   ignore, V);
+            if (!nplanes)
+                return 0;
+            const auto launch = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, grid, dim3(kRowThreads), 0, stream, planes, ignore, V);
+            };
+            if constexpr (sizeof(T) == 4)
+                launch(planes_kernel<T, true, 2>);
+            else if (mode.f16)
+                launch(planes_kernel<T, true, 1>);
+            else
+                launch(planes_kernel<T, false, 1>);
+            return 0;
+        });
+    }
+};
+
+// Describes src as an operand by rows: as it is, or as planes in the workspace
+// that `prep` is to lay out. Of rows without a target (`target` not NULL) the
+// scale takes no notice, and with `drop` they become zeros.
+MatOperand make_operand(Preparation& prep, const void* src, size_t rows, size_t D, const Mode& mode, int dtype,
+                        const PlaneRoom& room, char* ws, const int64_t* target, bool drop)
 {
     MatOperand m{};
     if (!drop && direct_ok(src, D, mode)) {
@@ -658,26 +723,11 @@ MatOperand make_operand(const void* src, size_t rows, size_t D, int dtype, const
         return m;
     }
     uint16_t* out = reinterpret_cast<uint16_t*>(ws + room.off);
-    float* parts = mode.scaled ? reinterpret_cast<float*>(ws + room.parts) : nullptr;
     int* exponent = mode.scaled ? reinterpret_cast<int*>(ws + room.exponent) : nullptr;
-    with_dtype(dtype, [&](auto t) {
-        using T = decltype(t);
-        const T* p = static_cast<const T*>(src);
-        if (parts)
-            launch_largest(p, rows, D, target, ignore, V, parts, stream);
-        const auto launch = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, dim3(unsigned(std::min<size_t>(ceil_div(room.rows, kRowWaves), 256 * 8))),
-                               dim3(kRowThreads), 0, stream, p, rows, D, out, room.rows, room.d,
-                               drop ? target : nullptr, ignore, V, parts, exponent);
-        };
-        if constexpr (sizeof(T) == 4)
-            launch(planes_kernel<T, true, 2>);
-        else if (mode.f16)
-            launch(planes_kernel<T, true, 1>);
-        else
-            launch(planes_kernel<T, false, 1>);
-        return 0;
-    });
+    if (mode.scaled)
+        prep.scale_by(src, dtype == GC_F32, rows, D, target, reinterpret_cast<float*>(ws + room.parts));
+    prep.lay_out(PlanesOf{src, rows, D, out, room.rows, room.d, drop ? target : nullptr, nullptr, 0, exponent},
+                 mode.scaled);
     m.plane0 = out;
     m.plane_stride = room.rows * room.d;
     m.ld = uint32_t(room.d);
@@ -878,8 +928,10 @@ GCQ_API int linear_xent_loss(const void* hidden, const void* weight, int dtype, 
     if (!aligned16(ws) || *ws_bytes < L.total)
         return fail(GC_EINVAL, "linear_xent_loss: workspace too small or not 16-byte aligned");
     char* w = static_cast<char*>(ws);
-    const MatOperand wo = make_operand(weight, V, D, dtype, L.mode, L.weight, w, nullptr, false, 0, V, stream);
-    const MatOperand ho = make_operand(hidden, N, D, dtype, L.mode, L.hidden, w, target, false, ignore_index, V, stream);
+    Preparation prep;
+    const MatOperand wo = make_operand(prep, weight, V, D, L.mode, dtype, L.weight, w, nullptr, false);
+    const MatOperand ho = make_operand(prep, hidden, N, D, L.mode, dtype, L.hidden, w, target, false);
+    prep.launch(dtype, L.mode, ignore_index, V, stream);
     ProductShape sh{};
     sh.turns = uint32_t(round_up(D, kTurnK) / kTurnK);
     set_pairs(sh, L.weight.planes, L.hidden.planes);
@@ -947,18 +999,19 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
         return GC_OK;
 
     char* w = static_cast<char*>(ws);
-    const MatOperand wo = make_operand(weight, V, D, dtype, L.mode, L.weight, w, nullptr, false, 0, V, stream);
+    Preparation prep;
+    const MatOperand wo = make_operand(prep, weight, V, D, L.mode, dtype, L.weight, w, nullptr, false);
     // always a copy: rows without a target become zeros
-    const MatOperand ho = make_operand(hidden, N, D, dtype, L.mode, L.hidden, w, target, true, ignore_index, V, stream);
+    const MatOperand ho = make_operand(prep, hidden, N, D, L.mode, dtype, L.hidden, w, target, true);
     GradOut g{};
     MatOperand go{};
     if (L.mode.f16) {
-        float* parts = reinterpret_cast<float*>(w + L.g_parts);
         int* exponent = reinterpret_cast<int*>(w + L.g_exponent);
-        launch_largest(dloss, N, 1, target, ignore_index, V, parts, stream);
-        hipLaunchKernelGGL(exponent_kernel, dim3(1), dim3(kRowThreads), 0, stream, parts, exponent);
+        prep.scale_by(dloss, true, N, 1, target, reinterpret_cast<float*>(w + L.g_parts));
+        prep.lay_out(PlanesOf{nullptr, 0, 0, nullptr, 0, 0, nullptr, nullptr, 0, exponent}, true);
         go.exponent = g.exponent = exponent;
     }
+    prep.launch(dtype, L.mode, ignore_index, V, stream);
     go.plane0 = g.plane0 = reinterpret_cast<uint16_t*>(w + L.g);
     go.plane_stride = g.plane_stride = L.n_pad * L.piece;
     go.ld = g.ld = uint32_t(L.piece);
