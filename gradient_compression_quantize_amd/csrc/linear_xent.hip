@@ -376,10 +376,10 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
     const int back = kF16 ? unscale(weight, hidden) : 0, up = kF16 ? *out.exponent : 0;
 
     // this wave's buffer, for its turn of values into rows
-    static_assert(TA == TB && P::kWaves == 2 * kBuffers, "a buffer for each wave");
+    static_assert(P::kWaves <= kBuffers || (P::kWaves <= 2 * kBuffers && TA == TB), "a buffer for each wave");
     uint16_t* part = lds.a[0];
 #pragma unroll
-    for (int k = 1; k < 2 * kBuffers; ++k)
+    for (int k = 1; k < P::kWaves; ++k)
         part = wave == k ? (k < kBuffers ? lds.a[k] : lds.b[k - kBuffers]) : part;
 
 #pragma unroll
@@ -742,16 +742,24 @@ struct LossConfig {
     int ta, tb, wa;
 };
 
-// Tiles of 256 x 256 read the least and need some rounds of 256 of them; few
-// tokens take smaller ones, which fill the chip with tiles of the vocabulary
-// alone and leave less of a tile empty. V = 30522, D = 768, us:
+// Tiles of 256 x 256 read the least and need some rounds of 256 of them; what
+// has fewer than half a round takes smaller ones, two of which share a compute
+// unit. V = 30522, D = 768, us:
 //   tokens        1     32     64    128    256    512
 //   128 x 64   14.5   16.5   16.2
 //   128 x 128                19.4   19.1   25.6   39.8
 //   256 x 256  24.7   25.1   21.6   21.0   27.2   31.1
-LossConfig loss_config(size_t N)
+constexpr int kTile = 256, kSmallTile = 128;
+constexpr size_t kCus = 256;
+
+int logit_tile(size_t N, size_t V)
 {
-    return N <= 64 ? LossConfig{128, 64, 2} : N <= 256 ? LossConfig{128, 128, 2} : LossConfig{256, 256, 2};
+    return ceil_div(N, kTile) * ceil_div(V, kTile) <= kCus / 2 ? kSmallTile : kTile;
+}
+
+LossConfig loss_config(size_t N, size_t V)
+{
+    return N <= 64 ? LossConfig{128, 64, 2} : LossConfig{logit_tile(N, V), logit_tile(N, V), 2};
 }
 
 struct LossLayout {
@@ -766,7 +774,7 @@ LossLayout loss_layout(size_t N, size_t V, size_t D, int dtype)
     LossLayout L{};
     Carver c;
     L.mode = mode_of(dtype, dtype != GC_BF16);
-    L.cfg = loss_config(N);
+    L.cfg = loss_config(N, V);
     L.weight = plane_room(c, V, D, L.mode);
     L.hidden = plane_room(c, N, D, L.mode);
     L.nparts = ceil_div(V, L.cfg.ta) * L.cfg.wa;
@@ -785,8 +793,10 @@ LossLayout loss_layout(size_t N, size_t V, size_t D, int dtype)
 // 1024 and 2048 MB; 8192 x 64000 x 4096 in bf16 10.96, 10.83, 10.83, 10.73 and
 // 10.75 ms.
 constexpr size_t kPieceBytes = size_t(512) << 20;
-constexpr int kTile = 256;
-constexpr size_t kCus = 256;
+struct ProductPlan {
+    int tile;
+    uint32_t splits;
+};
 
 struct GradLayout {
     Mode mode;
@@ -795,7 +805,7 @@ struct GradLayout {
     int g_planes;
     size_t g, g_parts, g_exponent, h_slab, w_slab, total;
     size_t d4;  // row length of the slabs
-    uint32_t h_splits, w_splits;
+    ProductPlan h, w;
 };
 
 // Splits of a product of `tiles` tiles over `turns` turns: as many as find a
@@ -803,9 +813,20 @@ struct GradLayout {
 // tiles with more of them cost more in partial results than it gave: 8192 x
 // 30522 x 768 with an fp32 gradient (192 tiles of 128 turns into 16384 x 768)
 // took 1974 us with 4 splits, 1884 with 1.
-uint32_t splits_for(size_t tiles, size_t turns)
+//
+// Few tiles are smaller ones: of 128 x 128, two share a compute unit. The
+// fp32 gradient of 100 x 3001 x 256 took 63 us with tiles of 256 alone, 46
+// with these; that of 4000 x 9000 x 1024, whose dhidden is 64 tiles, 770 and
+// 812.
+constexpr size_t kFewTiles = 32;
+
+ProductPlan product_plan(size_t rows, size_t D, size_t turns)
 {
-    return uint32_t(std::max<size_t>(1, std::min(kCus / std::max<size_t>(tiles, 1), turns / 4)));
+    ProductPlan p{};
+    p.tile = ceil_div(rows, kTile) * ceil_div(D, kTile) <= kFewTiles ? kSmallTile : kTile;
+    const size_t tiles = ceil_div(rows, p.tile) * ceil_div(D, p.tile), room = p.tile == kTile ? kCus : 2 * kCus;
+    p.splits = uint32_t(std::max<size_t>(1, std::min(room / tiles, turns / 4)));
+    return p;
 }
 
 // Planes of G for a gradient of the type: one, rounded to the 16 bits that the
@@ -835,32 +856,40 @@ GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, in
     L.g = c.take(L.g_planes * L.n_pad * L.piece * 2);
     L.g_parts = c.take(kMaxParts * sizeof(float));
     L.g_exponent = c.take(sizeof(int));
-    const size_t ta = ceil_div(D, kTile);
-    L.h_splits = splits_for(ceil_div(N, kTile) * ta,
-                            L.piece / kTurnK * grad_shape(L.weight.planes, dh_dtype).segments);
-    L.w_splits = splits_for(L.piece / kTile * ta,
-                            L.n_pad / kTurnK * grad_shape(L.hidden.planes, dw_dtype).segments);
-    L.h_slab = c.take(L.h_splits > 1 || L.pieces > 1 ? L.h_splits * N * L.d4 * 4 : 0);
-    L.w_slab = c.take(L.w_splits > 1 ? L.w_splits * L.piece * L.d4 * 4 : 0);
+    L.h = product_plan(N, D, L.piece / kTurnK * grad_shape(L.weight.planes, dh_dtype).segments);
+    L.w = product_plan(L.piece, D, L.n_pad / kTurnK * grad_shape(L.hidden.planes, dw_dtype).segments);
+    L.h_slab = c.take(L.h.splits > 1 || L.pieces > 1 ? L.h.splits * N * L.d4 * 4 : 0);
+    L.w_slab = c.take(L.w.splits > 1 ? L.w.splits * L.piece * L.d4 * 4 : 0);
     L.total = c.used;
     return L;
 }
 
 // A product into `out` of type T.
 template <bool kBK, typename T>
-void launch_product(const MatOperand& A, const MatOperand& B, ProductShape sh, const ProductOut<T>& out, bool f16,
-                    hipStream_t stream)
+void launch_product(const MatOperand& A, const MatOperand& B, ProductShape sh, int tile, const ProductOut<T>& out,
+                    bool f16, hipStream_t stream)
 {
-    const dim3 grid(sh.tiles_a * sh.tiles_b * sh.splits), block(8 * kWave);
+    sh.tiles_a = uint32_t(ceil_div(out.na, tile));
+    sh.tiles_b = uint32_t(ceil_div(out.nb, tile));
+    const dim3 grid(sh.tiles_a * sh.tiles_b * sh.splits);
+    const auto either = [&](auto f) {
+        constexpr bool kF16 = decltype(f)::value;
+        if (tile == kTile)
+            hipLaunchKernelGGL((product_kernel<kF16, kBK, kTile, kTile, 2, 4, T>), grid, dim3(8 * kWave), 0, stream, A,
+                               B, sh, out);
+        else
+            hipLaunchKernelGGL((product_kernel<kF16, kBK, kSmallTile, kSmallTile, 2, 2, T>), grid, dim3(4 * kWave), 0,
+                               stream, A, B, sh, out);
+    };
     if (f16)
-        hipLaunchKernelGGL((product_kernel<true, kBK, kTile, kTile, 2, 4, T>), grid, block, 0, stream, A, B, sh, out);
+        either(std::true_type());
     else if constexpr (!std::is_same_v<T, f16_t>)
-        hipLaunchKernelGGL((product_kernel<false, kBK, kTile, kTile, 2, 4, T>), grid, block, 0, stream, A, B, sh, out);
+        either(std::false_type());
 }
 
 template <bool kBK>
-void launch_product_any(const MatOperand& A, const MatOperand& B, const ProductShape& sh, void* out, int dtype,
-                        size_t nb, size_t D, bool f16, hipStream_t stream)
+void launch_product_any(const MatOperand& A, const MatOperand& B, const ProductShape& sh, int tile, void* out,
+                        int dtype, size_t nb, size_t D, bool f16, hipStream_t stream)
 {
     with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
@@ -870,7 +899,7 @@ void launch_product_any(const MatOperand& A, const MatOperand& B, const ProductS
         o.na = uint32_t(D);
         o.nb = uint32_t(nb);
         o.vec = D % 4 == 0 && aligned_to(out, 4 * sizeof(T));
-        launch_product<kBK, T>(A, B, sh, o, f16, stream);
+        launch_product<kBK, T>(A, B, sh, tile, o, f16, stream);
         return 0;
     });
 }
@@ -1018,7 +1047,7 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
     g.rows_out = uint32_t(L.n_pad);
     float* h_slab = reinterpret_cast<float*>(w + L.h_slab);
     float* w_slab = reinterpret_cast<float*>(w + L.w_slab);
-    const bool h_direct = L.h_splits == 1 && L.pieces == 1;
+    const bool h_direct = L.h.splits == 1 && L.pieces == 1;
 
     for (size_t v0 = 0; v0 < V; v0 += L.piece) {
         const size_t vp = std::min(L.piece, V - v0);
@@ -1028,20 +1057,30 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
         ProductShape sh{};
         sh.turns = uint32_t(round_up(D, kTurnK) / kTurnK);
         set_pairs(sh, L.weight.planes, L.hidden.planes);
-        sh.tiles_a = uint32_t(ceil_div(vp, kTile));
-        sh.tiles_b = uint32_t(ceil_div(L.n_pad, kTile));
+        const int tile = logit_tile(L.n_pad, vp);
+        sh.tiles_a = uint32_t(ceil_div(vp, tile));
+        sh.tiles_b = uint32_t(ceil_div(L.n_pad, tile));
         sh.splits = 1;
-        const dim3 grid(sh.tiles_a * sh.tiles_b), block(8 * kWave);
-        const auto logits = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, grid, block, 0, stream, wp, ho, sh, uint32_t(N), uint32_t(v0), uint32_t(V),
-                               target, ignore_index, lse, dloss, g);
+        const dim3 grid(sh.tiles_a * sh.tiles_b), block(tile == kTile ? 8 * kWave : 4 * kWave);
+        const auto logits = [&](auto whole, auto small) {
+            const auto launch = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, grid, block, 0, stream, wp, ho, sh, uint32_t(N), uint32_t(v0), uint32_t(V),
+                                   target, ignore_index, lse, dloss, g);
+            };
+            if (tile == kTile)
+                launch(whole);
+            else
+                launch(small);
         };
         if (!L.mode.f16)
-            logits(logit_grad_kernel<false, kTile, kTile, 2, 4, 1>);
+            logits(logit_grad_kernel<false, kTile, kTile, 2, 4, 1>,
+                   logit_grad_kernel<false, kSmallTile, kSmallTile, 2, 2, 1>);
         else if (L.g_planes == 1)
-            logits(logit_grad_kernel<true, kTile, kTile, 2, 4, 1>);
+            logits(logit_grad_kernel<true, kTile, kTile, 2, 4, 1>,
+                   logit_grad_kernel<true, kSmallTile, kSmallTile, 2, 2, 1>);
         else
-            logits(logit_grad_kernel<true, kTile, kTile, 2, 4, 2>);
+            logits(logit_grad_kernel<true, kTile, kTile, 2, 4, 2>,
+                   logit_grad_kernel<true, kSmallTile, kSmallTile, 2, 2, 2>);
         if (dhidden) {
             MatOperand A = wp, B = go;
             A.extent = uint32_t(wo.ld);
@@ -1049,14 +1088,12 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
             B.extent = uint32_t(N);
             ProductShape ps = grad_shape(L.weight.planes, dhidden_dtype);
             ps.turns = uint32_t(ceil_div(vp, kTurnK));
-            ps.tiles_a = uint32_t(ceil_div(D, kTile));
-            ps.tiles_b = uint32_t(ceil_div(N, kTile));
-            ps.splits = L.h_splits;
+            ps.splits = L.h.splits;
             if (h_direct) {
-                launch_product_any<false>(A, B, ps, dhidden, dhidden_dtype, N, D, L.mode.f16, stream);
+                launch_product_any<false>(A, B, ps, L.h.tile, dhidden, dhidden_dtype, N, D, L.mode.f16, stream);
             } else {
                 ProductOut<float> o{h_slab, L.d4, N * L.d4, uint32_t(L.d4), uint32_t(N), true, v0 > 0};
-                launch_product<false, float>(A, B, ps, o, L.mode.f16, stream);
+                launch_product<false, float>(A, B, ps, L.h.tile, o, L.mode.f16, stream);
             }
         }
         if (dweight) {
@@ -1066,20 +1103,18 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
             B.extent = uint32_t(L.piece);
             ProductShape ps = grad_shape(L.hidden.planes, dweight_dtype);
             ps.turns = uint32_t(L.n_pad / kTurnK);
-            ps.tiles_a = uint32_t(ceil_div(D, kTile));
-            ps.tiles_b = uint32_t(ceil_div(vp, kTile));
-            ps.splits = L.w_splits;
+            ps.splits = L.w.splits;
             char* out = static_cast<char*>(dweight) + v0 * D * dtype_bytes(dweight_dtype);
-            if (L.w_splits == 1) {
-                launch_product_any<true>(A, B, ps, out, dweight_dtype, vp, D, L.mode.f16, stream);
+            if (L.w.splits == 1) {
+                launch_product_any<true>(A, B, ps, L.w.tile, out, dweight_dtype, vp, D, L.mode.f16, stream);
             } else {
                 ProductOut<float> o{w_slab, L.d4, L.piece * L.d4, uint32_t(L.d4), uint32_t(vp), true, false};
-                launch_product<true, float>(A, B, ps, o, L.mode.f16, stream);
-                launch_sum(w_slab, L.d4, L.piece * L.d4, L.w_splits, vp, D, out, dweight_dtype, stream);
+                launch_product<true, float>(A, B, ps, L.w.tile, o, L.mode.f16, stream);
+                launch_sum(w_slab, L.d4, L.piece * L.d4, L.w.splits, vp, D, out, dweight_dtype, stream);
             }
         }
     }
     if (dhidden && !h_direct)
-        launch_sum(h_slab, L.d4, N * L.d4, L.h_splits, N, D, dhidden, dhidden_dtype, stream);
+        launch_sum(h_slab, L.d4, N * L.d4, L.h.splits, N, D, dhidden, dhidden_dtype, stream);
     return check_launch("linear_xent_grad");
 }
