@@ -596,9 +596,9 @@ struct Carver {
 };
 
 // Sizes the index arithmetic of the kernels holds: 32-bit tokens, vocabulary
-// and channels, 32-bit byte offsets within a tile of 256 rows (2^31 / 512
-// values a row).
+// and channels, 32-bit byte offsets within a tile of 256 rows.
 constexpr size_t kMaxTokens = size_t(1) << 28, kMaxVocab = size_t(1) << 28, kMaxChannels = size_t(1) << 20;
+constexpr size_t kMaxTiles = size_t(1) << 22, kMaxPiece = size_t(1) << 21;
 
 int check_sizes(const char* what, size_t N, size_t V, size_t D, int dtype)
 {
@@ -609,6 +609,10 @@ int check_sizes(const char* what, size_t N, size_t V, size_t D, int dtype)
     if (N > kMaxTokens || V > kMaxVocab || D > kMaxChannels)
         return fail(GC_EUNSUPPORTED, std::string(what) + ": sizes beyond 2^28 tokens, 2^28 rows of the "
                                                          "vocabulary or 2^20 channels");
+    // a launch has fewer than 2^32 threads: 2^22 tiles of 256 x 256
+    if (ceil_div(N, 256) * ceil_div(V, 256) > kMaxTiles || ceil_div(N, 256) * ceil_div(D, 256) > kMaxTiles ||
+        ceil_div(std::min(V, kMaxPiece), 256) * ceil_div(D, 256) > kMaxTiles)
+        return fail(GC_EUNSUPPORTED, std::string(what) + ": a product of more than 2^22 tiles of 256 x 256");
     return GC_OK;
 }
 
@@ -851,7 +855,7 @@ GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, in
     L.d4 = round_up(D, 4);
     L.g_planes = std::max(g_planes(dh_dtype), g_planes(dw_dtype));
     const size_t columns = kPieceBytes / (L.n_pad * 2 * L.g_planes) / kTile * kTile;
-    L.piece = std::min(std::max<size_t>(columns, kTile), round_up(V, kTile));
+    L.piece = std::min({std::max<size_t>(columns, kTile), round_up(V, kTile), kMaxPiece});
     L.pieces = ceil_div(V, L.piece);
     L.g = c.take(L.g_planes * L.n_pad * L.piece * 2);
     L.g_parts = c.take(kMaxParts * sizeof(float));

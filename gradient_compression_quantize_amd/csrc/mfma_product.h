@@ -88,8 +88,9 @@ struct StageLoader {
     static_assert(kLoads >= 1, "every wave moves at least one load");
     static constexpr int kChunks = T / 8;                // by k: 16-byte chunks of a row
     static constexpr int kRowsPerLoad = 1024 / (2 * T);  // by k
-    uint32_t off[kLoads];  // by rows: byte offset of each load; by k: of its columns alone
+    uint32_t off[kLoads];  // by rows: byte offset of each load from the tile's first row; by k: of its columns alone
     uint32_t row;          // by k: the first load's row
+    size_t origin;         // by rows: values before the tile's first row
     int wave;
 
     // XOR on the chunk index of LDS row `row`, so that what is read in one
@@ -104,6 +105,7 @@ struct StageLoader {
     __device__ __forceinline__ void init(const MatOperand& m, uint32_t first, int wave_, int lane)
     {
         wave = wave_;
+        origin = kKRows ? 0 : size_t(first) * m.ld;
         row = wave * kLoads * kRowsPerLoad + lane / kChunks;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
@@ -113,18 +115,19 @@ struct StageLoader {
             } else {
                 const uint32_t r = (wave * kLoads + j) * 16 + lane / 4;
                 const uint32_t chunk = (lane & 3) ^ swizzle(r);
-                off[j] = min(first + r, m.extent - 1) * m.ld * 2 + chunk * 16;
+                // 255 rows of up to 2^22 bytes
+                off[j] = min(r, m.extent - 1 - first) * m.ld * 2 + chunk * 16;
             }
         }
     }
 
     // Where the stage from k0 on of plane p starts, as a descriptor of `bytes`
     // bytes: of none, its loads fetch nothing.
-    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage(const MatOperand& m, const uint16_t* p, uint32_t k0,
-                                                                   uint32_t bytes)
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage(const MatOperand& m, const uint16_t* p, uint32_t k0,
+                                                            uint32_t bytes) const
     {
         // (by k: not past the last row)
-        const uint16_t* base = p + (kKRows ? size_t(min(k0, m.krows - 1)) * m.ld : size_t(k0));
+        const uint16_t* base = p + (kKRows ? size_t(min(k0, m.krows - 1)) * m.ld : origin + k0);
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, bytes, 0x00020000);
     }
 
@@ -243,8 +246,8 @@ struct TileProduct {
             // (readfirstlane keeps what the compiler would select in vector
             // registers in scalar ones)
             const uint32_t bytes = __builtin_amdgcn_readfirstlane(left ? 0xFFFFFFFFu : 0u);
-            const Fetch f = {LoadA::stage(A, A.plane0 + pa * A.plane_stride, k0, bytes),
-                             LoadB::stage(B, B.plane0 + pb * B.plane_stride, k0, bytes), k0};
+            const Fetch f = {ga.stage(A, A.plane0 + pa * A.plane_stride, k0, bytes),
+                             gb.stage(B, B.plane0 + pb * B.plane_stride, k0, bytes), k0};
             left -= bytes & 1;
             k0 += kStageK;
             const uint32_t over = __builtin_amdgcn_readfirstlane(k0 == k_end ? 1u : 0u);

@@ -668,6 +668,8 @@ GCQ_API int norm_residual(const void* x, const void* y, int dtype, size_t rows, 
     const size_t b = dtype_bytes(dtype);
     if (!x || !y || !z || (pre_gain && (!h || !rstd_pre)) || (post_gain && !rstd_post))
         return fail(GC_EINVAL, "norm_residual: a buffer is NULL");
+    if (!pre_gain && h)
+        return fail(GC_EINVAL, "norm_residual: h without pre_gain");
     if (!aligned_to(x, b) || !aligned_to(y, b) || !aligned_to(z, b) || !aligned_to(h, b) || !aligned4(post_gain) ||
         !aligned4(gate) || !aligned4(pre_gain) || !aligned4(rstd_post) || !aligned4(rstd_pre))
         return fail(GC_EINVAL, "norm_residual: a buffer is misaligned");

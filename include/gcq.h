@@ -347,7 +347,7 @@ int dropout_backward(const void* grad_out, size_t n, int dtype, double p,
  * rounding.
  *   x, y, z, h  [rows, d] of `dtype`, rows contiguous; z may be x or y, h
  *               may be the other one
- *   post_gain, pre_gain  [d] fp32, or NULL
+ *   post_gain, pre_gain  [d] fp32, or NULL (h is then NULL too)
  *   gate        [gates, d] fp32, or NULL; `gates` divides rows, and row r
  *               takes gate row r / (rows / gates)
  *   rstd_post, rstd_pre  [rows] fp32 out, for the gradient; needed where the
@@ -370,6 +370,7 @@ int norm_residual(const void* x, const void* y, int dtype, size_t rows, size_t d
  *               computed. fp32 sums over the rows in a fixed order.
  *   ws          16-byte-aligned workspace; ws == NULL: *ws_bytes = its size
  *               for (rows, d, gates), else *ws_bytes must be at least that.
+ *               Calls that may overlap in time need workspaces of their own.
  * rows may be 0: the gains' gradients are then zero. */
 int norm_residual_grad(const void* z, const void* y, int dtype, size_t rows, size_t d,
                        const float* post_gain, const float* gate, size_t gates,
@@ -397,7 +398,9 @@ int norm_residual_grad(const void* z, const void* y, int dtype, size_t rows, siz
  *   ws      16-byte-aligned workspace; ws == NULL: *ws_bytes is set to the
  *           size needed for (N, V, D, dtype) and nothing is enqueued.
  *           Otherwise *ws_bytes is its size and must be at least that.
- *   N, V <= 2^28, D <= 2^20, V and D at least 1; N may be 0. */
+ *           Calls that may overlap in time need workspaces of their own.
+ *   N, V <= 2^28, D <= 2^20, V and D at least 1, N V, N D and V D of at most
+ *   2^22 tiles of 256 x 256 (else GC_EUNSUPPORTED); N may be 0. */
 int linear_xent_loss(const void* hidden, const void* weight, int dtype, size_t N,
                      size_t V, size_t D, const int64_t* target,
                      int64_t ignore_index, float* loss, float* lse, void* ws,

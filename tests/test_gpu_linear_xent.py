@@ -425,3 +425,61 @@ def test_graph_replays_and_streams(gcq):
         for s, ref in zip(sets, want):
             for k, r in zip(("loss", "lse", "dh", "dw"), ref):
                 assert torch.equal(s[k], r)
+
+
+@pytest.mark.slow
+def test_offsets_past_32_bits(gcq):
+    """A weight matrix of 4.6 GB: byte offsets of its rows, and of its
+    gradient's, pass 2^32. Against float64 on the device, in pieces."""
+    N, V, D = 130, 1_100_003, 2112
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GiB of device memory")
+    announce(f"linear_xent V={V} D={D}")
+    g = torch.Generator(device=gu.DEV).manual_seed(1)
+    w = (torch.empty(V, D, dtype=torch.bfloat16, device=gu.DEV).normal_(generator=g)).mul_(2.0 / D ** 0.5)
+    h = torch.randn(N, D, generator=g, device=gu.DEV).to(torch.bfloat16)
+    y = torch.randint(V - 70_000, V, (N,), generator=g, device=gu.DEV)
+    y[3] = IGNORE
+    y[4], y[5] = 0, V - 1
+    d = torch.randn(N, generator=g, device=gu.DEV)
+    loss, lse = torch.empty(N, device=gu.DEV), torch.empty(N, device=gu.DEV)
+    gcq.linear_xent_loss(h, w, y, loss, lse,
+                         torch.empty(gcq.linear_xent_loss_ws_bytes(N, V, D, w.dtype), dtype=torch.uint8, device=gu.DEV))
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    gcq.linear_xent_grad(h, w, y, lse, d, dh, dw,
+                         torch.empty(gcq.linear_xent_grad_ws_bytes(N, V, D, w.dtype), dtype=torch.uint8, device=gu.DEV))
+    gu.sync()
+    h64 = h.double()
+    sums = torch.zeros(N, dtype=torch.float64, device=gu.DEV)
+    target = torch.zeros(N, dtype=torch.float64, device=gu.DEV)
+    rh = torch.zeros(N, D, dtype=torch.float64, device=gu.DEV)
+    has = y != IGNORE
+    dl = torch.where(has, d.double(), 0.0)
+    e = (D + 2) * po.F32 * (h64.abs().sum(1).max() * 2.0 / D ** 0.5 * 6)  # |w| stays below 6 deviations
+    for lo in range(0, V, 50_000):
+        wp = w[lo:lo + 50_000].double()
+        l = h64 @ wp.t()
+        sums += torch.exp(l).sum(1)
+        at = torch.where(has & (y >= lo) & (y < lo + wp.shape[0]), y - lo, -1)
+        rows = (at >= 0).nonzero()[:, 0]
+        target[rows] = l[rows, at[rows]]
+        gm = torch.exp(l - lse.double()[:, None])
+        gm[rows, at[rows]] -= 1.0
+        gm *= dl[:, None]
+        rh += gm @ wp
+        ref = gm.t() @ torch.where(has[:, None], h64, 0.0)
+        mag = gm.abs().t() @ h64.abs()
+        got = dw[lo:lo + 50_000].double()
+        assert bool(((got - ref).abs() <= mag * (2.0 ** -8 + e + 300 * po.F32) + ref.abs() * 1.01 * 2.0 ** -8).all()), lo
+        # every term of dhidden is off by at most G's rounding and the logit's error
+        # and the fp32 sums, 16 products deep at a time, by their steps
+        errh = gm.abs() @ wp.abs() * (2.0 ** -8 + e + (V / 16 + 300) * po.F32)
+        eh = errh if lo == 0 else eh + errh
+    ref_lse = sums.log()
+    assert bool(((lse.double() - ref_lse).abs() <= e + 64 * po.F32 * (1 + ref_lse)).all())
+    ref = torch.where(has, ref_lse - target, 0.0)
+    assert bool(((loss.double() - ref).abs() <= 2 * e + 200 * po.F32 * (1 + ref_lse)).all())
+    assert bool(((dh.double() - rh).abs() <= eh + rh.abs() * 1.01 * 2.0 ** -8).all())
+    del w, dw
+    torch.cuda.empty_cache()

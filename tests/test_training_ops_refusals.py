@@ -65,7 +65,7 @@ def norm(lib, **kw):
 def test_norm_residual_refusals(lib):
     for bad in (dict(x=None), dict(y=None), dict(z=None), dict(h=None), dict(rp=None), dict(rz=None), dict(d=0),
                 dict(gates=3), dict(gates=0), dict(dt=7), dict(eps=-1.0), dict(eps=math.nan), dict(p=2.0),
-                dict(x=FAKE + 2), dict(gate=FAKE + 1), dict(step=FAKE + 2), dict(dt=1, h=FAKE + 1)):
+                dict(x=FAKE + 2), dict(gate=FAKE + 1), dict(step=FAKE + 2), dict(dt=1, h=FAKE + 1), dict(pre=None)):
         assert norm(lib, **bad) == gcq.GC_EINVAL, bad
     assert norm(lib, d=16385) == gcq.GC_EUNSUPPORTED
     assert norm(lib, rows=0) == gcq.GC_OK
@@ -133,7 +133,7 @@ def test_linear_xent_loss_refusals(lib):
                 dict(dt=5), dict(h=FAKE + 1), dict(w=FAKE + 2, dt=0), dict(y=FAKE + 4), dict(lse=FAKE + 2),
                 dict(ws=FAKE + 4), dict(size=8)):
         assert xent(lib, **bad)[0] == gcq.GC_EINVAL, bad
-    for big in (dict(N=2 ** 28 + 1), dict(V=2 ** 28 + 1), dict(D=2 ** 20 + 1)):
+    for big in (dict(N=2 ** 28 + 1), dict(V=2 ** 28 + 1), dict(D=2 ** 20 + 1), dict(N=2 ** 24, V=2 ** 24)):
         assert xent(lib, **big)[0] == gcq.GC_EUNSUPPORTED, big
     assert xent(lib, N=0)[0] == gcq.GC_OK
     rc, size = xent(lib, ws=None, N=8192, V=30522, D=768)
