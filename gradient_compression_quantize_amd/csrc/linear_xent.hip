@@ -224,12 +224,14 @@ struct LossPart {
     float top, sum;  // the maximum, and the sum of exp(l - top)
 };
 
-// Vocabulary tile x token tile. A wave's part of a token's row is kRowsA
-// logits, half of them in each half of the wave.
+// Vocabulary tile x token tile, of the rows v0 .. v0 + v - 1 of the
+// vocabulary, which `weight` begins with; their parts are part0 and on. A
+// wave's part of a token's row is kRowsA logits, half of them in each half of
+// the wave.
 template <bool kF16, int TA, int TB, int WA, int WB>
 __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
-    MatOperand weight, MatOperand hidden, ProductShape sh, uint32_t N, uint32_t V,
-    const int64_t* __restrict__ target, LossPart* __restrict__ parts, uint32_t nparts,
+    MatOperand weight, MatOperand hidden, ProductShape sh, uint32_t N, uint32_t v0, uint32_t v, uint32_t V,
+    const int64_t* __restrict__ target, LossPart* __restrict__ parts, uint32_t nparts, uint32_t part0,
     float* __restrict__ target_logit)
 {
     using L = LogitTile<kF16, TA, TB, WA, WB>;
@@ -258,7 +260,7 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
         }
         // the target's place in this wave's part, if it is there: it hardly
         // ever is, and only the last tile reaches past the vocabulary
-        const uint32_t at = t >= 0 && t < int64_t(V) ? uint32_t(t) - a_wave : 0xFFFFFFFFu;
+        const uint32_t at = t >= 0 && t < int64_t(V) ? uint32_t(t) - (v0 + a_wave) : 0xFFFFFFFFu;
         if (__any(at < uint32_t(L::kRowsA))) {
             float mine = 0.0f;
             bool found = false;
@@ -273,8 +275,8 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
             if (found)
                 target_logit[n] = mine;
         }
-        if (a_wave + L::kRowsA > V) {
-            const uint32_t left = V > a_wave ? V - a_wave : 0;
+        if (a_wave + L::kRowsA > v) {
+            const uint32_t left = v > a_wave ? v - a_wave : 0;
 #pragma unroll
             for (int i = 0; i < P::RA; ++i)
 #pragma unroll
@@ -301,7 +303,7 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
         float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
         sum += __shfl_xor(sum, 32);
         if (lane < 32 && n < N)
-            parts[size_t(n) * nparts + ta * WA + wa] = LossPart{top, sum};
+            parts[size_t(n) * nparts + part0 + ta * WA + wa] = LossPart{top, sum};
     }
 }
 
@@ -742,10 +744,6 @@ MatOperand make_operand(Preparation& prep, const void* src, size_t rows, size_t 
 
 // ---- loss
 
-struct LossConfig {
-    int ta, tb, wa;
-};
-
 // Tiles of 256 x 256 read the least and need some rounds of 256 of them; what
 // has fewer than half a round takes smaller ones, two of which share a compute
 // unit. V = 30522, D = 768, us:
@@ -753,22 +751,53 @@ struct LossConfig {
 //   128 x 64   14.5   16.5   16.2
 //   128 x 128                19.4   19.1   25.6   39.8
 //   256 x 256  24.7   25.1   21.6   21.0   27.2   31.1
-constexpr int kTile = 256, kSmallTile = 128;
+constexpr int kTile = 256, kSmallTile = 128, kLogitWavesA = 2;
 constexpr size_t kCus = 256;
 
-int logit_tile(size_t N, size_t V)
-{
-    return ceil_div(N, kTile) * ceil_div(V, kTile) <= kCus / 2 ? kSmallTile : kTile;
-}
+// A range of the vocabulary and the tiles that it takes.
+struct LogitRange {
+    size_t v0, v;
+    int ta, tb;
+    size_t tiles_a() const { return ceil_div(v, ta); }
+};
 
-LossConfig loss_config(size_t N, size_t V)
+struct LogitPlan {
+    LogitRange range[2];
+    int count;
+};
+
+// The logits of N rows. A last round of 256 x 256 tiles that would leave more
+// than half of the chip empty goes as tiles of 128 x 128 instead: 1001 x 33333
+// x 1001 fp32, 524 tiles, took 329 us in three rounds.
+LogitPlan logit_plan(size_t N, size_t V, bool few_rows)
 {
-    return N <= 64 ? LossConfig{128, 64, 2} : LossConfig{logit_tile(N, V), logit_tile(N, V), 2};
+    LogitPlan p{};
+    p.count = 1;
+    if (few_rows && N <= 64) {
+        p.range[0] = LogitRange{0, V, kSmallTile, 64};
+        return p;
+    }
+    const size_t tb = ceil_div(N, kTile), tiles = tb * ceil_div(V, kTile);
+    if (tiles <= kCus / 2) {
+        p.range[0] = LogitRange{0, V, kSmallTile, kSmallTile};
+        return p;
+    }
+    p.range[0] = LogitRange{0, V, kTile, kTile};
+    const size_t whole = tiles / kCus * kCus / tb;  // tiles of the vocabulary in whole rounds
+    if (whole > 0 && whole * kTile < V) {
+        const LogitRange rest{whole * kTile, V - whole * kTile, kSmallTile, kSmallTile};
+        if (rest.tiles_a() * ceil_div(N, kSmallTile) <= 2 * kCus) {
+            p.range[0].v = whole * kTile;
+            p.range[1] = rest;
+            p.count = 2;
+        }
+    }
+    return p;
 }
 
 struct LossLayout {
     Mode mode;
-    LossConfig cfg;
+    LogitPlan plan;
     PlaneRoom weight, hidden;
     size_t parts, target_logit, nparts, total;
 };
@@ -778,10 +807,11 @@ LossLayout loss_layout(size_t N, size_t V, size_t D, int dtype)
     LossLayout L{};
     Carver c;
     L.mode = mode_of(dtype, dtype != GC_BF16);
-    L.cfg = loss_config(N, V);
+    L.plan = logit_plan(N, V, true);
     L.weight = plane_room(c, V, D, L.mode);
     L.hidden = plane_room(c, N, D, L.mode);
-    L.nparts = ceil_div(V, L.cfg.ta) * L.cfg.wa;
+    for (int k = 0; k < L.plan.count; ++k)
+        L.nparts += L.plan.range[k].tiles_a() * kLogitWavesA;
     L.parts = c.take(N * L.nparts * sizeof(LossPart));
     L.target_logit = c.take(N * 4);
     L.total = c.used;
@@ -968,29 +998,37 @@ GCQ_API int linear_xent_loss(const void* hidden, const void* weight, int dtype, 
     ProductShape sh{};
     sh.turns = uint32_t(round_up(D, kTurnK) / kTurnK);
     set_pairs(sh, L.weight.planes, L.hidden.planes);
-    sh.tiles_a = uint32_t(ceil_div(V, L.cfg.ta));
-    sh.tiles_b = uint32_t(ceil_div(N, L.cfg.tb));
     sh.splits = 1;
     LossPart* parts = reinterpret_cast<LossPart*>(w + L.parts);
     float* tl = reinterpret_cast<float*>(w + L.target_logit);
-    const dim3 grid(sh.tiles_a * sh.tiles_b);
-    const auto tiles = [&](auto kernel, int waves) {
-        hipLaunchKernelGGL(kernel, grid, dim3(waves * kWave), 0, stream, wo, ho, sh, uint32_t(N), uint32_t(V), target,
-                           parts, uint32_t(L.nparts), tl);
-    };
-    const auto either = [&](auto f16) {
-        constexpr bool kF16 = decltype(f16)::value;
-        if (L.cfg.tb == 64)
-            tiles(loss_tiles_kernel<kF16, 128, 64, 2, 2>, 4);
-        else if (L.cfg.tb == 128)
-            tiles(loss_tiles_kernel<kF16, 128, 128, 2, 2>, 4);
+    size_t part0 = 0;
+    for (int k = 0; k < L.plan.count; ++k) {
+        const LogitRange& r = L.plan.range[k];
+        MatOperand wr = wo;
+        wr.plane0 += r.v0 * wo.ld;
+        wr.extent = uint32_t(r.v);
+        sh.tiles_a = uint32_t(r.tiles_a());
+        sh.tiles_b = uint32_t(ceil_div(N, r.tb));
+        const dim3 grid(sh.tiles_a * sh.tiles_b);
+        const auto tiles = [&](auto kernel, int waves) {
+            hipLaunchKernelGGL(kernel, grid, dim3(waves * kWave), 0, stream, wr, ho, sh, uint32_t(N), uint32_t(r.v0),
+                               uint32_t(r.v), uint32_t(V), target, parts, uint32_t(L.nparts), uint32_t(part0), tl);
+        };
+        const auto either = [&](auto f16) {
+            constexpr bool kF16 = decltype(f16)::value;
+            if (r.tb == 64)
+                tiles(loss_tiles_kernel<kF16, kSmallTile, 64, kLogitWavesA, 2>, 4);
+            else if (r.tb == kSmallTile)
+                tiles(loss_tiles_kernel<kF16, kSmallTile, kSmallTile, kLogitWavesA, 2>, 4);
+            else
+                tiles(loss_tiles_kernel<kF16, kTile, kTile, kLogitWavesA, 4>, 8);
+        };
+        if (L.mode.f16)
+            either(std::true_type());
         else
-            tiles(loss_tiles_kernel<kF16, 256, 256, 2, 4>, 8);
-    };
-    if (L.mode.f16)
-        either(std::true_type());
-    else
-        either(std::false_type());
+            either(std::false_type());
+        part0 += r.tiles_a() * kLogitWavesA;
+    }
     hipLaunchKernelGGL(loss_join_kernel, dim3(stride_grid(N, kJoinThreads / kWave)), dim3(kJoinThreads), 0,
                        stream, parts, uint32_t(L.nparts), tl, target, ignore_index, uint32_t(N), uint32_t(V),
                        loss, lse);
@@ -1061,30 +1099,38 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
         ProductShape sh{};
         sh.turns = uint32_t(round_up(D, kTurnK) / kTurnK);
         set_pairs(sh, L.weight.planes, L.hidden.planes);
-        const int tile = logit_tile(L.n_pad, vp);
-        sh.tiles_a = uint32_t(ceil_div(vp, tile));
-        sh.tiles_b = uint32_t(ceil_div(L.n_pad, tile));
+        const LogitPlan plan = logit_plan(L.n_pad, vp, false);
         sh.splits = 1;
-        const dim3 grid(sh.tiles_a * sh.tiles_b), block(tile == kTile ? 8 * kWave : 4 * kWave);
-        const auto logits = [&](auto whole, auto small) {
-            const auto launch = [&](auto kernel) {
-                hipLaunchKernelGGL(kernel, grid, block, 0, stream, wp, ho, sh, uint32_t(N), uint32_t(v0), uint32_t(V),
-                                   target, ignore_index, lse, dloss, g);
+        for (int k = 0; k < plan.count; ++k) {
+            const LogitRange& r = plan.range[k];
+            MatOperand wr = wp;
+            wr.plane0 += r.v0 * wo.ld;
+            wr.extent = uint32_t(r.v);
+            GradOut gr = g;
+            gr.plane0 += r.v0;
+            sh.tiles_a = uint32_t(r.tiles_a());
+            sh.tiles_b = uint32_t(ceil_div(L.n_pad, r.tb));
+            const dim3 grid(sh.tiles_a * sh.tiles_b);
+            const auto logits = [&](auto whole, auto small) {
+                const auto launch = [&](auto kernel, int waves) {
+                    hipLaunchKernelGGL(kernel, grid, dim3(waves * kWave), 0, stream, wr, ho, sh, uint32_t(N),
+                                       uint32_t(v0 + r.v0), uint32_t(V), target, ignore_index, lse, dloss, gr);
+                };
+                if (r.tb == kTile)
+                    launch(whole, 8);
+                else
+                    launch(small, 4);
             };
-            if (tile == kTile)
-                launch(whole);
+            if (!L.mode.f16)
+                logits(logit_grad_kernel<false, kTile, kTile, 2, 4, 1>,
+                       logit_grad_kernel<false, kSmallTile, kSmallTile, 2, 2, 1>);
+            else if (L.g_planes == 1)
+                logits(logit_grad_kernel<true, kTile, kTile, 2, 4, 1>,
+                       logit_grad_kernel<true, kSmallTile, kSmallTile, 2, 2, 1>);
             else
-                launch(small);
-        };
-        if (!L.mode.f16)
-            logits(logit_grad_kernel<false, kTile, kTile, 2, 4, 1>,
-                   logit_grad_kernel<false, kSmallTile, kSmallTile, 2, 2, 1>);
-        else if (L.g_planes == 1)
-            logits(logit_grad_kernel<true, kTile, kTile, 2, 4, 1>,
-                   logit_grad_kernel<true, kSmallTile, kSmallTile, 2, 2, 1>);
-        else
-            logits(logit_grad_kernel<true, kTile, kTile, 2, 4, 2>,
-                   logit_grad_kernel<true, kSmallTile, kSmallTile, 2, 2, 2>);
+                logits(logit_grad_kernel<true, kTile, kTile, 2, 4, 2>,
+                       logit_grad_kernel<true, kSmallTile, kSmallTile, 2, 2, 2>);
+        }
         if (dhidden) {
             MatOperand A = wp, B = go;
             A.extent = uint32_t(wo.ld);
