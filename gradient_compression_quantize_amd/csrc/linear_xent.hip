@@ -850,9 +850,9 @@ struct GradLayout {
 //
 // Few tiles are smaller ones: of 128 x 128, two share a compute unit. The
 // fp32 gradient of 100 x 3001 x 256 took 63 us with tiles of 256 alone, 46
-// with these; that of 4000 x 9000 x 1024, whose dhidden is 64 tiles, 770 and
-// 812.
-constexpr size_t kFewTiles = 32;
+// with these; that of 600 x 5000 x 500, whose dweight is 40 tiles of 256, 100
+// and 90; that of 4000 x 9000 x 1024, whose dhidden is 64, 770 and 812.
+constexpr size_t kFewTiles = 48;
 
 ProductPlan product_plan(size_t rows, size_t D, size_t turns)
 {
@@ -874,6 +874,42 @@ ProductShape grad_shape(int planes_a, int out_dtype)
     return sh;
 }
 
+// Tiles of the vocabulary of one piece: all of them if that is at most `most`
+// (two pieces of 4000 x 9000 x 1024 took 500 us, one 400), else at least half
+// of `most`. The pieces' products for dweight run in rounds of 256 tiles, which some
+// sizes fill better than others; splits and pieces cost their partial results
+// (about 4 TB/s, in turns of 3.4 us). 8192 x 30522 x 768 with an fp32
+// gradient: 1955 us in pieces of 64 tiles (192 of dweight), 1890 in pieces of
+// 42 (126, in two splits).
+size_t piece_tiles(size_t most, size_t N, size_t V, size_t D, size_t h_turns_a_tile, size_t w_turns)
+{
+    const size_t all = ceil_div(V, kTile), from = std::max<size_t>(most / 2, 1);
+    if (all <= most)
+        return all;
+    constexpr double kTurnBytes = 4e12 * 3.4e-6;
+    size_t best = most;
+    double least = 0.0;
+    for (size_t p = best; p >= from; p -= std::max<size_t>(p / 64, 1)) {
+        const auto turns = [&](size_t tiles) {
+            const ProductPlan w = product_plan(tiles * kTile, D, w_turns), h = product_plan(N, D, tiles * h_turns_a_tile);
+            const size_t room = w.tile == kTile ? kCus : 2 * kCus;
+            const double a_turn = w.tile == kTile ? 1.0 : 0.5;
+            return double(ceil_div(ceil_div(tiles * kTile, w.tile) * ceil_div(D, w.tile) * w.splits, room)) *
+                       double(ceil_div(w_turns, w.splits)) * a_turn +
+                   (w.splits > 1 ? double(w.splits * tiles * kTile * D) * 8.0 / kTurnBytes : 0.0) +
+                   double(h.splits * N * D) * 8.0 / kTurnBytes;
+        };
+        const double t = double(all / p) * turns(p) + (all % p ? turns(all % p) : 0.0);
+        if (p == best || t < least) {
+            best = p;
+            least = t;
+        }
+        if (p == 1)
+            break;
+    }
+    return best;
+}
+
 GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, int dw_dtype)
 {
     GradLayout L{};
@@ -884,14 +920,16 @@ GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, in
     L.hidden = plane_room(c, L.n_pad, D, L.mode);
     L.d4 = round_up(D, 4);
     L.g_planes = std::max(g_planes(dh_dtype), g_planes(dw_dtype));
-    const size_t columns = kPieceBytes / (L.n_pad * 2 * L.g_planes) / kTile * kTile;
-    L.piece = std::min({std::max<size_t>(columns, kTile), round_up(V, kTile), kMaxPiece});
+    const size_t h_turns = kTile / kTurnK * grad_shape(L.weight.planes, dh_dtype).segments;  // of a tile of the vocabulary
+    const size_t w_turns = L.n_pad / kTurnK * grad_shape(L.hidden.planes, dw_dtype).segments;
+    const size_t most = std::min(std::max<size_t>(kPieceBytes / (L.n_pad * 2 * L.g_planes * kTile), 1), kMaxPiece / kTile);
+    L.piece = piece_tiles(most, N, V, D, h_turns, w_turns) * kTile;
     L.pieces = ceil_div(V, L.piece);
     L.g = c.take(L.g_planes * L.n_pad * L.piece * 2);
     L.g_parts = c.take(kMaxParts * sizeof(float));
     L.g_exponent = c.take(sizeof(int));
-    L.h = product_plan(N, D, L.piece / kTurnK * grad_shape(L.weight.planes, dh_dtype).segments);
-    L.w = product_plan(L.piece, D, L.n_pad / kTurnK * grad_shape(L.hidden.planes, dw_dtype).segments);
+    L.h = product_plan(N, D, L.piece / kTile * h_turns);
+    L.w = product_plan(L.piece, D, w_turns);
     L.h_slab = c.take(L.h.splits > 1 || L.pieces > 1 ? L.h.splits * N * L.d4 * 4 : 0);
     L.w_slab = c.take(L.w.splits > 1 ? L.w.splits * L.piece * L.d4 * 4 : 0);
     L.total = c.used;
