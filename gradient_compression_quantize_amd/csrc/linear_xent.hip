@@ -11,7 +11,13 @@
 // Gradient: piece by piece of the vocabulary, the logits are computed again
 // and turned into G in the tile's registers; G of one piece is the only
 // matrix of tokens x vocabulary that is ever in memory, and the two products
-// of the gradient read it back from the cache.
+// of the gradient read it back.
+//
+// Bound by the matrix cores and, for narrow models, by what G costs: 8192 x
+// 30522 x 768 bf16 takes 355 to 390 us for the loss (1.0 to 1.1 PFLOP/s) and
+// 1.87 ms for a gradient with fp32 dweight (a third of it in tiles of G, whose
+// 1 GB of stores no other tile's products run under); 8192 x 64000 x 4096 takes
+// 10.7 to 11.1 ms for the gradient (1.2 PFLOP/s).
 #include <algorithm>
 #include <limits>
 #include <string>

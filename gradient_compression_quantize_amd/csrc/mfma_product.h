@@ -27,6 +27,14 @@
 // chunks permuted by an XOR of the row, which the loads apply to their global
 // addresses (LDS-direct loads write lane after lane) and the fragment reads to
 // their LDS addresses.
+//
+// Measured on 8192 x 64000 x 4096 bf16: 1.13 to 1.27 PFLOP/s (torch's library
+// product of that shape: 1.50). The matrix cores are busy 62 to 70% of the
+// cycles, and power holds the clock near 1.7 GHz: the first form, two stages of
+// 64 k with the reads of one stage behind its barrier, kept them busy 46% at
+// 2.16 GHz and was a tenth slower. Tiles of 128 x 128, two to a compute unit,
+// were a fifth slower; four waves of 128 x 128 outputs each half as fast;
+// s_setprio around the products made no difference.
 #pragma once
 
 #include "values.h"

@@ -18,6 +18,11 @@
 // and the gate are sums over rows: a workgroup adds its rows in registers,
 // writes one partial row, and a second launch adds the partial rows in their
 // order.
+//
+// Bound by HBM: 16384 x 4096 bf16 with dropout takes 112 us forward (537 MB,
+// 4.8 TB/s) and 166 us backward (805 MB, 4.8 TB/s), a plain copy moving 5.2.
+// The backward pass has some 60 vector instructions a value, about 105 us of
+// them: they have to run under the loads, which the row fetched ahead does.
 #include "dropout_mask.h"
 
 #include <algorithm>
