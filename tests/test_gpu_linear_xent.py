@@ -156,6 +156,24 @@ def test_grad(gcq, size, types):
     check_grad(dw, rw, ew)
 
 
+@pytest.mark.parametrize("t", TYPES, ids=str)
+def test_a_last_round_of_small_tiles(gcq, t):
+    """258 tiles of 256 x 256: the vocabulary's end goes as smaller ones, with
+    targets on both sides of the border and in the last row."""
+    N, V, D = 300, 33_000, 72
+    announce(f"linear_xent {N} x {V} x {D} {t}")
+    h, w, y, d = inputs(N, V, D, t, seed=6)
+    y[:6] = torch.tensor([0, 128 * 256 - 1, 128 * 256, 128 * 256 + 127, 128 * 256 + 128, V - 1])
+    ref, ref_lse, e = plain_loss(h, w, y)
+    check_loss(*run_loss(gcq, h, w, y), ref, ref_lse, e)
+    lse = ref_lse.float()
+    dh, dw = run_grad(gcq, h, w, y, lse, d, t, torch.float32)
+    rh, eh, _, _ = plain_grad(h, w, y, lse, d, t, torch.float32)
+    _, _, rw, ew = plain_grad(h, w, y, lse, d, torch.float32, t)
+    check_grad(dh, rh, eh)
+    check_grad(dw, rw, ew)
+
+
 def test_grad_alone_of_each(gcq):
     announce("linear_xent_grad of one operand")
     h, w, y, d = inputs(70, 500, 96, torch.bfloat16)
