@@ -553,6 +553,21 @@ def _at(t, dtype, what: str, cur):
     return None if t is None else _ptr(t, dtype, what, cur)
 
 
+def _ats(cur, dtype, names: str, *ts) -> list:
+    """_at of several tensors of one dtype; `names` holds theirs, in order. One
+    loop for them all, since a small call is mostly marshalling."""
+    out = []
+    for k, t in enumerate(ts):
+        if t is None:
+            out.append(None)
+        elif (not t.is_cuda or t.dtype != dtype or not t.is_contiguous()
+              or (cur is not None and t.get_device() != cur)):
+            _refuse(t, dtype, names.split()[k], cur)
+        else:
+            out.append(t.data_ptr())
+    return out
+
+
 def _ws(ws, what: str):
     """The size of a workspace; one of no bytes would read as a query."""
     if ws.numel() == 0:
@@ -617,12 +632,16 @@ def _norm_shape(y, what: str, same, gate, columns, per_row):
         raise ValueError(f"{what}: a row must hold at least one value")
     d = y.shape[-1]
     rows = y.numel() // d
-    if any(t is not None and t.numel() != rows * d for t in same):
-        raise ValueError(f"{what}: the activations differ in size")
-    if any(t is not None and t.numel() != d for t in columns):
-        raise ValueError(f"{what}: a gain must hold one value a column")
-    if any(t is not None and t.numel() != rows for t in per_row):
-        raise ValueError(f"{what}: rstd_post and rstd_pre must hold one value a row")
+    n = rows * d
+    for t in same:
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{what}: the activations differ in size")
+    for t in columns:
+        if t is not None and t.numel() != d:
+            raise ValueError(f"{what}: a gain must hold one value a column")
+    for t in per_row:
+        if t is not None and t.numel() != rows:
+            raise ValueError(f"{what}: rstd_post and rstd_pre must hold one value a row")
     if gate is None:
         return rows, d, 1
     gates = gate.numel() // d
@@ -637,17 +656,16 @@ def norm_residual(x, y, z, h=None, post_gain=None, gate=None, pre_gain=None,
     """z = residual_scale * x + gate * dropout(norm(y) * post_gain) and
     h = norm(z) * pre_gain. x, y, z, h: [..., d] of one dtype; gains [d], gate
     [gates, d] or [d], rstd_post and rstd_pre (one value a row) float32."""
-    torch = _torch()
     rows, d, gates = _norm_shape(y, "norm_residual", (x, z, h), gate, (post_gain, pre_gain),
                                  (rstd_post, rstd_pre))
-    f32 = torch.float32
     cur = _current_device()
-    _check(load().norm_residual(
-        _at(x, y.dtype, "x", cur), _at(y, y.dtype, "y", cur), _dtype(y, "y"), rows, d,
-        _at(post_gain, f32, "post_gain", cur), _at(gate, f32, "gate", cur), gates,
-        _at(pre_gain, f32, "pre_gain", cur), float(residual_scale), float(eps), float(p), _u64(seed),
-        _worker(worker), _step(step, cur), _at(z, y.dtype, "z", cur), _at(h, y.dtype, "h", cur),
-        _at(rstd_post, f32, "rstd_post", cur), _at(rstd_pre, f32, "rstd_pre", cur), _stream(stream)))
+    code = _dtype(y, "y")
+    xp, yp, zp, hp = _ats(cur, y.dtype, "x y z h", x, y, z, h)
+    post, gp, pre, rp, rz = _ats(cur, _torch().float32, "post_gain gate pre_gain rstd_post rstd_pre",
+                                 post_gain, gate, pre_gain, rstd_post, rstd_pre)
+    _check(load().norm_residual(xp, yp, code, rows, d, post, gp, gates, pre, residual_scale, eps, p,
+                                _u64(seed), _worker(worker), _step(step, cur), zp, hp, rp, rz,
+                                _stream(stream)))
 
 
 def norm_residual_grad_ws_bytes(rows: int, d: int, gates: int = 1) -> int:
@@ -671,18 +689,18 @@ def norm_residual_grad(z, y, dx, dy, ws, dz=None, dh=None, post_gain=None, gate=
                                  (rstd_post, rstd_pre))
     if dgate is not None and (gate is None or dgate.numel() != gate.numel()):
         raise ValueError("norm_residual_grad: dgate differs from gate in size")
-    f32 = torch.float32
     size = _ws(ws, "norm_residual_grad")
     cur = _current_device()
+    code = _dtype(y, "y")
+    zp, yp, dzp, dhp, dxp, dyp = _ats(cur, y.dtype, "z y dz dh dx dy", z, y, dz, dh, dx, dy)
+    post, gp, pre, rp, rz, dpost, dgp, dpre = _ats(
+        cur, torch.float32,
+        "post_gain gate pre_gain rstd_post rstd_pre dpost_gain dgate dpre_gain", post_gain, gate,
+        pre_gain, rstd_post, rstd_pre, dpost_gain, dgate, dpre_gain)
     _check(load().norm_residual_grad(
-        _at(z, y.dtype, "z", cur), _at(y, y.dtype, "y", cur), _dtype(y, "y"), rows, d,
-        _at(post_gain, f32, "post_gain", cur), _at(gate, f32, "gate", cur), gates,
-        _at(pre_gain, f32, "pre_gain", cur), float(residual_scale), float(p), _u64(seed),
-        _worker(worker), _step(step, cur), _at(rstd_post, f32, "rstd_post", cur),
-        _at(rstd_pre, f32, "rstd_pre", cur), _at(dz, y.dtype, "dz", cur), _at(dh, y.dtype, "dh", cur),
-        _at(dx, y.dtype, "dx", cur), _at(dy, y.dtype, "dy", cur), _at(dpost_gain, f32, "dpost_gain", cur),
-        _at(dgate, f32, "dgate", cur), _at(dpre_gain, f32, "dpre_gain", cur), _at(ws, torch.uint8, "ws", cur),
-        ctypes.byref(size), _stream(stream)))
+        zp, yp, code, rows, d, post, gp, gates, pre, residual_scale, p, _u64(seed),
+        _worker(worker), _step(step, cur), rp, rz, dzp, dhp, dxp, dyp, dpost, dgp, dpre,
+        _at(ws, torch.uint8, "ws", cur), ctypes.byref(size), _stream(stream)))
 
 
 def _dtype_code(dtype) -> int:
