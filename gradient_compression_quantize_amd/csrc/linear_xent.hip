@@ -42,6 +42,12 @@ __device__ __forceinline__ float exp_neg(float x)
     return r == 0.0f ? 0.0f : __builtin_fmaf(r, lo * kLn2, r);
 }
 
+// 2^(ref - x log2 e) for ref = x log2 e rounded to fp32.
+__device__ __forceinline__ float rounding_factor(float x, float ref)
+{
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(-x, kLog2e, ref));
+}
+
 // Whether row n has a target among the rows of the vocabulary.
 __device__ __forceinline__ bool has_target(const int64_t* target, size_t n, int64_t ignore, size_t V)
 {
@@ -297,8 +303,9 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
             for (int e = 0; e < 16; ++e)
                 top = fmaxf(top, acc.v[i][j][e]);
         top = fmaxf(top, __shfl_xor(top, 32));
-        // exp(l - top) = 2^(l log2 e - top log2 e); a part that holds no logit
-        // above -inf adds nothing
+        // exp(l - top) = 2^(l log2 e - ref) 2^(ref - top log2 e): what rounding
+        // ref leaves, up to 2^-24 |top|, goes back in as one factor of the sum.
+        // A part that holds no logit above -inf adds nothing.
         const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
         float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -308,12 +315,15 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
                 sums[e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][e], kLog2e, -ref));
         float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
         sum += __shfl_xor(sum, 32);
+        sum *= top == -INFINITY ? 1.0f : rounding_factor(top, ref);
         if (lane < 32 && n < N)
             parts[size_t(n) * nparts + part0 + ta * WA + wa] = LossPart{top, sum};
     }
 }
 
-// One wave for each token joins the parts of its row.
+// One wave for each token joins the parts of its row. The loss of a token whose
+// target leads is log(sum) with a sum near 1, far below lse: the target's logit
+// is taken from the maximum, before the logarithm's bits are lost in lse.
 constexpr int kJoinThreads = 256;
 
 __global__ __launch_bounds__(kJoinThreads) void loss_join_kernel(
@@ -339,12 +349,13 @@ __global__ __launch_bounds__(kJoinThreads) void loss_join_kernel(
             top = both;
         }
         if (lane == 0) {
-            const float all = top + logf(sum);
-            lse[n] = all;
+            // (the sum holds exp(0), whatever its rounding left of it)
+            const float rest = logf(sum < 1.0f ? 1.0f : sum);
+            lse[n] = top + rest;
             const int64_t t = target[n];
             float x = 0.0f;
             if (t != ignore)
-                x = t >= 0 && t < int64_t(V) ? all - target_logit[n]
+                x = t >= 0 && t < int64_t(V) ? (top - target_logit[n]) + rest
                                              : std::numeric_limits<float>::quiet_NaN();
             loss[n] = x;
         }

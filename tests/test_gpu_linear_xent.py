@@ -501,3 +501,38 @@ def test_offsets_past_32_bits(gcq):
     assert bool(((dh.double() - rh).abs() <= eh + rh.abs() * 1.01 * 2.0 ** -8).all())
     del w, dw
     torch.cuda.empty_cache()
+
+
+def leading(t, base, N=12, V=400):
+    """Logits that are exact in every type: base plus sixteenths, one of each
+    row some 10 to 15 above the others. Returns inputs, logits, leaders."""
+    g = torch.Generator().manual_seed(17)
+    x = torch.randint(0, 32, (V, N), generator=g).double() / 16
+    lead = torch.randint(0, V, (N,), generator=g)
+    x[lead, torch.arange(N)] = torch.randint(192, 256, (N,), generator=g).double() / 16
+    w = torch.cat([torch.full((V, 1), float(base), dtype=torch.float64), x], dim=1).to(t)
+    h = torch.cat([torch.ones(N, 1), torch.eye(N)], dim=1).to(t)
+    l = h.double() @ w.double().t()
+    assert torch.equal(l.float().double(), l) and torch.equal(w.double()[:, 1:], x)
+    return h, w, l, lead
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+@pytest.mark.parametrize("base", [0, 960, -960, 32768])
+def test_loss_of_a_leading_target(gcq, t, base):
+    """log(sum) with a sum near 1 is the loss of a confident token, whatever
+    the size of its lse. The sum of at most 16 + 3 + 7 rounded additions, the
+    leader's exponential and factors (6 steps), log's own steps and those of
+    the small terms (some 25 of at most 0.02): 40 F."""
+    announce(f"linear_xent_loss of leading targets {t} {base}")
+    h, w, l, lead = leading(t, base)
+    y = lead.clone()
+    y[::4] = (y[::4] + 1) % w.shape[0]  # and some that do not lead
+    loss, lse = run_loss(gcq, h, w, y)
+    top = l.max(dim=1, keepdim=True).values
+    ref = (top - l.gather(1, y[:, None]))[:, 0] + (l - top).exp().sum(1).log()
+    assert float(ref[1::4].max()) < 0.02
+    assert bool(((loss.double() - ref).abs() <= 40 * po.F32 + 4 * po.F32 * ref.abs()).all())
+    ref_lse = torch.logsumexp(l, dim=1)
+    assert bool(((lse.double() - ref_lse).abs() <= 40 * po.F32 + 1.01 * po.F32 * ref_lse.abs()).all())
+    assert bool((loss >= 0).all())
