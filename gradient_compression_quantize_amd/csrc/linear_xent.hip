@@ -42,12 +42,6 @@ __device__ __forceinline__ float exp_neg(float x)
     return r == 0.0f ? 0.0f : __builtin_fmaf(r, lo * kLn2, r);
 }
 
-// 2^(ref - x log2 e) for ref = x log2 e rounded to fp32.
-__device__ __forceinline__ float rounding_factor(float x, float ref)
-{
-    return __builtin_amdgcn_exp2f(__builtin_fmaf(-x, kLog2e, ref));
-}
-
 // Whether row n has a target among the rows of the vocabulary.
 __device__ __forceinline__ bool has_target(const int64_t* target, size_t n, int64_t ignore, size_t V)
 {
@@ -303,19 +297,19 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
             for (int e = 0; e < 16; ++e)
                 top = fmaxf(top, acc.v[i][j][e]);
         top = fmaxf(top, __shfl_xor(top, 32));
-        // exp(l - top) = 2^(l log2 e - ref) 2^(ref - top log2 e): what rounding
-        // ref leaves, up to 2^-24 |top|, goes back in as one factor of the sum.
-        // A part that holds no logit above -inf adds nothing.
-        const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
+        // exp(l - top) = 2^((l - top) log2 e). The difference comes first: l log2
+        // e - top log2 e in one fma is off by the rounding of the second, 2^-24
+        // |top| of the sum, and by everything past |top| = 1e9. A part that
+        // holds no logit above -inf adds nothing.
+        const float ref = top == -INFINITY ? 0.0f : top;
         float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < P::RA; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                sums[e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][e], kLog2e, -ref));
+                sums[e & 3] += __builtin_amdgcn_exp2f((acc.v[i][j][e] - ref) * kLog2e);
         float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
         sum += __shfl_xor(sum, 32);
-        sum *= top == -INFINITY ? 1.0f : rounding_factor(top, ref);
         if (lane < 32 && n < N)
             parts[size_t(n) * nparts + part0 + ta * WA + wa] = LossPart{top, sum};
     }

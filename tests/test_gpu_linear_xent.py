@@ -536,3 +536,23 @@ def test_loss_of_a_leading_target(gcq, t, base):
     ref_lse = torch.logsumexp(l, dim=1)
     assert bool(((lse.double() - ref_lse).abs() <= 40 * po.F32 + 1.01 * po.F32 * ref_lse.abs()).all())
     assert bool((loss >= 0).all())
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("base", [2.0 ** 34, -2.0 ** 34, 2.0 ** 62, -2.0 ** 62, 2.0 ** 126])
+def test_logits_of_any_size(gcq, t, base):
+    """Logits far beyond those whose exponential's argument still has bits of
+    its own: one leads by 2^-6 of the others' size, so that its probability is 1."""
+    announce(f"linear_xent_loss of logits of {base} {t}")
+    N, V, D = 5, 300, 8
+    h, w = torch.ones(N, D).to(t), torch.full((V, D), base / D).to(t)
+    lead = torch.tensor([0, 17, 128, 255, 299])
+    for n in range(N):
+        h[n] = 0
+        h[n, n] = D
+    w[lead, torch.arange(N)] += base / D / 64 if base > 0 else -base / D / 64
+    l = h.double() @ w.double().t()
+    loss, lse = run_loss(gcq, h, w, lead)
+    assert torch.equal(lse.double(), l.max(dim=1).values) and bool((loss == 0).all())
+    loss, lse = run_loss(gcq, h, w, (lead + 1) % V)
+    assert torch.equal(loss.double(), (l.max(dim=1).values - base))
