@@ -408,15 +408,15 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
             z = live ? lse[n] : 0.0f;
             d = live ? dloss[n] : 0.0f;
         }
-        // p. In one plane in the end, it takes one rounding of (l - lse)
-        // log2 e: 2^-24 of it, some 1e-6 of p
-        const float zl = z * kLog2e;
+        // p, from the difference l - lse: its error goes by that, and not by the
+        // size of lse. In one plane in the end, p takes two roundings of (l -
+        // lse) log2 e, 2^-24 of it each, some 1e-6 of p
 #pragma unroll
         for (int i = 0; i < P::RA; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const float l = kF16 ? __builtin_amdgcn_ldexpf(acc.v[i][j][e], back) : acc.v[i][j][e];
-                acc.v[i][j][e] = kPlanes == 1 ? __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2e, -zl)) : exp_neg(l - z);
+                acc.v[i][j][e] = kPlanes == 1 ? __builtin_amdgcn_exp2f((l - z) * kLog2e) : exp_neg(l - z);
             }
         if (__any(at < uint32_t(L::kRowsA))) {
 #pragma unroll

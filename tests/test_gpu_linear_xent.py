@@ -556,3 +556,30 @@ def test_logits_of_any_size(gcq, t, base):
     assert torch.equal(lse.double(), l.max(dim=1).values) and bool((loss == 0).all())
     loss, lse = run_loss(gcq, h, w, (lead + 1) % V)
     assert torch.equal(loss.double(), (l.max(dim=1).values - base))
+
+
+@pytest.mark.parametrize("types", CASES, ids=lambda c: "-".join(str(t)[6:] for t in c))
+@pytest.mark.parametrize("base", [0, 960, 32768])
+def test_grad_of_a_leading_target(gcq, types, base):
+    """p - 1 of a confident token, whatever the size of its lse. Each token has
+    a channel of its own, h = 1 in it: dweight is G there. p is off by the
+    exponential's argument (|l - lse| < 24: two half steps of it), 2 steps of
+    exp and one of the difference: 60 F of p for l far below, 8 F of p at the
+    target, where |l - lse| < 1; then G's rounding and the output's."""
+    t, th, tw = types
+    announce(f"linear_xent_grad of leading targets {types} {base}")
+    h, w, l, lead = leading(t, base)
+    N, V = h.shape[0], w.shape[0]
+    lse = torch.logsumexp(l, dim=1).float()
+    d = torch.ones(N)
+    dh, dw = run_grad(gcq, h, w, lead, lse, d, th, tw)
+    p = (l - lse.double()[:, None]).exp()
+    assert float(p.gather(1, lead[:, None]).min()) > 0.5
+    g = p.clone()
+    g[torch.arange(N), lead] -= 1.0
+    rounding = 2.0 ** -22 if tw == torch.float32 else po.HALF_STEP[t] if th == t == tw else 2.0 ** -11
+    off = (dw.double()[:, 1:].t() - g).abs()
+    # (a p of 1e-7 is subnormal in fp16, a multiple of 2^-24: off by half of that)
+    allowed = 60 * po.F32 * p + g.abs() * (1.01 * rounding + 1.01 * po.HALF_STEP[tw]) + 2.0 ** -38 + po.TINY[tw]
+    allowed[torch.arange(N), lead] += 8 * po.F32
+    assert bool((off <= allowed).all()), float((off / allowed).max())
