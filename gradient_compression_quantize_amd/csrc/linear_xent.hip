@@ -71,6 +71,15 @@ __device__ __forceinline__ void load8(const T* row, size_t c, size_t d, float (&
         v[k] = c + k < d ? float(row[c + k]) : 0.0f;
 }
 
+// max(m, |x|) over the finite ones of eight values
+__device__ __forceinline__ float largest_finite(float m, const float (&v)[8])
+{
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        m = fabsf(v[k]) <= std::numeric_limits<float>::max() ? fmaxf(m, fabsf(v[k])) : m;
+    return m;
+}
+
 // What the scale of a matrix goes by: the largest finite |x| of its rows (of
 // those with a target, if `target` is not NULL), a maximum for each workgroup.
 constexpr unsigned kMaxParts = 1024;
@@ -119,9 +128,7 @@ __device__ __forceinline__ void largest(const MaxOf& a, int64_t ignore, size_t V
         for (size_t c = lane * 8; c < a.d; c += kWave * 8) {
             float v[8];
             load8(row, c, a.d, v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                m = fabsf(v[k]) <= std::numeric_limits<float>::max() ? fmaxf(m, fabsf(v[k])) : m;
+            m = largest_finite(m, v);
         }
     }
     m = workgroup_max(m);
@@ -142,11 +149,12 @@ __global__ __launch_bounds__(kRowThreads) void largest_kernel(MaxOfAll all, int6
 }
 
 // src [rows][d] -> planes [rows_out][d_out] (d_out a multiple of 8), one
-// behind the other, of bf16 as it is or of fp16, scaled where `parts` is not
-// NULL so that the largest value comes to [2^14, 2^15); zeros behind the last
-// column and row, and in the rows that have no target if `target` is not NULL:
-// what such rows hold, NaN included, reaches nothing. One wave a row. Without
-// an `out` only the exponent is set.
+// behind the other, of bf16 as it is or of fp16, scaled so that the largest
+// finite value comes to [2^14, 2^15): that of the matrix where `parts` is not
+// NULL, that of each row, with an exponent of its own, where by_row is set.
+// Zeros behind the last column and row, and in the rows that have no target if
+// `target` is not NULL: what such rows hold, NaN included, reaches nothing. One
+// wave a row. Without an `out` only the exponent is set.
 struct PlanesOf {
     const void* src;
     size_t rows, d;
@@ -155,8 +163,12 @@ struct PlanesOf {
     const int64_t* target;
     const float* parts;
     unsigned nparts;
-    int* exponent;
+    int* exponent;  // one, or one a row
+    bool by_row;
 };
+
+// The power of two that brings m, the largest value, to [2^14, 2^15).
+__device__ __forceinline__ int exponent_for(float m) { return m > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(m) : 0; }
 
 struct PlanesOfAll {
     PlanesOf of[3];
@@ -174,7 +186,7 @@ __global__ __launch_bounds__(kRowThreads) void planes_kernel(PlanesOfAll all, in
         for (unsigned k = threadIdx.x; k < a.nparts; k += kRowThreads)
             m = fmaxf(m, a.parts[k]);
         m = workgroup_max(m);
-        scale = m > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(m) : 0;
+        scale = exponent_for(m);
         if (blockIdx.x == 0 && threadIdx.x == 0)
             *a.exponent = scale;
     }
@@ -185,6 +197,20 @@ __global__ __launch_bounds__(kRowThreads) void planes_kernel(PlanesOfAll all, in
     for (size_t r = size_t(blockIdx.x) * kRowWaves + threadIdx.x / kWave; r < a.rows_out;
          r += size_t(gridDim.x) * kRowWaves) {
         const bool live = r < a.rows && (!a.target || has_target(a.target, r, ignore, V));
+        if (kF16 && a.by_row) {
+            float m = 0.0f;
+            for (size_t c = lane * 8; live && c < a.d; c += kWave * 8) {
+                float v[8];
+                load8(src + r * a.d, c, a.d, v);
+                m = largest_finite(m, v);
+            }
+#pragma unroll
+            for (int off = kWave / 2; off > 0; off >>= 1)
+                m = fmaxf(m, __shfl_xor(m, off));
+            scale = exponent_for(m);
+            if (lane == 0)
+                a.exponent[r] = scale;
+        }
 #pragma unroll 2
         for (size_t c = lane * 8; c < a.d_out; c += kWave * 8) {
             float v[8] = {};
@@ -212,10 +238,11 @@ __global__ __launch_bounds__(kRowThreads) void planes_kernel(PlanesOfAll all, in
     }
 }
 
-// What sums of products of scaled operands are multiplied by, as an exponent.
-__device__ __forceinline__ int unscale(const MatOperand& a, const MatOperand& b)
+// What sums of products of scaled operands are multiplied by, as an exponent:
+// of row n of b, if its rows have exponents of their own.
+__device__ __forceinline__ int unscale(const MatOperand& a, const MatOperand& b, uint32_t n = 0)
 {
-    return -((a.exponent ? *a.exponent : 0) + (b.exponent ? *b.exponent : 0));
+    return -((a.exponent ? *a.exponent : 0) + (b.exponent ? b.exponent[b.by_row ? n : 0] : 0));
 }
 
 // ---- tiles of the logits -------------------------------------------------------
@@ -257,7 +284,7 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void loss_tiles_kernel(
         const uint32_t n = tb * TB + wb * L::kRowsB + j * 32 + acc_col(lane);
         const int64_t t = n < N ? target[n] : -1;
         if (kF16) {
-            const int back = unscale(weight, hidden);
+            const int back = unscale(weight, hidden, min(n, N - 1));
 #pragma unroll
             for (int i = 0; i < P::RA; ++i)
 #pragma unroll
@@ -655,17 +682,19 @@ bool direct_ok(const void* p, size_t D, const Mode& m) { return !m.scaled && D %
 struct PlaneRoom {
     size_t rows, d, off, parts, exponent;
     int planes;
+    bool by_row;  // each row has a scale of its own
 };
 
-PlaneRoom plane_room(Carver& c, size_t rows, size_t D, const Mode& m)
+PlaneRoom plane_room(Carver& c, size_t rows, size_t D, const Mode& m, bool by_row = false)
 {
     PlaneRoom r{};
     r.rows = rows;
     r.d = round_up(D, kTurnK);
     r.planes = m.planes;
     r.off = c.take(r.planes * rows * r.d * 2);
-    r.parts = c.take(kMaxParts * sizeof(float));
-    r.exponent = c.take(sizeof(int));
+    r.by_row = by_row;
+    r.parts = c.take(by_row ? 0 : kMaxParts * sizeof(float));
+    r.exponent = c.take((by_row ? rows : 1) * sizeof(int));
     return r;
 }
 
@@ -727,13 +756,13 @@ struct Preparation {
 };
 
 // Describes src as an operand by rows: as it is, or as planes in the workspace
-// that `prep` is to lay out. Of rows without a target (`target` not NULL) the
-// scale takes no notice, and with `drop` they become zeros.
+// that `prep` is to lay out. With a `target`, rows that have none become zeros
+// and the scale takes no notice of them.
 MatOperand make_operand(Preparation& prep, const void* src, size_t rows, size_t D, const Mode& mode, int dtype,
-                        const PlaneRoom& room, char* ws, const int64_t* target, bool drop)
+                        const PlaneRoom& room, char* ws, const int64_t* target)
 {
     MatOperand m{};
-    if (!drop && direct_ok(src, D, mode)) {
+    if (!target && direct_ok(src, D, mode)) {
         m.plane0 = static_cast<const uint16_t*>(src);
         m.ld = uint32_t(D);
         m.extent = uint32_t(rows);
@@ -741,15 +770,16 @@ MatOperand make_operand(Preparation& prep, const void* src, size_t rows, size_t 
     }
     uint16_t* out = reinterpret_cast<uint16_t*>(ws + room.off);
     int* exponent = mode.scaled ? reinterpret_cast<int*>(ws + room.exponent) : nullptr;
-    if (mode.scaled)
+    const bool by_row = mode.scaled && room.by_row, whole = mode.scaled && !by_row;
+    if (whole)
         prep.scale_by(src, dtype == GC_F32, rows, D, target, reinterpret_cast<float*>(ws + room.parts));
-    prep.lay_out(PlanesOf{src, rows, D, out, room.rows, room.d, drop ? target : nullptr, nullptr, 0, exponent},
-                 mode.scaled);
+    prep.lay_out(PlanesOf{src, rows, D, out, room.rows, room.d, target, nullptr, 0, exponent, by_row}, whole);
     m.plane0 = out;
     m.plane_stride = room.rows * room.d;
     m.ld = uint32_t(room.d);
     m.extent = uint32_t(room.rows);
     m.exponent = exponent;
+    m.by_row = by_row;
     return m;
 }
 
@@ -820,7 +850,8 @@ LossLayout loss_layout(size_t N, size_t V, size_t D, int dtype)
     L.mode = mode_of(dtype, dtype != GC_BF16);
     L.plan = logit_plan(N, V, true);
     L.weight = plane_room(c, V, D, L.mode);
-    L.hidden = plane_room(c, N, D, L.mode);
+    // a scale for each token, so that none costs another one bits
+    L.hidden = plane_room(c, N, D, L.mode, true);
     for (int k = 0; k < L.plan.count; ++k)
         L.nparts += L.plan.range[k].tiles_a() * kLogitWavesA;
     L.parts = c.take(N * L.nparts * sizeof(LossPart));
@@ -1043,8 +1074,8 @@ GCQ_API int linear_xent_loss(const void* hidden, const void* weight, int dtype, 
         return fail(GC_EINVAL, "linear_xent_loss: workspace too small or not 16-byte aligned");
     char* w = static_cast<char*>(ws);
     Preparation prep;
-    const MatOperand wo = make_operand(prep, weight, V, D, L.mode, dtype, L.weight, w, nullptr, false);
-    const MatOperand ho = make_operand(prep, hidden, N, D, L.mode, dtype, L.hidden, w, target, false);
+    const MatOperand wo = make_operand(prep, weight, V, D, L.mode, dtype, L.weight, w, nullptr);
+    const MatOperand ho = make_operand(prep, hidden, N, D, L.mode, dtype, L.hidden, w, nullptr);
     prep.launch(dtype, L.mode, ignore_index, V, stream);
     ProductShape sh{};
     sh.turns = uint32_t(round_up(D, kTurnK) / kTurnK);
@@ -1122,15 +1153,15 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
 
     char* w = static_cast<char*>(ws);
     Preparation prep;
-    const MatOperand wo = make_operand(prep, weight, V, D, L.mode, dtype, L.weight, w, nullptr, false);
+    const MatOperand wo = make_operand(prep, weight, V, D, L.mode, dtype, L.weight, w, nullptr);
     // always a copy: rows without a target become zeros
-    const MatOperand ho = make_operand(prep, hidden, N, D, L.mode, dtype, L.hidden, w, target, true);
+    const MatOperand ho = make_operand(prep, hidden, N, D, L.mode, dtype, L.hidden, w, target);
     GradOut g{};
     MatOperand go{};
     if (L.mode.f16) {
         int* exponent = reinterpret_cast<int*>(w + L.g_exponent);
         prep.scale_by(dloss, true, N, 1, target, reinterpret_cast<float*>(w + L.g_parts));
-        prep.lay_out(PlanesOf{nullptr, 0, 0, nullptr, 0, 0, nullptr, nullptr, 0, exponent}, true);
+        prep.lay_out(PlanesOf{nullptr, 0, 0, nullptr, 0, 0, nullptr, nullptr, 0, exponent, false}, true);
         go.exponent = g.exponent = exponent;
     }
     prep.launch(dtype, L.mode, ignore_index, V, stream);

@@ -62,6 +62,7 @@ struct MatOperand {
     uint32_t krows;   // by k: rows that may be read (what lies past them reads the last one again, against
                       // zeros of the other operand)
     const int* exponent;  // values are held times 2^exponent; NULL: 0
+    bool by_row;          // row r times 2^exponent[r]
 };
 
 struct ProductShape {

@@ -391,10 +391,10 @@ int norm_residual_grad(const void* z, const void* y, int dtype, size_t rows, siz
  * and sum of their part of the vocabulary. bf16 and fp16 inputs are
  * multiplied as they are; an fp32 value x as two fp16 values that hold it to
  * 2^-22 of x or 2^-37 of the largest finite one of its matrix (of hidden: of
- * the rows that have a target), whichever is more. Sums are fp32.
+ * its row), whichever is more. Sums are fp32.
  *   hidden  [N, D], weight [V, D] of `dtype`, rows contiguous
- *   target  [N] int64;  loss, lse [N] fp32 (lse is written for every row; of
- *           fp32 inputs only rows that have a target get one to rely on)
+ *   target  [N] int64;  loss, lse [N] fp32 (lse of every row, with a target or
+ *           without)
  *   ws      16-byte-aligned workspace; ws == NULL: *ws_bytes is set to the
  *           size needed for (N, V, D, dtype) and nothing is enqueued.
  *           Otherwise *ws_bytes is its size and must be at least that.

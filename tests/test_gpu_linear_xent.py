@@ -583,3 +583,32 @@ def test_grad_of_a_leading_target(gcq, types, base):
     allowed = 60 * po.F32 * p + g.abs() * (1.01 * rounding + 1.01 * po.HALF_STEP[tw]) + 2.0 ** -38 + po.TINY[tw]
     allowed[torch.arange(N), lead] += 8 * po.F32
     assert bool((off <= allowed).all()), float((off / allowed).max())
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+def test_lse_of_rows_without_a_target(gcq, t):
+    """Padded rows some times larger than the others have an lse like any
+    other row, and no row's size costs another one bits."""
+    announce(f"linear_xent_loss lse of padded rows {t}")
+    N, V, D = 80, 300, 96
+    h, w, y, _ = inputs(N, V, D, t, seed=12, ignore=0.0)
+    y[::3] = IGNORE
+    want = run_loss(gcq, h, w, y)
+    for k in (2, 4, 7):
+        big = h.clone()
+        big[::3] = torch.ldexp(h[::3].float(), torch.tensor(k)).to(t)
+        loss, lse = run_loss(gcq, big, w, y)
+        rest = torch.arange(N) % 3 != 0
+        assert torch.equal(loss[rest], want[0][rest]) and torch.equal(lse[rest], want[1][rest])
+        for n in range(0, N, 3):  # each with the bounds of its own size
+            ref, ref_lse, e = plain_loss(big[n:n + 1], w, y[n:n + 1])
+            check_loss(loss[n:n + 1], lse[n:n + 1], ref, ref_lse, e)
+    # of a token with a target too, however large
+    if t != torch.float16:
+        big = h.clone()
+        big[1] = torch.ldexp(h[1].float(), torch.tensor(60)).to(t)
+        loss, lse = run_loss(gcq, big, w, y)
+        rest = torch.arange(N) != 1
+        assert torch.equal(loss[rest], want[0][rest]) and torch.equal(lse[rest], want[1][rest])
+        ref, ref_lse, e = plain_loss(big[1:2], w, y[1:2])
+        check_loss(loss[1:2], lse[1:2], ref, ref_lse, e)
