@@ -659,7 +659,8 @@ int check_sizes(const char* what, size_t N, size_t V, size_t D, int dtype)
 // How a call computes. bf16 operands are multiplied as they are where no more
 // is asked than 16 bits of a gradient; everything else in fp16: fp16 inputs as
 // they are, others scaled by a power of two, fp32 ones in two planes. (fp16
-// holds a bf16 value exactly down to 2^-29 of the largest one of the matrix.)
+// holds a bf16 value exactly down to 2^-31 of the largest one of the matrix,
+// and to 2^-39 of that one below.)
 struct Mode {
     bool f16;       // matrix products in fp16
     bool scaled;    // inputs scaled, from copies
@@ -880,7 +881,7 @@ struct GradLayout {
     Mode mode;
     PlaneRoom weight, hidden;
     size_t n_pad, piece, pieces;  // rows of G, vocabulary of one piece
-    int g_planes;
+    int g_planes, h_planes, w_planes;  // of G: in memory, in each product
     size_t g, g_parts, g_exponent, h_slab, w_slab, total;
     size_t d4;  // row length of the slabs
     ProductPlan h, w;
@@ -911,10 +912,15 @@ ProductPlan product_plan(size_t rows, size_t D, size_t turns)
 // gradient is rounded to as well, or two.
 int g_planes(int dtype) { return dtype == GC_F32 ? 2 : 1; }
 
-ProductShape grad_shape(int planes_a, int out_dtype)
+// Planes for dweight. One plane of fp16 ends at 2^-39 of the largest |dloss|,
+// far above what a bf16 dweight holds of the rows of rare tokens: next to an
+// fp32 dhidden, for which both planes are there, it takes both.
+int w_planes(const Mode& m, int dtype, int dw_dtype) { return dtype == GC_BF16 && m.f16 ? 2 : g_planes(dw_dtype); }
+
+ProductShape grad_shape(int planes_a, int planes_g)
 {
     ProductShape sh{};
-    set_pairs(sh, planes_a, g_planes(out_dtype));
+    set_pairs(sh, planes_a, planes_g);
     return sh;
 }
 
@@ -963,9 +969,11 @@ GradLayout grad_layout(size_t N, size_t V, size_t D, int dtype, int dh_dtype, in
     L.n_pad = round_up(N, kTurnK);
     L.hidden = plane_room(c, L.n_pad, D, L.mode);
     L.d4 = round_up(D, 4);
-    L.g_planes = std::max(g_planes(dh_dtype), g_planes(dw_dtype));
-    const size_t h_turns = kTile / kTurnK * grad_shape(L.weight.planes, dh_dtype).segments;  // of a tile of the vocabulary
-    const size_t w_turns = L.n_pad / kTurnK * grad_shape(L.hidden.planes, dw_dtype).segments;
+    L.h_planes = g_planes(dh_dtype);
+    L.w_planes = w_planes(L.mode, dtype, dw_dtype);
+    L.g_planes = std::max(L.h_planes, L.w_planes);
+    const size_t h_turns = kTile / kTurnK * grad_shape(L.weight.planes, L.h_planes).segments;  // of a tile of the vocabulary
+    const size_t w_turns = L.n_pad / kTurnK * grad_shape(L.hidden.planes, L.w_planes).segments;
     const size_t most = std::min(std::max<size_t>(kPieceBytes / (L.n_pad * 2 * L.g_planes * kTile), 1), kMaxPiece / kTile);
     L.piece = piece_tiles(most, N, V, D, h_turns, w_turns) * kTile;
     L.pieces = ceil_div(V, L.piece);
@@ -1218,7 +1226,7 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
             A.extent = uint32_t(wo.ld);
             A.krows = uint32_t(vp);
             B.extent = uint32_t(N);
-            ProductShape ps = grad_shape(L.weight.planes, dhidden_dtype);
+            ProductShape ps = grad_shape(L.weight.planes, L.h_planes);
             ps.turns = uint32_t(ceil_div(vp, kTurnK));
             ps.splits = L.h.splits;
             if (h_direct) {
@@ -1233,7 +1241,7 @@ GCQ_API int linear_xent_grad(const void* hidden, const void* weight, int dtype, 
             A.extent = uint32_t(ho.ld);
             A.krows = B.krows = uint32_t(L.n_pad);
             B.extent = uint32_t(L.piece);
-            ProductShape ps = grad_shape(L.hidden.planes, dweight_dtype);
+            ProductShape ps = grad_shape(L.hidden.planes, L.w_planes);
             ps.turns = uint32_t(L.n_pad / kTurnK);
             ps.splits = L.w.splits;
             char* out = static_cast<char*>(dweight) + v0 * D * dtype_bytes(dweight_dtype);

@@ -13,11 +13,12 @@
 // Precision: an operand of more than 11 significant bits is held as two planes
 // of fp16, x = p0 + 2^-11 p1, p0 the rounding of x (off by at most 2^-11 of it)
 // and p1 that of the rest times 2^11: together they are within 2^-22 of x, as
-// long as x is within 2^-29 of the largest value (the caller scales that to
-// about 2^15), and within 2^-37 of the largest value below. A product then
-// runs over segments, one for each pair of planes: first those of one p1,
-// whose sum is then multiplied by 2^-11, then p0 p0. The pair of two p1, at
-// most 2^-22 of a term, is left out.
+// long as x is within 2^-28 of the largest value (which the caller scales to
+// [2^14, 2^15)), and below that within 2^-50 of the largest value (half of
+// 2^-24, the smallest fp16, times 2^-11). A product then runs over segments,
+// one for each pair of planes: first those of one p1, whose sum is then
+// multiplied by 2^-11, then p0 p0. The pair of two p1, at most 2^-22 of a term,
+// is left out.
 //
 // A workgroup of WA x WB waves owns a tile of TA x TB outputs. k advances in
 // stages of 32 values of both operands, moved straight into LDS

@@ -390,7 +390,7 @@ int norm_residual_grad(const void* z, const void* y, int dtype, size_t rows, siz
  * The logits are never kept: tiles of the product end in a running maximum
  * and sum of their part of the vocabulary. bf16 and fp16 inputs are
  * multiplied as they are; an fp32 value x as two fp16 values that hold it to
- * 2^-22 of x or 2^-37 of the largest finite one of its matrix (of hidden: of
+ * 2^-22 of x or 2^-50 of the largest finite one of its matrix (of hidden: of
  * its row), whichever is more. Sums are fp32.
  *   hidden  [N, D], weight [V, D] of `dtype`, rows contiguous
  *   target  [N] int64;  loss, lse [N] fp32 (lse of every row, with a target or
@@ -417,11 +417,15 @@ int linear_xent_loss(const void* hidden, const void* weight, int dtype, size_t N
  *   dhidden     [N, D] of dhidden_dtype, or NULL: not computed
  *   dweight     [V, D] of dweight_dtype, or NULL: not computed
  *   a gradient's type is the inputs' or fp32, and says how exactly it is
- *   computed. G is rounded to the 16 bits of a gradient of 16 bits on its way
- *   into the product; for an fp32 one it is held to 2^-22 of itself or 2^-37
- *   of the largest |dloss|, whichever is more, and inputs of fp32 as in
- *   linear_xent_loss (bf16 ones are exact to 2^-39 of their largest). An fp32
- *   dweight is what compress_2bit and qsgd_maxnorm_quantize take.
+ *   computed. With everything in bf16, G is rounded to bf16 on its way into
+ *   the products, 2^-8 of itself however small it is. Otherwise it is held
+ *   scaled by the largest |dloss|, m: for a gradient of 16 bits to 2^-11 of
+ *   itself or 2^-39 m, for an fp32 one, and a bf16 dweight next to an fp32
+ *   dhidden, to 2^-22 of itself or 2^-50 m, whichever is more. Inputs of fp32
+ *   are held as in linear_xent_loss, with one scale for all tokens that have a
+ *   target; bf16 ones next to an fp32 gradient are exact to 2^-39 of their
+ *   largest. An fp32 dweight is what compress_2bit and qsgd_maxnorm_quantize
+ *   take.
  *   ws          as in linear_xent_loss. The query asks by the types alone.
  * N may be 0: dweight is then zero. */
 int linear_xent_grad(const void* hidden, const void* weight, int dtype, size_t N,

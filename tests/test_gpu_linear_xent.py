@@ -612,3 +612,40 @@ def test_lse_of_rows_without_a_target(gcq, t):
         assert torch.equal(loss[rest], want[0][rest]) and torch.equal(lse[rest], want[1][rest])
         ref, ref_lse, e = plain_loss(big[1:2], w, y[1:2])
         check_loss(loss[1:2], lse[1:2], ref, ref_lse, e)
+
+
+@pytest.mark.parametrize("types", CASES, ids=lambda c: "-".join(str(t)[6:] for t in c))
+def test_range_of_small_probabilities(gcq, types):
+    """Probabilities down to e^-60, next to |dloss| up to 1. Each token has a
+    channel of its own with h = 1: dweight is G there. G in bf16 has no floor.
+    Two planes of fp16, the largest |dloss| of them at 2^14 or more, are off by
+    half of 2^-24 times 2^-11 at least, 2^-50 of it, one by 2^-39, which
+    no fp16 output can tell from 0."""
+    t, th, tw = types
+    announce(f"linear_xent_grad of small probabilities {types}")
+    N, V = 6, 250
+    g = torch.Generator().manual_seed(2)
+    x = -torch.randint(0, 241, (V, N), generator=g).double() / 4
+    x[0] = 0
+    h, w = torch.eye(N).to(t), x.to(t)
+    y, d = torch.zeros(N, dtype=torch.int64), torch.tensor([1.0, -1.0, 0.5, 2.0 ** -6, 2.0 ** -10, -2.0 ** -12])
+    l = h.double() @ w.double().t()
+    lse = torch.logsumexp(l, dim=1).float()
+    dh, dw = run_grad(gcq, h, w, y, lse, d, th, tw)
+    p = (l - lse.double()[:, None]).exp()
+    gm = p.clone()
+    gm[:, 0] -= 1.0
+    gm *= d.double()[:, None]
+    wide = torch.float32 in (th, tw)
+    if t == torch.bfloat16 and not wide:
+        rounding, floor = po.HALF_STEP[t], 0.0
+    elif tw == torch.float32 or t == torch.bfloat16:
+        rounding, floor = 2.0 ** -22, 2.0 ** -50
+    else:
+        rounding, floor = 2.0 ** -11, 2.0 ** -39
+    # |l - lse| < 64: its difference, and two half steps of the argument; exp
+    ep = d.double().abs()[:, None] * (p * 200 * po.F32)
+    ep[:, 0] += 4 * po.F32 * d.double().abs()
+    off = (dw.double().t() - gm).abs()
+    allowed = ep + gm.abs() * 1.01 * (rounding + po.HALF_STEP[tw]) + 1.01 * floor + po.TINY[tw]
+    assert bool((off <= allowed).all()), float((off / allowed).max())
