@@ -135,7 +135,7 @@ int dropout_impl(const char* what, const void* x, const void* residual, size_t n
         return fail(GC_EINVAL, std::string(what) + ": unknown dtype");
     if (!dropout_p_ok(p))
         return fail(GC_EINVAL, std::string(what) + ": p must lie in [0, 1]");
-    if (n > SIZE_MAX / 8 || offset > UINT64_MAX - n)
+    if (n > SIZE_MAX / 8 || (n && offset > UINT64_MAX - (n - 1)))
         return fail(GC_EINVAL, std::string(what) + ": offset + n exceeds 2^64");
     if (!aligned_to(step, 8))
         return fail(GC_EINVAL, std::string(what) + ": step must be 8-byte aligned");

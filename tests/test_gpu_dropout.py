@@ -180,3 +180,18 @@ def test_grid_strides_over_many_tiles(gcq):
         assert torch.equal(x[lo:lo + 4000].cpu().double(), f)
     del x
     torch.cuda.empty_cache()
+
+
+def test_the_last_indices(gcq):
+    """offset + n = 2^64, and not one value more."""
+    announce("dropout up to index 2^64 - 1")
+    for n in (1, 4, 9, 8192, 8195):
+        x = values(n, torch.float32, n).to(gu.DEV)
+        out = torch.full_like(x, float("nan"))
+        gcq.dropout(x, 0.5, 4, 1, out, offset=2 ** 64 - n)
+        check(out, x, po.factor(n, 0.5, 4, 1, 2 ** 64 - n), None, torch.float32)
+        gcq.dropout_backward(x, 0.5, 4, 1, out, offset=2 ** 64 - n)
+        check(out, x, po.factor(n, 0.5, 4, 1, 2 ** 64 - n), None, torch.float32)
+        if n > 1:
+            with pytest.raises(gcq.GcqError, match="exceeds 2"):
+                gcq.dropout(x, 0.5, 4, 1, out, offset=2 ** 64 - n + 1)
