@@ -484,7 +484,9 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_grad_
                     e[v][k] = __builtin_fmaf(-c1, zn[v][k], e[v][k]);
                     const float wm = R::keep(kept[v], k, e[v][k]);
                     sum[v][k] = __builtin_fmaf(wm, yn[v][k], sum[v][k]);
-                    out[k] = __builtin_fmaf(-c2, yn[v][k], wm * w[v][k] * ry);
+                    const float direct = wm * w[v][k] * ry;
+                    // (without a norm y is in no mean, whatever it holds)
+                    out[k] = has_post ? __builtin_fmaf(-c2, yn[v][k], direct) : direct;
                 }
                 R::store(dx + row * a.d, c, a.d, e[v] * a.scale);
                 R::store(dy + row * a.d, c, a.d, out);

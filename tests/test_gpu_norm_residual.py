@@ -322,3 +322,22 @@ def test_graph_replays(gcq):
         gu.sync()
         compare_forward(c2, (z, h, rp, rz), 0.5, 0.1, 3 + k, 1)
         compare_grad(c2, (dx, dy, *grads), z, rp, rz, 0.5, 0.1, 3 + k, 1)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+@pytest.mark.parametrize("p", [0.0, 0.3])
+def test_grad_without_norms_of_specials(gcq, t, p):
+    """Without gains z is linear in y: its gradient does not depend on what y
+    holds, infinities and NaN included. (dgate does, where they are kept.)"""
+    announce(f"norm_residual_grad of infinities in y {t} p={p}")
+    rows, d = 12, 136
+    c = case(rows, d, 3, t) | dict.fromkeys(("post", "pre", "dh"))
+    want = backward(gcq, c, c["y"].to(gu.DEV), None, None, 0.5, p, 8, 2)
+    bad = dict(c, y=c["y"].clone())
+    for k, v in enumerate((float("inf"), -float("inf"), float("nan"))):
+        bad["y"][k::4, k::5] = v
+    got = backward(gcq, bad, c["y"].to(gu.DEV), None, None, 0.5, p, 8, 2)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    f = po.factor(rows * d, p, 8, 2).reshape(rows, d) if p else torch.ones(rows, d)
+    reached = ((bad["y"] != c["y"]) & (f != 0)).reshape(3, -1, d).any(1)
+    assert bool(torch.isfinite(got[3].cpu())[~reached].all()) and not bool(torch.isfinite(got[3].cpu())[reached].any())
