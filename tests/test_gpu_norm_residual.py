@@ -341,3 +341,47 @@ def test_grad_without_norms_of_specials(gcq, t, p):
     f = po.factor(rows * d, p, 8, 2).reshape(rows, d) if p else torch.ones(rows, d)
     reached = ((bad["y"] != c["y"]) & (f != 0)).reshape(3, -1, d).any(1)
     assert bool(torch.isfinite(got[3].cpu())[~reached].all()) and not bool(torch.isfinite(got[3].cpu())[reached].any())
+
+
+# more gates than strips of rows: a workgroup has several, the last one fewer
+# (teams of one wave twice, teams of a workgroup)
+MANY_GATES = [(1545, 72, 515), (3081, 513, 1027), (771, 2056, 257)]
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+@pytest.mark.parametrize("shape", MANY_GATES, ids=str)
+@pytest.mark.parametrize("p", [0.0, 0.3])
+def test_grad_of_several_gates_a_strip(gcq, shape, t, p):
+    announce(f"norm_residual_grad {shape} {t} p={p}")
+    c = case(*shape, t, seed=sum(shape))
+    z, _, rp, rz = forward(gcq, c, 0.5, p, 11, 3)
+    got = backward(gcq, c, z, rp, rz, 0.5, p, 11, 3)
+    compare_grad(c, got, z, rp, rz, 0.5, p, 11, 3)
+    # dgate left out, and each gain's gradient: the rest stays the same
+    rows, d, gates = shape
+    v = to(c, "y", "post", "pre", "gate", "dz", "dh")
+    ws = torch.full((gcq.norm_residual_grad_ws_bytes(rows, d, gates),), 255, dtype=torch.uint8, device=gu.DEV)
+    for names in ({"post", "pre"}, {"gate"}, {"pre"}, set()):
+        out = {k: torch.full_like(v[k], float("nan")) if k in names else None for k in ("post", "gate", "pre")}
+        dx, dy = torch.empty_like(v["y"]), torch.empty_like(v["y"])
+        gcq.norm_residual_grad(z, v["y"], dx, dy, ws, dz=v["dz"], dh=v["dh"], post_gain=v["post"], gate=v["gate"],
+                               pre_gain=v["pre"], residual_scale=0.5, p=p, seed=11, worker=3, rstd_post=rp,
+                               rstd_pre=rz, dpost_gain=out["post"], dgate=out["gate"], dpre_gain=out["pre"])
+        gu.sync()
+        assert torch.equal(dx, got[0]) and torch.equal(dy, got[1])
+        for k, full in zip(("post", "gate", "pre"), got[2:]):
+            assert out[k] is None or torch.equal(out[k], full)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+@pytest.mark.parametrize("shape", [(600, 4096, 3), (1100, 2100, 11), (300, 8192, 3), (150, 16384, 3), (150, 9001, 5)],
+                         ids=str)
+def test_several_rows_of_a_wide_team(gcq, shape, t):
+    """More rows than teams of several waves: each takes rows in turn, the next
+    one's loads under this one's sums, over a gate's end too."""
+    announce(f"norm_residual {shape} {t}")
+    c = case(*shape, t, seed=sum(shape))
+    got = forward(gcq, c, 0.5, 0.1, 11, 3)
+    compare_forward(c, got, 0.5, 0.1, 11, 3)
+    z, _, rp, rz = got
+    compare_grad(c, backward(gcq, c, z, rp, rz, 0.5, 0.1, 11, 3), z, rp, rz, 0.5, 0.1, 11, 3)
