@@ -474,57 +474,55 @@ __global__ __launch_bounds__(WA* WB* kWave, 2) void logit_grad_kernel(
             for (int e = 0; e < 16; ++e)
                 acc.v[i][j][e] = kF16 ? __builtin_amdgcn_ldexpf(acc.v[i][j][e] * d, up) : acc.v[i][j][e] * d;
     }
-    // kIs x 32 values of 32 tokens at a time, all planes of them
-    constexpr int kIs = P::RA, kCols = kIs * 32, kChunks = kCols / 8;
+    // this wave's part of 32 tokens at a time, all planes of them
+    constexpr int kCols = L::kRowsA, kChunks = kCols / 8;
     constexpr int kPlanePart = 32 * kCols;
-    static_assert(kPlanes * kPlanePart <= TA * kStageK && P::RA % kIs == 0, "the planes fit a buffer");
+    static_assert(kPlanes * kPlanePart <= TA * kStageK, "the planes fit a buffer");
 #pragma unroll
-    for (int j = 0; j < P::RB; ++j)
+    for (int j = 0; j < P::RB; ++j) {
+        const int row = int(acc_col(lane));
 #pragma unroll
-        for (int i0 = 0; i0 < P::RA; i0 += kIs) {
-            const int row = int(acc_col(lane));
+        for (int i = 0; i < P::RA; ++i)
 #pragma unroll
-            for (int i = 0; i < kIs; ++i)
+            for (int q = 0; q < 4; ++q) {
+                float x[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float x[4];
+                for (int e = 0; e < 4; ++e)
+                    x[e] = acc.v[i][j][q * 4 + e];
+                const int col = i * 32 + 8 * q + 4 * (lane >> 5);
+                uint16_t* to = part + row * kCols + ((col >> 3) ^ (row & (kChunks - 1))) * 8 + (col & 4);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[e] = acc.v[i0 + i][j][q * 4 + e];
-                    const int col = i * 32 + 8 * q + 4 * (lane >> 5);
-                    uint16_t* to = part + row * kCols + ((col >> 3) ^ (row & (kChunks - 1))) * 8 + (col & 4);
+                for (int plane = 0; plane < kPlanes; ++plane) {
+                    s16x4 w;
 #pragma unroll
-                    for (int plane = 0; plane < kPlanes; ++plane) {
-                        s16x4 w;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (!kF16) {
-                                w[e] = __builtin_bit_cast(short, bf16_t(x[e]));
-                                continue;
-                            }
-                            const f16_t h = f16_t(x[e]);
-                            w[e] = __builtin_bit_cast(short, h);
-                            x[e] = (x[e] - float(h)) * 0x1p11f;
+                    for (int e = 0; e < 4; ++e) {
+                        if (!kF16) {
+                            w[e] = __builtin_bit_cast(short, bf16_t(x[e]));
+                            continue;
                         }
-                        *reinterpret_cast<s16x4*>(to + plane * kPlanePart) = w;
+                        const f16_t h = f16_t(x[e]);
+                        w[e] = __builtin_bit_cast(short, h);
+                        x[e] = (x[e] - float(h)) * 0x1p11f;
                     }
+                    *reinterpret_cast<s16x4*>(to + plane * kPlanePart) = w;
                 }
-            wave_lds_sync();
-            constexpr int kRows = kWave / kChunks;
+            }
+        wave_lds_sync();
+        constexpr int kRows = kWave / kChunks;
 #pragma unroll
-            for (int plane = 0; plane < kPlanes; ++plane)
+        for (int plane = 0; plane < kPlanes; ++plane)
 #pragma unroll
-                for (int r = 0; r < 32; r += kRows) {
-                    const int from = r + lane / kChunks, chunk = lane % kChunks;
-                    const uint32_t n = b_wave + j * 32 + from;
-                    const s16x8 w = *reinterpret_cast<const s16x8*>(
-                        part + plane * kPlanePart + from * kCols + ((chunk ^ (from & (kChunks - 1))) << 3));
-                    if (n < out.rows_out)
-                        *reinterpret_cast<s16x8*>(out.plane0 + plane * out.plane_stride + size_t(n) * out.ld +
-                                                   a_wave + i0 * 32 + chunk * 8) = w;
-                }
-            wave_lds_sync();
-        }
+            for (int r = 0; r < 32; r += kRows) {
+                const int from = r + lane / kChunks, chunk = lane % kChunks;
+                const uint32_t n = b_wave + j * 32 + from;
+                const s16x8 w = *reinterpret_cast<const s16x8*>(
+                    part + plane * kPlanePart + from * kCols + ((chunk ^ (from & (kChunks - 1))) << 3));
+                if (n < out.rows_out)
+                    *reinterpret_cast<s16x8*>(out.plane0 + plane * out.plane_stride + size_t(n) * out.ld +
+                                               a_wave + chunk * 8) = w;
+            }
+        wave_lds_sync();
+    }
 }
 
 // ---- the two products of the gradient ----------------------------------------

@@ -325,7 +325,6 @@ struct NormGradArgs {
     const float *rstd_post, *rstd_pre;
     float *part_post, *part_pre;  // [workgroups][d]
     float* gate_out;              // [gate strips][d]: partial rows, or dgate itself
-    size_t strips;                // workgroup ranges: strips of rows
     size_t strips_per_gate;       // > 1: a gate's rows are split over so many strips
     size_t gates_per_strip;       // > 1: a strip has so many gates (then strips_per_gate is 1)
 };
@@ -765,7 +764,6 @@ GCQ_API int norm_residual_grad(const void* z, const void* y, int dtype, size_t r
         g.part_post = dpost_gain ? reinterpret_cast<float*>(w + room.post) : nullptr;
         g.part_pre = dpre_gain ? reinterpret_cast<float*>(w + room.pre) : nullptr;
         g.gate_out = !dgate ? nullptr : s.per_gate > 1 ? reinterpret_cast<float*>(w + room.gate) : dgate;
-        g.strips = s.strips;
         g.strips_per_gate = s.per_gate;
         g.gates_per_strip = s.gates_per;
         with_dtype(dtype, [&](auto t) {

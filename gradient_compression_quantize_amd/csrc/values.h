@@ -27,25 +27,11 @@ __device__ __forceinline__ vec_f32<T> load_vec(const T* p)
     return __builtin_convertvector(*reinterpret_cast<const vec_of<T, kVec<T>>*>(p), vec_f32<T>);
 }
 
-template <typename T>
-__device__ __forceinline__ vec_f32<T> load_vec_nt(const T* p)
-{
-    return __builtin_convertvector(
-        __builtin_nontemporal_load(reinterpret_cast<const vec_of<T, kVec<T>>*>(p)), vec_f32<T>);
-}
-
 // Each value rounds once, to nearest even.
 template <typename T>
 __device__ __forceinline__ void store_vec(T* p, vec_f32<T> v)
 {
     *reinterpret_cast<vec_of<T, kVec<T>>*>(p) = __builtin_convertvector(v, vec_of<T, kVec<T>>);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_vec_nt(T* p, vec_f32<T> v)
-{
-    __builtin_nontemporal_store(__builtin_convertvector(v, vec_of<T, kVec<T>>),
-                                reinterpret_cast<vec_of<T, kVec<T>>*>(p));
 }
 
 // Bytes of one value, 0 for an unknown type.
