@@ -14,10 +14,13 @@
 // of the gradient read it back.
 //
 // Bound by the matrix cores and, for narrow models, by what G costs: 8192 x
-// 30522 x 768 bf16 takes 355 to 390 us for the loss (1.0 to 1.1 PFLOP/s) and
-// 1.87 ms for a gradient with fp32 dweight (a third of it in tiles of G, whose
-// 1 GB of stores no other tile's products run under); 8192 x 64000 x 4096 takes
-// 10.7 to 11.1 ms for the gradient (1.2 PFLOP/s).
+// 30522 x 768 bf16 takes 361 to 395 us for the loss (0.97 to 1.06 PFLOP/s: six
+// turns of k a tile, then its epilogue) and 1.81 to 1.87 ms for a gradient with
+// fp32 dweight (a third of it in tiles of G, whose 1 GB of stores no other
+// tile's products run under); 8192 x 64000 x 4096 takes 10.7 to 10.9 ms for the
+// gradient (1.2 PFLOP/s). A few tokens are bound by bytes: bf16 ones read the
+// matrix once (14.5 us for one token of 30522 x 768, floor 9.1), but fp32
+// weights, and 16-bit ones with D off a multiple of 128, are copied first.
 #include <algorithm>
 #include <limits>
 #include <string>
@@ -743,12 +746,12 @@ struct Preparation {
             const auto launch = [&](auto kernel) {
                 hipLaunchKernelGGL(kernel, grid, dim3(kRowThreads), 0, stream, planes, ignore, V);
             };
-            if constexpr (sizeof(T) == 4)
+            if constexpr (std::is_same_v<T, float>)
                 launch(planes_kernel<T, true, 2>);
-            else if (mode.f16)
+            else if constexpr (std::is_same_v<T, f16_t>)
                 launch(planes_kernel<T, true, 1>);
             else
-                launch(planes_kernel<T, false, 1>);
+                launch(mode.f16 ? planes_kernel<T, true, 1> : planes_kernel<T, false, 1>);
             return 0;
         });
     }

@@ -23,6 +23,13 @@
 // 4.8 TB/s) and 166 us backward (805 MB, 4.8 TB/s), a plain copy moving 5.2.
 // The backward pass has some 60 vector instructions a value, about 105 us of
 // them: they have to run under the loads, which the row fetched ahead does.
+//
+// Past 4096 values a row the backward kernels spill registers (teams of 8
+// waves 72 bytes of scratch a lane in 16-bit types and 264 in fp32, of 16 waves
+// 224 to 256; off 16 bytes up to 860), and so does the forward one in fp32 past
+// 8192: 4096 x 8192 bf16 takes 100 us backward (floor 78), 4096 x 12288 301
+// (117). Gates of a few rows each start with nothing fetched ahead and exchange
+// their sums: 16383 x 1024 bf16 with 5461 gates takes 78 us backward (floor 48).
 #include "dropout_mask.h"
 
 #include <algorithm>
@@ -425,8 +432,8 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void norm_residual_grad_
             if (has_post)
                 next_ry = g.rstd_post[row];
         };
-        // the next row's loads run under this row's arithmetic, where the
-        // registers hold both (a workgroup of 1024 threads has 128 a lane)
+        // the next row's loads run under this row's arithmetic; a workgroup of
+        // 1024 threads, which has 128 registers a lane, takes them row by row
         constexpr bool kAhead = kTeam < 1024;
         if (kAhead && lo + team < hi)
             fetch(lo + team);
@@ -573,7 +580,9 @@ void with_team(size_t d, F f)
 
 // Waves of one launch: 8 a compute unit, each with a contiguous range of
 // rows. 16384 x 4096 bf16: 117 us, against 169, 138, 134 and 136 with 4, 6, 10
-// and 16; rows dealt out in turn instead took 205.
+// and 16; rows dealt out in turn instead took 205. Teams of 16 waves (more than
+// 8192 values a row) come to one workgroup for every other compute unit, which
+// leaves half of them idle: 4096 x 12288 bf16 takes 168 us, floor 78.
 constexpr size_t kForwardWaves = 256 * 8;
 
 // Strips of the backward launch, each of which leaves a partial row: one
