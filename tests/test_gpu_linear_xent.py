@@ -649,3 +649,28 @@ def test_range_of_small_probabilities(gcq, types):
     off = (dw.double().t() - gm).abs()
     allowed = ep + gm.abs() * 1.01 * (rounding + po.HALF_STEP[tw]) + 1.01 * floor + po.TINY[tw]
     assert bool((off <= allowed).all()), float((off / allowed).max())
+
+
+@pytest.mark.parametrize("types", [c for c in CASES if c[0] != torch.float16],
+                         ids=lambda c: "-".join(str(t)[6:] for t in c))
+@pytest.mark.parametrize("base", [2.0 ** 34, -2.0 ** 62])
+def test_grad_of_logits_of_any_size(gcq, types, base):
+    """One logit leads by far more than an exponential holds: p is 1 there and 0
+    elsewhere, and every product of the gradient is exact."""
+    t, th, tw = types
+    announce(f"linear_xent_grad of logits of {base} {types}")
+    N, V, D = 5, 300, 8
+    h, w = (torch.eye(N, D) * D).to(t), torch.full((V, D), base / D).to(t)
+    lead = torch.tensor([0, 17, 128, 255, 299])
+    w[lead, torch.arange(N)] += abs(base) / D / 64
+    y = lead.clone()
+    y[::2] = (y[::2] + 3) % V
+    d = torch.tensor([1.0, -0.5, 2.0, 0.25, 1.0])
+    lse = (h.double() @ w.double().t()).max(dim=1).values.float()
+    dh, dw = run_grad(gcq, h, w, y, lse, d, th, tw)
+    g = torch.zeros(N, V, dtype=torch.float64)
+    g[torch.arange(N), lead] += d.double()
+    g[torch.arange(N), y] -= d.double()
+    assert torch.equal(dw.double(), g.t() @ h.double())
+    ref = g @ w.double()
+    assert bool(((dh.double() - ref).abs() <= ref.abs() * po.HALF_STEP[th] + abs(base) * 2.0 ** -21).all())

@@ -385,3 +385,44 @@ def test_several_rows_of_a_wide_team(gcq, shape, t):
     compare_forward(c, got, 0.5, 0.1, 11, 3)
     z, _, rp, rz = got
     compare_grad(c, backward(gcq, c, z, rp, rz, 0.5, 0.1, 11, 3), z, rp, rz, 0.5, 0.1, 11, 3)
+
+
+@pytest.mark.slow
+def test_offsets_past_32_bits(gcq):
+    """2^32 values and more: rows on both sides of that index, in place."""
+    rows, d, gates, t, p, seed, worker = 1_048_583, 4096, 1, torch.bfloat16, 0.3, 5, 2
+    free, _ = torch.cuda.mem_get_info()
+    if free < 50 << 30:
+        pytest.skip("needs 50 GiB of device memory")
+    announce(f"norm_residual {rows} x {d}")
+    g = torch.Generator(device=gu.DEV).manual_seed(1)
+    big = [torch.empty(rows, d, dtype=t, device=gu.DEV).normal_(generator=g) for _ in range(4)]
+    x, y, dz, dh = big
+    at = torch.tensor([0, 3, 524_287, 1_048_575, 1_048_576, rows - 1])
+    post, pre, gate = (1 + 0.1 * torch.randn(d, generator=g, device=gu.DEV) for _ in range(3))
+    c = dict(x=x[at].cpu(), y=y[at].cpu(), dz=dz[at].cpu(), dh=dh[at].cpu(), post=post.cpu(), pre=pre.cpu(),
+             gate=gate[None].cpu())
+    rp, rz = torch.empty(rows, device=gu.DEV), torch.empty(rows, device=gu.DEV)
+    h = torch.empty_like(y)
+    kw = dict(post_gain=post, gate=gate, pre_gain=pre, residual_scale=0.5, p=p, seed=seed, worker=worker,
+              rstd_post=rp, rstd_pre=rz)
+    gcq.norm_residual(x, y, x, h=h, eps=EPS, **kw)  # z over x
+    z = x
+    got = [v[at].cpu() for v in (z, h, rp, rz)]
+    ws = torch.empty(gcq.norm_residual_grad_ws_bytes(rows, d, gates), dtype=torch.uint8, device=gu.DEV)
+    gcq.norm_residual_grad(z, y, dz, dh, ws, dz=dz, dh=dh, **kw)  # dx over dz, dy over dh
+    gu.sync()
+    grads = [v[at].cpu() for v in (dz, dh)]
+    for k, row in enumerate(at.tolist()):
+        one_row = {n: v if n in ("post", "pre", "gate") else v[k:k + 1] for n, v in c.items()}
+        # the row's own part of the mask: 1 row at offset row * d
+        f = po.factor(d, p, seed, worker, row * d).reshape(1, d)
+        with pytest.MonkeyPatch.context() as m:
+            m.setattr(po, "factor", lambda *a, **kw: f)
+            for v, (ref, err) in zip(got, plain(one_row, 0.5, p, seed, worker)):
+                check(v[k:k + 1], ref, err)
+            ref = plain_grad(one_row, got[0][k:k + 1], got[2][k:k + 1], got[3][k:k + 1], 0.5, p, seed, worker)
+            check(grads[0][k:k + 1], *ref[0])
+            check(grads[1][k:k + 1], *ref[1])
+    del big, x, y, z, dz, dh, h
+    torch.cuda.empty_cache()
