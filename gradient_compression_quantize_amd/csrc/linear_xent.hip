@@ -910,7 +910,11 @@ ProductPlan product_plan(size_t rows, size_t D, size_t turns)
 }
 
 // Planes of G for a gradient of the type: one, rounded to the 16 bits that the
-// gradient is rounded to as well, or two.
+// gradient is rounded to as well, or two. A 16-bit gradient thus carries two
+// roundings to its type where one cannot be avoided: it is some 1.4 times as
+// far from 64 bits (1.75 at most in 60 sizes). A second plane would undo that
+// and take 2.20 ms for 8192 x 30522 x 768, where one takes 1.25; who needs it
+// asks for fp32.
 int g_planes(int dtype) { return dtype == GC_F32 ? 2 : 1; }
 
 // Planes for dweight. One plane of fp16 ends at 2^-39 of the largest |dloss|,
