@@ -26,6 +26,8 @@ float32, bfloat16 or float16; gradients of parameters in float32):
     mask drawn again where it is needed instead of stored;
   * norm_residual and norm_residual_grad: the norms around a block fused with
     its dropout, gate and residual scale;
+  * layer_norm and layer_norm_grad: layer norm behind a block's dropout and
+    residual sum;
   * linear_xent_loss and linear_xent_grad: softmax cross entropy of a linear
     layer over a large vocabulary, the logits never kept.
 """
@@ -117,6 +119,10 @@ def _declare(L):
     L.norm_residual_grad.argtypes = [_vp, _vp, _i, _sz, _sz, _vp, _vp, _sz, _vp, _f, dbl, u64, u32,
                                      _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                      ctypes.POINTER(_sz), _vp]
+    L.layer_norm.argtypes = [_vp, _vp, _i, _sz, _sz, _vp, _vp, _f, dbl, u64, u32, _vp, _vp, _vp,
+                             _vp, _vp, _vp]
+    L.layer_norm_grad.argtypes = [_vp, _vp, _vp, _i, _sz, _sz, _vp, dbl, u64, u32, _vp, _vp, _vp,
+                                  _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(_sz), _vp]
     i64 = ctypes.c_int64
     L.linear_xent_loss.argtypes = [_vp, _vp, _i, _sz, _sz, _sz, _vp, i64, _vp, _vp, _vp,
                                    ctypes.POINTER(_sz), _vp]
@@ -130,7 +136,7 @@ def _declare(L):
                  "qsgd_quantize_sum",
                  "grandk_indices", "gather_f32", "grandk_mn_step",
                  "dropout", "dropout_backward", "norm_residual", "norm_residual_grad",
-                 "linear_xent_loss", "linear_xent_grad"):
+                 "layer_norm", "layer_norm_grad", "linear_xent_loss", "linear_xent_grad"):
         getattr(L, name).restype = _i
     return L
 
@@ -701,6 +707,67 @@ def norm_residual_grad(z, y, dx, dy, ws, dz=None, dh=None, post_gain=None, gate=
         zp, yp, code, rows, d, post, gp, gates, pre, residual_scale, p, _u64(seed),
         _worker(worker), _step(step, cur), rp, rz, dzp, dhp, dxp, dyp, dpost, dgp, dpre,
         _at(ws, torch.uint8, "ws", cur), ctypes.byref(size), _stream(stream)))
+
+
+def _row_shape(x, what: str, same, columns, per_row):
+    """(rows, d) of x [..., d], after the sizes of everything else: `same`
+    like x, `columns` of d values, `per_row` of one value a row."""
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError(f"{what}: a row must hold at least one value")
+    d = x.shape[-1]
+    n = x.numel()
+    for t in same:
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{what}: the activations differ in size")
+    for t in columns:
+        if t is not None and t.numel() != d:
+            raise ValueError(f"{what}: gain, bias and their gradients must hold one value a column")
+    for t in per_row:
+        if t is not None and t.numel() != n // d:
+            raise ValueError(f"{what}: mean and rstd must hold one value a row")
+    return n // d, d
+
+
+def layer_norm(x, h, y=None, z=None, gain=None, bias=None, eps: float = 1e-5, p: float = 0.0,
+               seed: int = 0, worker: int = 0, step=None, mean=None, rstd=None, stream=None) -> None:
+    """z = x + dropout(y) and h = (z - mean) * rstd * gain + bias. x, y, z, h:
+    [..., d] of one dtype; gain and bias [d], mean and rstd (one value a row)
+    float32. Without y, z is x and is not written."""
+    rows, d = _row_shape(x, "layer_norm", (h, y, z), (gain, bias), (mean, rstd))
+    cur = _current_device()
+    code = _dtype(x, "x")
+    xp, yp, zp, hp = _ats(cur, x.dtype, "x y z h", x, y, z, h)
+    gp, bp, mp, rp = _ats(cur, _torch().float32, "gain bias mean rstd", gain, bias, mean, rstd)
+    _check(load().layer_norm(xp, yp, code, rows, d, gp, bp, eps, p, _u64(seed), _worker(worker),
+                             _step(step, cur), zp, hp, mp, rp, _stream(stream)))
+
+
+def layer_norm_grad_ws_bytes(rows: int, d: int) -> int:
+    size = _sz(0)
+    _check(load().layer_norm_grad(None, None, None, GC_F32, rows, d, None, 0.0, 0, 0, None, None,
+                                  None, None, None, None, None, None, ctypes.byref(size), None))
+    return int(size.value)
+
+
+def layer_norm_grad(z, dh, dx, ws, dz=None, dy=None, gain=None, p: float = 0.0, seed: int = 0,
+                    worker: int = 0, step=None, mean=None, rstd=None, dgain=None, dbias=None,
+                    stream=None) -> None:
+    """The gradient of layer_norm, from its z (without y: its x), arguments,
+    mean and rstd; dz is what reaches z by another way. ws: uint8 device
+    tensor of at least layer_norm_grad_ws_bytes(rows, d) bytes. dgain and
+    dbias are float32, or None."""
+    torch = _torch()
+    rows, d = _row_shape(z, "layer_norm_grad", (dh, dx, dz, dy), (gain, dgain, dbias), (mean, rstd))
+    size = _ws(ws, "layer_norm_grad")
+    cur = _current_device()
+    code = _dtype(z, "z")
+    zp, dhp, dxp, dzp, dyp = _ats(cur, z.dtype, "z dh dx dz dy", z, dh, dx, dz, dy)
+    gp, mp, rp, dgp, dbp = _ats(cur, torch.float32, "gain mean rstd dgain dbias", gain, mean, rstd,
+                                dgain, dbias)
+    _check(load().layer_norm_grad(zp, dhp, dzp, code, rows, d, gp, p, _u64(seed), _worker(worker),
+                                  _step(step, cur), mp, rp, dxp, dyp, dgp, dbp,
+                                  _at(ws, torch.uint8, "ws", cur), ctypes.byref(size),
+                                  _stream(stream)))
 
 
 def _dtype_code(dtype) -> int:

@@ -381,6 +381,46 @@ int norm_residual_grad(const void* z, const void* y, int dtype, size_t rows, siz
                        float* dgate, float* dpre_gain, void* ws, size_t* ws_bytes,
                        hipStream_t stream);
 
+/* ---- layer norm behind a block's dropout and residual sum ------------------- */
+
+/* For each row of d values:
+ *   z = x + drop(y)                 (y NULL: z = x)
+ *   h = (z - mean) * rstd * gain + bias   (gain NULL: 1, bias NULL: 0)
+ *   mean = mean(z),  rstd = 1 / sqrt(mean((z - mean)^2) + eps)
+ * with the mask of dropout() at offset 0 over the rows x d values (p = 0: no
+ * dropout). Everything between is fp32; the squares are those of the
+ * deviations from the mean, and h is that of the z before its rounding.
+ *   x, y, z, h  [rows, d] of `dtype`, rows contiguous; z NULL: not kept, and
+ *               NULL without y. h may be x or y, z the other one
+ *   gain, bias  [d] fp32, or NULL
+ *   mean, rstd  [rows] fp32 out, for the gradient, or NULL
+ *   d 1 .. 16384, eps >= 0, p 0 .. 1; seed, worker, step as in dropout() */
+int layer_norm(const void* x, const void* y, int dtype, size_t rows, size_t d,
+               const float* gain, const float* bias, float eps, double p,
+               uint64_t seed, uint32_t worker, const uint64_t* step, void* z,
+               void* h, float* mean, float* rstd, hipStream_t stream);
+
+/* The gradient of layer_norm: dh is that of h, dz what reaches z by another
+ * way (the residual stream).
+ *   z           the forward call's z (without y: its x), with its mean, rstd
+ *               and the rest of its arguments
+ *   dh, dz      [rows, d] of `dtype`; dz may be NULL (zero)
+ *   dx, dy      [rows, d] of `dtype` out: dx is the gradient of z and x, dy
+ *               that of y (dx through the mask; p, seed, worker and step are
+ *               read for it alone), or NULL. Each may be z, dh or dz itself
+ *   dgain, dbias  [d] fp32 out, or NULL: not computed. fp32 sums over the
+ *               rows in a fixed order.
+ *   ws          16-byte-aligned workspace; ws == NULL: *ws_bytes = its size
+ *               for (rows, d), else *ws_bytes must be at least that. Calls
+ *               that may overlap in time need workspaces of their own.
+ * rows may be 0: dgain and dbias are then zero. */
+int layer_norm_grad(const void* z, const void* dh, const void* dz, int dtype,
+                    size_t rows, size_t d, const float* gain, double p,
+                    uint64_t seed, uint32_t worker, const uint64_t* step,
+                    const float* mean, const float* rstd, void* dx, void* dy,
+                    float* dgain, float* dbias, void* ws, size_t* ws_bytes,
+                    hipStream_t stream);
+
 /* ---- softmax cross entropy of a linear layer over a large vocabulary ------- */
 
 /* For tokens n < N, with logits l_nv = <hidden[n], weight[v]> over v < V:
