@@ -29,7 +29,10 @@ float32, bfloat16 or float16; gradients of parameters in float32):
   * layer_norm and layer_norm_grad: layer norm behind a block's dropout and
     residual sum;
   * linear_xent_loss and linear_xent_grad: softmax cross entropy of a linear
-    layer over a large vocabulary, the logits never kept.
+    layer over a large vocabulary, the logits never kept;
+  * orthogonalize and muon_step: an update made nearly orthogonal by
+    Newton-Schulz products, and the optimiser step from the reduced gradients
+    to the new weights.
 """
 from __future__ import annotations
 
@@ -128,6 +131,11 @@ def _declare(L):
                                    ctypes.POINTER(_sz), _vp]
     L.linear_xent_grad.argtypes = [_vp, _vp, _i, _sz, _sz, _sz, _vp, i64, _vp, _vp, _vp, _i, _vp,
                                    _i, _vp, ctypes.POINTER(_sz), _vp]
+    pp = ctypes.POINTER(_vp)
+    L.orthogonalize.argtypes = [pp, _i, _sz, _sz, _i, _vp, _i, _f, _f, pp, _i, _vp,
+                                ctypes.POINTER(_sz), _vp]
+    L.muon_step.argtypes = [pp, _i, _sz, _sz, pp, pp, _i, _i, _vp, _i, _f, _f, _f, _i, _f, _vp, _f,
+                            _f, pp, pp, _vp, ctypes.POINTER(_sz), _vp]
     for name in ("compress_2bit", "decompress_2bit", "decompress_2bit_sum",
                  "compress_ternary", "decompress_ternary", "decompress_ternary_sum",
                  "gc_plan_2bit_multi_create", "gc_plan_block_offsets", "compress_2bit_multi",
@@ -136,7 +144,8 @@ def _declare(L):
                  "qsgd_quantize_sum",
                  "grandk_indices", "gather_f32", "grandk_mn_step",
                  "dropout", "dropout_backward", "norm_residual", "norm_residual_grad",
-                 "layer_norm", "layer_norm_grad", "linear_xent_loss", "linear_xent_grad"):
+                 "layer_norm", "layer_norm_grad", "orthogonalize", "muon_step",
+                 "linear_xent_loss", "linear_xent_grad"):
         getattr(L, name).restype = _i
     return L
 
@@ -850,4 +859,107 @@ def linear_xent_grad(hidden, weight, target, lse, dloss, dhidden, dweight, ws,
         _at(dloss, torch.float32, "dloss", cur),
         _at(dhidden, None if dhidden is None else dhidden.dtype, "dhidden", cur), h_code,
         _at(dweight, None if dweight is None else dweight.dtype, "dweight", cur), w_code,
+        _at(ws, torch.uint8, "ws", cur), ctypes.byref(size), _stream(stream)))
+
+
+# ---- orthogonalised updates ---------------------------------------------------
+
+# (a, b, c) of each step: brings the singular values that are not far below the
+# largest one near 1.
+NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def _coefficients(coefficients):
+    """fp32 array of the steps' triples, and their number."""
+    flat = []
+    for triple in coefficients:
+        if len(triple) != 3:
+            raise ValueError("coefficients must hold three numbers a step")
+        flat += triple
+    return (_f * max(len(flat), 1))(*flat), len(flat) // 3
+
+
+def _matrices(what: str, names, *lists):
+    """(count, m, n) of lists of matrices of one size."""
+    first = lists[0]
+    if len(first) < 1 or len(first) > GC_MAX_WORKERS:
+        raise ValueError(f"{what}: the number of matrices must lie in 1 .. {GC_MAX_WORKERS}")
+    if first[0].dim() != 2:
+        raise ValueError(f"{what}: {names.split()[0]} must be matrices [m, n]")
+    shape = tuple(first[0].shape)
+    for name, ts in zip(names.split(), lists):
+        if len(ts) != len(first):
+            raise ValueError(f"{what}: {name} differ in number")
+        for t in ts:
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{what}: {name} differ in size")
+    return len(first), shape[0], shape[1]
+
+
+def orthogonalize_ws_bytes(count: int, m: int, n: int, out_dtype) -> int:
+    size = _sz(0)
+    _check(load().orthogonalize(None, count, m, n, GC_F32, None, 0, 0.0, 1.0, None,
+                                _dtype_code(out_dtype), None, ctypes.byref(size), None))
+    return int(size.value)
+
+
+def orthogonalize(xs: Sequence, outs: Sequence, ws, coefficients=NEWTON_SCHULZ,
+                  scale: float = 1.0, eps: float = 1e-7, stream=None) -> None:
+    """outs[k] = scale * (xs[k] / (its norm + eps) after a step a X + b (X X') X
+    + c (X X')^2 X for each triple of `coefficients`). xs and outs: up to 64
+    matrices [m, n], the xs of one dtype and the outs of one; the dtype of the
+    outs says how exactly they are computed. outs[k] may be xs[k] itself. ws:
+    uint8 device tensor of at least orthogonalize_ws_bytes(count, m, n,
+    out_dtype) bytes."""
+    count, m, n = _matrices("orthogonalize", "xs outs", xs, outs)
+    coef, steps = _coefficients(coefficients)
+    size = _ws(ws, "orthogonalize")
+    code, out_code = _dtype(xs[0], "xs"), _dtype(outs[0], "outs")
+    _check(load().orthogonalize(
+        _ptr_array(xs, xs[0].dtype, "xs"), count, m, n, code, coef, steps, eps, scale,
+        _ptr_array(outs, outs[0].dtype, "outs"), out_code,
+        _at(ws, _torch().uint8, "ws", _current_device()), ctypes.byref(size), _stream(stream)))
+
+
+def muon_step_ws_bytes(count: int, m: int, n: int, update_dtype) -> int:
+    """update_dtype: as in muon_step (by default the weights' dtype)."""
+    size = _sz(0)
+    _check(load().muon_step(None, count, m, n, None, None, GC_F32, _dtype_code(update_dtype), None,
+                            0, 0.0, 1.0, 0.0, 0, 0.0, None, 0.0, 1.0, None, None, None,
+                            ctypes.byref(size), None))
+    return int(size.value)
+
+
+def muon_step(grads: Sequence, momenta: Sequence, weights: Sequence, ws,
+              coefficients=NEWTON_SCHULZ, eps: float = 1e-7, momentum: float = 0.95,
+              nesterov: bool = True, grad_scale: float = 1.0, lr: float = 0.02, lr_scale=None,
+              weight_decay: float = 0.0, update_scale: float = 1.0, update_dtype=None,
+              new_momenta=None, new_weights=None, stream=None) -> None:
+    """Moves the momenta along the gradients, and the weights along the
+    orthogonalised momenta. Up to 64 matrices [m, n]: grads and momenta
+    float32, weights of one dtype; new_momenta and new_weights default to the
+    tensors themselves. update_dtype (by default the weights' dtype) says how
+    exactly the update is computed: bfloat16 is a third of the products of
+    float32. lr_scale: one-element float32 device tensor multiplied to lr on
+    the device. ws: uint8 device tensor of at least muon_step_ws_bytes(count,
+    m, n, update_dtype) bytes."""
+    torch = _torch()
+    new_momenta = momenta if new_momenta is None else new_momenta
+    new_weights = weights if new_weights is None else new_weights
+    count, m, n = _matrices("muon_step", "grads momenta weights new_momenta new_weights", grads,
+                            momenta, weights, new_momenta, new_weights)
+    coef, steps = _coefficients(coefficients)
+    size = _ws(ws, "muon_step")
+    cur = _current_device()
+    code = _dtype(weights[0], "weights")
+    if lr_scale is not None and lr_scale.numel() != 1:
+        raise ValueError("muon_step: lr_scale must hold one element")
+    f32 = torch.float32
+    _check(load().muon_step(
+        _ptr_array(grads, f32, "grads"), count, m, n, _ptr_array(momenta, f32, "momenta"),
+        _ptr_array(weights, weights[0].dtype, "weights"), code,
+        code if update_dtype is None else _dtype_code(update_dtype), coef, steps, eps, grad_scale,
+        momentum, int(bool(nesterov)), lr, _at(lr_scale, f32, "lr_scale", cur), weight_decay,
+        update_scale, _ptr_array(new_momenta, f32, "new_momenta"),
+        _ptr_array(new_weights, weights[0].dtype, "new_weights"),
         _at(ws, torch.uint8, "ws", cur), ctypes.byref(size), _stream(stream)))

@@ -25,7 +25,7 @@ CEILINGS_LIB_PATH = PKG / "libgcq_ceilings.so"
 BUILD_DIR = PKG / "_build"
 
 SOURCES = ["status.hip", "twobit.hip", "ternary.hip", "qsgd.hip", "dropout.hip", "norm_residual.hip",
-           "layer_norm.hip", "linear_xent.hip"]
+           "layer_norm.hip", "linear_xent.hip", "orthogonalize.hip"]
 # the benchmark's HBM ceiling kernels: a library of their own
 CEILINGS_SOURCES = ["hbm_ceilings.hip"]
 

@@ -105,11 +105,11 @@ struct StageLoader {
 
     // XOR on the chunk index of LDS row `row`, so that what is read in one
     // clock covers the 64 banks (256 bytes): by rows (64 bytes each) the same
-    // chunk of 16 rows, by k 64 bytes of 4 rows. SQ_LDS_BANK_CONFLICT is zero;
+    // chunk of 16 rows, by k 64 bytes of 4 rows (of 2 where a row is 128 bytes). SQ_LDS_BANK_CONFLICT is zero;
     // covering 32 banks alone left it at half of SQ_LDS_IDX_ACTIVE.
     static __device__ __forceinline__ uint32_t swizzle(uint32_t row)
     {
-        return kKRows ? 4 * (row & 3) : (row >> 2) & 3;
+        return kKRows ? 4 * (row & (T >= 128 ? 3 : 1)) : (row >> 2) & 3;
     }
 
     __device__ __forceinline__ void init(const MatOperand& m, uint32_t first, int wave_, int lane)

@@ -1,0 +1,767 @@
+// orthogonalize.hip -- the nearest thing to an orthogonal matrix that a few
+// products reach (Newton-Schulz), and the optimiser step around it.
+//
+//   X_0 = u / (|u|_F + eps),  X <- a X + P X,  P = b A + c A^2,  A = X X^T
+// with A of the smaller side (of a tall matrix A = X^T X and X <- a X + X P).
+// Every singular value s of X becomes a s + b s^3 + c s^5, the singular vectors
+// stay.
+//
+// A step of the iteration is three products: A and A^2 are symmetric, so that
+// only the tiles on and below the diagonal are computed and written twice; the
+// third ends in the sum with a X, in the last step in the output itself (the
+// scaled update, or the new weights). A tall matrix is never transposed: its
+// products read it by k (mfma_product.h).
+//
+// Precision. X is carried to 22 bits, as two planes of fp16; A and P are held
+// in one plane or two. The operands of the products are the first planes alone
+// (off by at most 2^-11 of a value) where the result is kept in bf16, else both (three
+// products each). a X never loses what the operands round away: its roundings
+// would grow with the small singular values, 3.4 times a step, up to 500 times,
+// while those of P X shrink with s^2. X is held times 2^12 and A times 2^12, P
+// times 2^10: entries are at most a singular value (s, s^2, ..) in size, and the
+// first ones, of a matrix of 4096 x 4096, near 2^-12 and 2^-18.
+#include <algorithm>
+#include <cmath>
+#include <string>
+#include <type_traits>
+
+#include "mfma_product.h"
+
+namespace gcq {
+namespace {
+
+constexpr int kXExp = 12, kAExp = 12, kPExp = 10;
+constexpr float kXScale = 4096.0f;
+
+// 2^e
+constexpr float pow2(int e)
+{
+    float r = 1.0f;
+    for (; e > 0; --e)
+        r *= 2.0f;
+    for (; e < 0; ++e)
+        r *= 0.5f;
+    return r;
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// ---- the norm, and the first X -------------------------------------------------
+
+constexpr int kThreads = 256;
+
+// Up to this many partial sums of squares a matrix.
+constexpr uint32_t kMaxParts = 1024;
+
+// Eight values of a row of n, from column c on (zeros behind the last),
+// whatever the alignment.
+template <typename T>
+__device__ __forceinline__ vec_of<float, 8> load8(const T* row, size_t c, size_t n)
+{
+    typedef T Vec __attribute__((ext_vector_type(8)));
+    typedef Vec VecAny __attribute__((aligned(sizeof(T))));
+    if (c + 8 <= n)
+        return __builtin_convertvector(*reinterpret_cast<const VecAny*>(row + c), vec_of<float, 8>);
+    vec_of<float, 8> v = {};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (c + k < n)
+            v[k] = float(row[c + k]);
+    return v;
+}
+
+__device__ __forceinline__ double workgroup_sum(double x)
+{
+    __shared__ double lds[kThreads / kWave];
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1)
+        x += __shfl_xor(x, off);
+    if ((threadIdx.x & (kWave - 1)) == 0)
+        lds[threadIdx.x / kWave] = x;
+    __syncthreads();
+    x = lds[0];
+    for (int w = 1; w < kThreads / kWave; ++w)
+        x += lds[w];
+    return x;
+}
+
+// What the update is made of: a matrix as it is, or the gradient and the
+// momentum, which the first pass over them moves on.
+struct Momentum {
+    float grad_scale, beta;
+    bool nesterov;
+};
+
+// g + beta (m - g) of g scaled, and of the new momentum
+__device__ __forceinline__ float mix(float g, float m, float beta) { return __builtin_fmaf(beta, m - g, g); }
+
+// parts[matrix][workgroup] = sum of squares of its share of u, in 64 bits: no
+// size of its values overflows or vanishes. Workgroups of one matrix take its
+// values in turn, matrices are contiguous. Also zeros `zero`, what the products
+// read of the workspace and do not write.
+template <typename T, bool kMomentum>
+__global__ __launch_bounds__(kThreads) void norm_kernel(PtrTable<T> x, PtrTable<float> momenta,
+                                                        PtrTable<float> new_momenta, Momentum mo, size_t values,
+                                                        double* __restrict__ parts, u32x4* __restrict__ zero,
+                                                        size_t zeros)
+{
+    const size_t k = blockIdx.y;
+    const T* src = x.p[k];
+    double sum = 0.0;
+    const size_t stride = size_t(gridDim.x) * kThreads * 8;
+    for (size_t i = (size_t(blockIdx.x) * kThreads + threadIdx.x) * 8; i < values; i += stride) {
+        vec_of<float, 8> v = load8(src, i, values);
+        if (kMomentum) {
+            const vec_of<float, 8> old = load8(momenta.p[k], i, values);
+            float* to = const_cast<float*>(new_momenta.p[k]) + i;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float g = v[e] * mo.grad_scale, m = mix(g, old[e], mo.beta);
+                if (i + e < values)
+                    to[e] = m;
+                v[e] = mo.nesterov ? mix(g, m, mo.beta) : m;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            sum = __builtin_fma(double(v[e]), double(v[e]), sum);
+    }
+    sum = workgroup_sum(sum);
+    if (threadIdx.x == 0)
+        parts[k * gridDim.x + blockIdx.x] = sum;
+    const size_t all = size_t(gridDim.x) * gridDim.y * kThreads;
+    for (size_t i = (k * gridDim.x + blockIdx.x) * kThreads + threadIdx.x; i < zeros; i += all)
+        zero[i] = u32x4{0, 0, 0, 0};
+}
+
+// Two planes of a value: x = p0 + 2^-11 p1 to 2^-22 of it.
+struct Planes4 {
+    vec_of<f16_t, 4> p0, p1;
+};
+
+__device__ __forceinline__ Planes4 split4(vec_of<float, 4> v)
+{
+    Planes4 s;
+    s.p0 = __builtin_convertvector(v, vec_of<f16_t, 4>);
+    s.p1 = __builtin_convertvector((v - __builtin_convertvector(s.p0, vec_of<float, 4>)) * 0x1p11f, vec_of<f16_t, 4>);
+    return s;
+}
+
+__device__ __forceinline__ vec_of<float, 4> join4(Planes4 s)
+{
+    const vec_of<float, 4> lo = __builtin_convertvector(s.p1, vec_of<float, 4>);
+    vec_of<float, 4> v = __builtin_convertvector(s.p0, vec_of<float, 4>);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        v[e] = __builtin_fmaf(lo[e], 0x1p-11f, v[e]);
+    return v;
+}
+
+// A matrix of the workspace, of each of `count`: [rows][ld], two planes of all
+// of them one behind the other.
+struct Held {
+    uint16_t* plane0;
+    size_t plane_stride, matrix_stride;
+    uint32_t ld, rows;
+};
+
+__device__ __forceinline__ uint16_t* held_at(const Held& h, size_t matrix, int plane)
+{
+    return h.plane0 + plane * h.plane_stride + matrix * h.matrix_stride;
+}
+
+// X_0 of each matrix, zeros behind its last row and column.
+template <typename T, bool kMomentum>
+__global__ __launch_bounds__(kThreads) void first_kernel(PtrTable<T> x, PtrTable<float> new_momenta, Momentum mo,
+                                                         size_t m, size_t n, float eps,
+                                                         const double* __restrict__ parts, uint32_t nparts, Held to)
+{
+    const size_t k = blockIdx.y;
+    double sum = 0.0;
+    for (uint32_t i = threadIdx.x; i < nparts; i += kThreads)
+        sum += parts[k * nparts + i];
+    sum = workgroup_sum(sum);
+    const double factor = double(kXScale) / (sqrt(sum) + double(eps));
+    const uint32_t chunks = to.ld / 8;
+    const size_t total = size_t(to.rows) * chunks;
+    for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < total; i += size_t(gridDim.x) * kThreads) {
+        const size_t r = i / chunks, c = (i - r * chunks) * 8;
+        vec_of<float, 8> v = {};
+        if (r < m && c < n) {
+            v = load8(x.p[k] + r * n, c, n);
+            if (kMomentum) {
+                const vec_of<float, 8> mom = load8(new_momenta.p[k] + r * n, c, n);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = mo.nesterov ? mix(v[e] * mo.grad_scale, mom[e], mo.beta) : mom[e];
+            }
+            // (a factor that overflows fp32 belongs to values that do not)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = float(double(v[e]) * factor);
+        }
+        const Planes4 lo = split4(v.lo), hi = split4(v.hi);
+        uint16_t* o = held_at(to, k, 0) + r * to.ld + c;
+        vec_of<f16_t, 8> w;
+        w.lo = lo.p0;
+        w.hi = hi.p0;
+        *reinterpret_cast<vec_of<f16_t, 8>*>(o) = w;
+        w.lo = lo.p1;
+        w.hi = hi.p1;
+        *reinterpret_cast<vec_of<f16_t, 8>*>(o + to.plane_stride) = w;
+    }
+}
+
+// ---- products --------------------------------------------------------------------
+
+// Tile `id` on or below the diagonal: ta <= tb.
+__device__ __forceinline__ void triangle_of(uint32_t id, uint32_t& ta, uint32_t& tb)
+{
+    tb = uint32_t((sqrtf(8.0f * float(id) + 1.0f) - 1.0f) * 0.5f);
+    // (the root may be off by one step)
+    while (tb * (tb + 1) / 2 > id)
+        --tb;
+    while ((tb + 1) * (tb + 2) / 2 <= id)
+        ++tb;
+    ta = id - tb * (tb + 1) / 2;
+}
+
+struct Tiles {
+    uint32_t per_matrix;
+    uint32_t a, b;  // of a product that is not symmetric
+};
+
+template <int T>
+struct Waves {
+    static constexpr int a = 2, b = T == 256 ? 4 : 2, threads = a * b * kWave;
+};
+
+// A symmetric product S = V V^T of the rows (by k: columns) of V, and what is
+// made of it: A = S (kSquare = false), or P = b A + c S of V = A.
+struct SymmetricOut {
+    Held to;
+    bool both;  // planes
+    float b, c;
+};
+
+template <bool kKRows, bool kSquare, int T>
+__global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOperand V, size_t matrix_stride,
+                                                                         ProductShape sh, Tiles tiles, SymmetricOut out)
+{
+    constexpr int WA = Waves<T>::a, WB = Waves<T>::b;
+    using P = TileProduct<true, kKRows, kKRows, T, T, WA, WB>;
+    GCQ_TILE_BUFFERS(lds, T, T);
+    const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), matrix = id / tiles.per_matrix;
+    uint32_t ta, tb;
+    triangle_of(id - matrix * tiles.per_matrix, ta, tb);
+    V.plane0 += matrix * matrix_stride;
+    typename P::Acc acc;
+    P::run(V, V, sh, ta * T, tb * T, 0, sh.turns * sh.segments, lds, acc);
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wa = wave % WA, wb = wave / WA;
+    uint16_t* to = held_at(out.to, matrix, 0);
+#pragma unroll
+    for (int j = 0; j < P::RB; ++j) {
+        const uint32_t b = tb * T + wb * (T / WB) + j * 32 + acc_col(lane);
+        if (b >= out.to.rows)
+            continue;
+#pragma unroll
+        for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t a = ta * T + wa * (T / WA) + i * 32 + acc_row(4 * q, lane);
+                if (a >= out.to.rows)
+                    continue;
+                vec_of<float, 4> v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = acc.v[i][j][4 * q + e];
+                if (kSquare) {
+                    const uint16_t* from = V.plane0 + size_t(b) * V.ld + a;
+                    Planes4 s = {};
+                    s.p0 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from);
+                    if (out.both)
+                        s.p1 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from + V.plane_stride);
+                    const vec_of<float, 4> A = join4(s);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = __builtin_fmaf(v[e], out.c * pow2(kPExp - 2 * kAExp), A[e] * (out.b * pow2(kPExp - kAExp)));
+                } else {
+                    v *= pow2(kAExp - 2 * kXExp);
+                }
+                const Planes4 s = split4(v);
+                uint16_t* o = to + size_t(b) * out.to.ld + a;
+                *reinterpret_cast<vec_of<f16_t, 4>*>(o) = s.p0;
+                if (out.both)
+                    *reinterpret_cast<vec_of<f16_t, 4>*>(o + out.to.plane_stride) = s.p1;
+                if (ta == tb)
+                    continue;
+                uint16_t* mirror = to + size_t(a) * out.to.ld + b;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    mirror[size_t(e) * out.to.ld] = __builtin_bit_cast(uint16_t, f16_t(s.p0[e]));
+                    if (out.both)
+                        mirror[out.to.plane_stride + size_t(e) * out.to.ld] = __builtin_bit_cast(uint16_t, f16_t(s.p1[e]));
+                }
+            }
+    }
+}
+
+// P = b A of a step without a second power.
+__global__ __launch_bounds__(kThreads) void scale_kernel(Held A, Held P, bool both, float b, size_t chunks)
+{
+    const float f = b * pow2(kPExp - kAExp);
+    for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < chunks; i += size_t(gridDim.x) * kThreads) {
+        Planes4 s = {};
+        s.p0 = *reinterpret_cast<const vec_of<f16_t, 4>*>(A.plane0 + i * 4);
+        if (both)
+            s.p1 = *reinterpret_cast<const vec_of<f16_t, 4>*>(A.plane0 + A.plane_stride + i * 4);
+        s = split4(join4(s) * f);
+        *reinterpret_cast<vec_of<f16_t, 4>*>(P.plane0 + i * 4) = s.p0;
+        if (both)
+            *reinterpret_cast<vec_of<f16_t, 4>*>(P.plane0 + P.plane_stride + i * 4) = s.p1;
+    }
+}
+
+// What the last step writes: out = scale X, or new weights = (1 - lr decay)
+// weights - lr scale X.
+struct LastOut {
+    PtrTable<void> weights, out;
+    int dtype;
+    bool update;
+    uint32_t m, n;
+    float scale, lr, decay;
+    const float* lr_scale;
+};
+
+template <typename T>
+__device__ __forceinline__ void write_last(const LastOut& o, uint32_t matrix, size_t r, uint32_t c, vec_of<float, 4> x,
+                                           float keep, float factor)
+{
+    const size_t at = r * o.n + c;
+    T* to = static_cast<T*>(const_cast<void*>(o.out.p[matrix])) + at;
+    const T* w = o.update ? static_cast<const T*>(o.weights.p[matrix]) + at : nullptr;
+    typedef T Vec __attribute__((ext_vector_type(4)));
+    typedef Vec VecAny __attribute__((aligned(sizeof(T))));
+    if (c + 4 <= o.n) {
+        x *= factor;
+        if (w) {
+            const vec_of<float, 4> old = __builtin_convertvector(*reinterpret_cast<const VecAny*>(w), vec_of<float, 4>);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[e] = __builtin_fmaf(old[e], keep, -x[e]);
+        }
+        *reinterpret_cast<VecAny*>(to) = __builtin_convertvector(x, Vec);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (c + e < o.n) {
+            const float v = x[e] * factor;
+            to[e] = T(w ? __builtin_fmaf(float(w[e]), keep, -v) : v);
+        }
+}
+
+// out[b][a] = X[b][a] * a_coef + sum over k of A(a, k) B(b, k): of a wide X, A
+// is X by k and B is P; of a tall one, A is P and B is X. kLast: the last step.
+struct UpdateOut {
+    Held from, to;
+    float a;
+};
+
+template <bool kTall, bool kLast, int T>
+__global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand A, size_t a_stride, MatOperand B,
+                                                                      size_t b_stride, ProductShape sh, Tiles tiles,
+                                                                      UpdateOut out, LastOut last)
+{
+    constexpr int WA = Waves<T>::a, WB = Waves<T>::b;
+    using P = TileProduct<true, !kTall, false, T, T, WA, WB>;
+    GCQ_TILE_BUFFERS(lds, T, T);
+    const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), matrix = id / tiles.per_matrix;
+    uint32_t ta, tb;
+    tile_of(id - matrix * tiles.per_matrix, tiles.a, tiles.b, ta, tb);
+    A.plane0 += matrix * a_stride;
+    B.plane0 += matrix * b_stride;
+    typename P::Acc acc;
+    P::run(A, B, sh, ta * T, tb * T, 0, sh.turns * sh.segments, lds, acc);
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wa = wave % WA, wb = wave / WA;
+    const uint16_t* from = held_at(out.from, matrix, 0);
+    uint16_t* to = kLast ? nullptr : held_at(out.to, matrix, 0);
+    float keep = 1.0f, factor = last.scale * (1.0f / kXScale);
+    if (kLast && last.update) {
+        const float lr = last.lr_scale ? last.lr * *last.lr_scale : last.lr;
+        keep = __builtin_fmaf(-lr, last.decay, 1.0f);
+        factor = lr * last.scale * (1.0f / kXScale);
+    }
+    const uint32_t rows = kLast ? last.m : out.from.rows, cols = kLast ? last.n : out.from.ld;
+#pragma unroll
+    for (int j = 0; j < P::RB; ++j) {
+        const uint32_t b = tb * T + wb * (T / WB) + j * 32 + acc_col(lane);
+        if (b >= rows)
+            continue;
+#pragma unroll
+        for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t a = ta * T + wa * (T / WA) + i * 32 + acc_row(4 * q, lane);
+                if (a >= cols)
+                    continue;
+                const size_t at = size_t(b) * out.from.ld + a;
+                Planes4 s;
+                s.p0 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from + at);
+                s.p1 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from + out.from.plane_stride + at);
+                vec_of<float, 4> v = join4(s);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = __builtin_fmaf(v[e], out.a, acc.v[i][j][4 * q + e] * pow2(-kPExp));
+                if (kLast) {
+                    if (last.dtype == GC_F32)
+                        write_last<float>(last, matrix, b, a, v, keep, factor);
+                    else if (last.dtype == GC_BF16)
+                        write_last<bf16_t>(last, matrix, b, a, v, keep, factor);
+                    else
+                        write_last<f16_t>(last, matrix, b, a, v, keep, factor);
+                } else {
+                    s = split4(v);
+                    *reinterpret_cast<vec_of<f16_t, 4>*>(to + at) = s.p0;
+                    *reinterpret_cast<vec_of<f16_t, 4>*>(to + out.to.plane_stride + at) = s.p1;
+                }
+            }
+    }
+}
+
+// ---- host side -----------------------------------------------------------------
+
+size_t round_up(size_t a, size_t b) { return ceil_div(a, b) * b; }
+
+constexpr size_t kMaxSide = size_t(1) << 20, kMaxSmallSide = size_t(1) << 15, kMaxTiles = size_t(1) << 22;
+constexpr int kMaxSteps = 64;
+
+struct Layout {
+    size_t m, n, small;     // small: the side of A
+    bool tall, both;        // both: products of both planes
+    Held x[2], A, P;        // their plane0: an offset into the workspace
+    size_t parts, zero, zeros, total;  // bytes
+    uint32_t nparts;
+};
+
+Layout layout_of(size_t count, size_t m, size_t n, bool both)
+{
+    Layout L{};
+    L.m = m;
+    L.n = n;
+    L.tall = m > n;
+    L.both = both;
+    L.small = std::min(m, n);
+    const size_t rows = round_up(m, kTurnK), cols = round_up(n, kTurnK), side = round_up(L.small, kTurnK);
+    size_t used = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t at = used;
+        used += (bytes + 255) & ~size_t(255);
+        return at;
+    };
+    const auto hold = [&](size_t r, size_t ld, int planes) {
+        Held h{};
+        h.matrix_stride = r * ld;
+        h.plane_stride = count * r * ld;
+        h.ld = uint32_t(ld);
+        h.rows = uint32_t(r);
+        h.plane0 = reinterpret_cast<uint16_t*>(take(planes * h.plane_stride * 2));
+        return h;
+    };
+    L.nparts = uint32_t(std::min<size_t>(kMaxParts, ceil_div(m * n, kThreads * 8 * 4)));
+    L.parts = take(count * L.nparts * sizeof(double));
+    L.x[0] = hold(rows, cols, 2);
+    L.zero = used;
+    L.x[1] = hold(rows, cols, 2);
+    L.A = hold(side, side, both ? 2 : 1);
+    L.P = hold(side, side, both ? 2 : 1);
+    L.zeros = used - L.zero;
+    L.total = used;
+    return L;
+}
+
+void place(Held& h, char* ws) { h.plane0 = reinterpret_cast<uint16_t*>(ws + reinterpret_cast<size_t>(h.plane0)); }
+
+MatOperand operand(const Held& h)
+{
+    MatOperand o{};
+    o.plane0 = h.plane0;
+    o.plane_stride = h.plane_stride;
+    o.ld = h.ld;
+    return o;
+}
+
+size_t triangle_tiles(size_t side, size_t t) { return ceil_div(side, t) * (ceil_div(side, t) + 1) / 2; }
+size_t all_tiles(size_t a, size_t b, size_t t) { return ceil_div(a, t) * ceil_div(b, t); }
+
+// Tiles of 256 x 256 as long as there are enough of them to fill half of the
+// chip, else of 128 x 128, else of 64 x 64.
+constexpr size_t kHalfOfChip = 128;
+
+int symmetric_tile(size_t count, size_t side)
+{
+    return count * triangle_tiles(side, 256) >= kHalfOfChip   ? 256
+           : count * triangle_tiles(side, 128) >= kHalfOfChip ? 128
+                                                              : 64;
+}
+
+int update_tile(size_t count, size_t m, size_t n)
+{
+    return count * all_tiles(m, n, 256) >= kHalfOfChip ? 256 : count * all_tiles(m, n, 128) >= kHalfOfChip ? 128 : 64;
+}
+
+// Calls f with the tile as an integral constant.
+template <typename F>
+void with_tile(int tile, F f)
+{
+    if (tile == 256)
+        f(std::integral_constant<int, 256>());
+    else if (tile == 128)
+        f(std::integral_constant<int, 128>());
+    else
+        f(std::integral_constant<int, 64>());
+}
+
+// Whether tiles of 64 leave padding unwritten (128 is what it goes by), which
+// then has to be zero from the start.
+bool leaves_padding(const Layout& L, size_t count)
+{
+    const auto half = [](size_t v) { return round_up(v, 64) % kTurnK != 0; };
+    return (symmetric_tile(count, L.small) == 64 && half(L.small)) ||
+           (update_tile(count, L.m, L.n) == 64 && (half(L.m) || half(L.n)));
+}
+
+ProductShape shape_of(size_t k, bool both)
+{
+    ProductShape sh{};
+    sh.turns = uint32_t(k / kTurnK);
+    set_pairs(sh, both ? 2 : 1, both ? 2 : 1);
+    sh.splits = 1;
+    return sh;
+}
+
+template <bool kKRows, bool kSquare>
+void launch_symmetric(const Held& v, size_t side, size_t k, size_t count, const SymmetricOut& out, hipStream_t stream)
+{
+    MatOperand o = operand(v);
+    o.extent = kKRows ? v.ld : v.rows;
+    o.krows = v.rows;
+    const ProductShape sh = shape_of(k, out.both);
+    with_tile(symmetric_tile(count, side), [&](auto t) {
+        constexpr int T = decltype(t)::value;
+        Tiles tiles{};
+        tiles.per_matrix = uint32_t(triangle_tiles(side, T));
+        hipLaunchKernelGGL((symmetric_kernel<kKRows, kSquare, T>), dim3(unsigned(tiles.per_matrix * count)),
+                           dim3(Waves<T>::threads), 0, stream, o, v.matrix_stride, sh, tiles, out);
+    });
+}
+
+template <bool kTall, bool kLast>
+void launch_update(const Layout& L, size_t count, const UpdateOut& out, const LastOut& last, hipStream_t stream)
+{
+    MatOperand X = operand(out.from), P = operand(L.P);
+    X.extent = kTall ? out.from.rows : out.from.ld;
+    X.krows = out.from.rows;
+    P.extent = L.P.rows;
+    const ProductShape sh = shape_of(L.P.ld, L.both);
+    with_tile(update_tile(count, L.m, L.n), [&](auto t) {
+        constexpr int T = decltype(t)::value;
+        Tiles tiles{};
+        tiles.a = uint32_t(ceil_div(L.n, T));
+        tiles.b = uint32_t(ceil_div(L.m, T));
+        tiles.per_matrix = tiles.a * tiles.b;
+        const dim3 grid(unsigned(tiles.per_matrix * count));
+        if (kTall)
+            hipLaunchKernelGGL((update_kernel<kTall, kLast, T>), grid, dim3(Waves<T>::threads), 0, stream, P,
+                               L.P.matrix_stride, X, out.from.matrix_stride, sh, tiles, out, last);
+        else
+            hipLaunchKernelGGL((update_kernel<kTall, kLast, T>), grid, dim3(Waves<T>::threads), 0, stream, X,
+                               out.from.matrix_stride, P, L.P.matrix_stride, sh, tiles, out, last);
+    });
+}
+
+// The iteration, from X_0 in L.x[0] on.
+template <bool kTall>
+void iterate(const Layout& L, size_t count, const float* coefficients, int steps, const LastOut& last,
+             hipStream_t stream)
+{
+    for (int s = 0; s < steps; ++s) {
+        const float a = coefficients[3 * s], b = coefficients[3 * s + 1], c = coefficients[3 * s + 2];
+        const Held &from = L.x[s & 1], &to = L.x[(s + 1) & 1];
+        launch_symmetric<kTall, false>(from, L.small, kTall ? from.rows : from.ld, count,
+                                       SymmetricOut{L.A, L.both, 0.0f, 0.0f}, stream);
+        if (c != 0.0f) {
+            launch_symmetric<false, true>(L.A, L.small, L.A.ld, count, SymmetricOut{L.P, L.both, b, c}, stream);
+        } else {
+            const size_t chunks = L.A.plane_stride / 4;
+            hipLaunchKernelGGL(scale_kernel, dim3(unsigned(std::min<size_t>(ceil_div(chunks, kThreads), 2048))),
+                               dim3(kThreads), 0, stream, L.A, L.P, L.both, b, chunks);
+        }
+        if (s + 1 < steps)
+            launch_update<kTall, false>(L, count, UpdateOut{from, to, a}, last, stream);
+        else
+            launch_update<kTall, true>(L, count, UpdateOut{from, to, a}, last, stream);
+    }
+}
+
+struct Call {
+    const char* what;
+    size_t count, m, n;
+    int out_dtype;      // of the accuracy asked for
+    const float* coefficients;
+    int steps;
+    float eps;
+    void* ws;
+    size_t* ws_bytes;
+};
+
+int refuse(const Call& c, const char* why, gc_status code = GC_EINVAL) { return fail(code, std::string(c.what) + ": " + why); }
+
+// What both entry points check; 1: a query of the workspace, answered.
+int check_call(const Call& c, Layout& L)
+{
+    if (!dtype_bytes(c.out_dtype))
+        return refuse(c, "unknown dtype");
+    if (c.count < 1 || c.count > GC_MAX_WORKERS)
+        return refuse(c, "the number of matrices must lie in 1 .. 64");
+    if (c.m > kMaxSide || c.n > kMaxSide || std::min(c.m, c.n) > kMaxSmallSide ||
+        c.count * all_tiles(c.m, c.n, 256) > kMaxTiles)
+        return refuse(c, "sides beyond 2^20 (the smaller one 2^15), or more than 2^22 tiles of 256 x 256",
+                      GC_EUNSUPPORTED);
+    if (!c.ws_bytes)
+        return refuse(c, "ws_bytes is NULL");
+    L = layout_of(c.count, c.m, c.n, c.out_dtype != GC_BF16);
+    if (!c.ws) {
+        *c.ws_bytes = std::max<size_t>(L.total, 256);
+        return 1;
+    }
+    if (c.steps < 1 || c.steps > kMaxSteps || !c.coefficients)
+        return refuse(c, "1 to 64 steps of three coefficients each");
+    for (int k = 0; k < 3 * c.steps; ++k)
+        if (!std::isfinite(c.coefficients[k]))
+            return refuse(c, "a coefficient is not finite");
+    if (!(c.eps >= 0.0f) || !std::isfinite(c.eps))
+        return refuse(c, "eps must not be negative");
+    if (!aligned16(c.ws) || *c.ws_bytes < L.total)
+        return refuse(c, "workspace too small or not 16-byte aligned");
+    place(L.x[0], static_cast<char*>(c.ws));
+    place(L.x[1], static_cast<char*>(c.ws));
+    place(L.A, static_cast<char*>(c.ws));
+    place(L.P, static_cast<char*>(c.ws));
+    return GC_OK;
+}
+
+// Copies `count` pointers, each to values of `bytes` bytes.
+template <typename T>
+bool take_pointers(PtrTable<T>& t, const void* const* p, size_t count, size_t bytes)
+{
+    for (size_t k = 0; k < count; ++k) {
+        if (!p || !p[k] || !aligned_to(p[k], bytes))
+            return false;
+        t.p[k] = static_cast<const T*>(p[k]);
+    }
+    return true;
+}
+
+template <typename T, bool kMomentum>
+int run_call(const Call& c, const Layout& L, const PtrTable<T>& x, const PtrTable<float>& momenta,
+             const PtrTable<float>& new_momenta, const Momentum& mo, const LastOut& last, hipStream_t stream)
+{
+    char* ws = static_cast<char*>(c.ws);
+    double* parts = reinterpret_cast<double*>(ws + L.parts);
+    hipLaunchKernelGGL((norm_kernel<T, kMomentum>), dim3(L.nparts, unsigned(c.count)), dim3(kThreads), 0, stream, x,
+                       momenta, new_momenta, mo, c.m * c.n, parts, reinterpret_cast<u32x4*>(ws + L.zero),
+                       leaves_padding(L, c.count) ? L.zeros / 16 : 0);
+    const size_t chunks = L.x[0].matrix_stride / 8;
+    hipLaunchKernelGGL((first_kernel<T, kMomentum>),
+                       dim3(unsigned(std::min<size_t>(ceil_div(chunks, kThreads * 4), kMaxParts)), unsigned(c.count)),
+                       dim3(kThreads), 0, stream, x, new_momenta, mo, c.m, c.n, c.eps, parts, L.nparts, L.x[0]);
+    if (L.tall)
+        iterate<true>(L, c.count, c.coefficients, c.steps, last, stream);
+    else
+        iterate<false>(L, c.count, c.coefficients, c.steps, last, stream);
+    return check_launch(c.what);
+}
+
+}  // namespace
+}  // namespace gcq
+
+using namespace gcq;
+
+GCQ_API int orthogonalize(const void* const* x, int count, size_t m, size_t n, int dtype, const float* coefficients,
+                          int steps, float eps, float scale, void* const* out, int out_dtype, void* ws,
+                          size_t* ws_bytes, hipStream_t stream)
+{
+    clear_error();
+    const Call c{"orthogonalize", size_t(std::max(count, 0)), m, n, out_dtype, coefficients, steps, eps, ws, ws_bytes};
+    Layout L;
+    if (int rc = check_call(c, L))
+        return rc > 0 ? GC_OK : rc;
+    if (!dtype_bytes(dtype))
+        return refuse(c, "unknown dtype");
+    if (m == 0 || n == 0)
+        return GC_OK;
+    PtrTable<void> from{};
+    LastOut last{};
+    if (!take_pointers(from, x, c.count, dtype_bytes(dtype)) ||
+        !take_pointers(last.out, out, c.count, dtype_bytes(out_dtype)))
+        return refuse(c, "a matrix is NULL or misaligned");
+    last.dtype = out_dtype;
+    last.m = uint32_t(m);
+    last.n = uint32_t(n);
+    last.scale = scale;
+    return with_dtype(dtype, [&](auto e) {
+        using T = decltype(e);
+        PtrTable<T> typed{};
+        for (size_t k = 0; k < c.count; ++k)
+            typed.p[k] = static_cast<const T*>(from.p[k]);
+        return run_call<T, false>(c, L, typed, PtrTable<float>{}, PtrTable<float>{}, Momentum{}, last, stream);
+    });
+}
+
+GCQ_API int muon_step(const float* const* grads, int count, size_t m, size_t n, const float* const* momenta,
+                      const void* const* weights, int dtype, int update_dtype, const float* coefficients, int steps,
+                      float eps, float grad_scale, float momentum, int nesterov, float lr, const float* lr_scale,
+                      float weight_decay, float update_scale, float* const* new_momenta, void* const* new_weights,
+                      void* ws, size_t* ws_bytes, hipStream_t stream)
+{
+    clear_error();
+    const Call c{"muon_step", size_t(std::max(count, 0)), m, n, update_dtype, coefficients, steps, eps, ws, ws_bytes};
+    Layout L;
+    if (int rc = check_call(c, L))
+        return rc > 0 ? GC_OK : rc;
+    const size_t b = dtype_bytes(dtype);
+    if (!b)
+        return refuse(c, "unknown dtype");
+    if (!(momentum >= 0.0f && momentum < 1.0f))
+        return refuse(c, "momentum must lie in [0, 1)");
+    if (!std::isfinite(grad_scale) || !std::isfinite(lr) || !std::isfinite(weight_decay) ||
+        !std::isfinite(update_scale))
+        return refuse(c, "a scale, rate or decay is not finite");
+    if (!aligned4(lr_scale))
+        return refuse(c, "lr_scale is misaligned");
+    if (m == 0 || n == 0)
+        return GC_OK;
+    PtrTable<float> g{}, m0{}, m1{};
+    LastOut last{};
+    if (!take_pointers(g, reinterpret_cast<const void* const*>(grads), c.count, 4) ||
+        !take_pointers(m0, reinterpret_cast<const void* const*>(momenta), c.count, 4) ||
+        !take_pointers(m1, reinterpret_cast<const void* const*>(new_momenta), c.count, 4) ||
+        !take_pointers(last.weights, weights, c.count, b) || !take_pointers(last.out, new_weights, c.count, b))
+        return refuse(c, "a matrix is NULL or misaligned");
+    last.dtype = dtype;
+    last.update = true;
+    last.m = uint32_t(m);
+    last.n = uint32_t(n);
+    last.scale = update_scale;
+    last.lr = lr;
+    last.decay = weight_decay;
+    last.lr_scale = lr_scale;
+    return run_call<float, true>(c, L, g, m0, m1, Momentum{grad_scale, momentum, nesterov != 0}, last, stream);
+}

@@ -475,6 +475,66 @@ int linear_xent_grad(const void* hidden, const void* weight, int dtype, size_t N
                      int dweight_dtype, void* ws, size_t* ws_bytes,
                      hipStream_t stream);
 
+/* ---- orthogonalised updates ------------------------------------------------- */
+
+/* For each of `count` matrices of m x n:
+ *   X = x / (|x| + eps), |x| the Frobenius norm, then for each step
+ *   X = a X + b (X X') X + c (X X')^2 X   with the step's a, b, c;
+ *   out = scale * X
+ * so that every singular value s of X becomes a s + b s^3 + c s^5 a step and the
+ * singular vectors stay: with (3.4445, -4.7750, 2.0315) five times those that
+ * are not far below the largest come near 1.
+ *   x        host array of `count` pointers to [m, n] of `dtype`
+ *   coefficients  host [steps][3] fp32, read before the call returns
+ *   steps    1 .. 64;  eps >= 0 (0: a zero matrix gives NaN)
+ *   out      host array of `count` pointers to [m, n] of out_dtype; out[k] may
+ *            be x[k] itself
+ *   ws       16-byte-aligned workspace; ws == NULL: *ws_bytes = its size for
+ *            (count, m, n, out_dtype) and nothing is enqueued. Otherwise
+ *            *ws_bytes is its size and must be at least that. Calls that may
+ *            overlap in time need workspaces of their own.
+ * The norm is summed in 64 bits. X is carried from step to step to 22 bits of a
+ * value; the factors of the products are rounded to 11 bits for a bf16 out, to
+ * 22 (three products for each one) for fp16 and fp32; their sums are fp32. The
+ * coefficients have to keep the singular values of X below 3.9, and b s^2 + c
+ * s^4 within 60. A matrix that holds a NaN or an infinity gives NaN throughout;
+ * the others are not touched by it.
+ * count 1 .. 64; m, n <= 2^20, the smaller one <= 2^15, at most 2^22 tiles of
+ * 256 x 256 in all (else GC_EUNSUPPORTED); m or n may be 0. */
+int orthogonalize(const void* const* x, int count, size_t m, size_t n, int dtype,
+                  const float* coefficients, int steps, float eps, float scale,
+                  void* const* out, int out_dtype, void* ws, size_t* ws_bytes,
+                  hipStream_t stream);
+
+/* One step of an optimiser that moves weight matrices along the orthogonalised
+ * momentum of their gradients. For each of `count` matrices of m x n:
+ *   g = grad_scale * grads;  new_momenta = g + momentum * (momenta - g)
+ *   u = nesterov ? g + momentum * (new_momenta - g) : new_momenta
+ *   X = what orthogonalize() makes of u (coefficients, steps, eps)
+ *   new_weights = (1 - r weight_decay) * weights - r update_scale X,
+ *   r = lr * (lr_scale ? *lr_scale : 1)
+ *   grads, momenta, new_momenta  host arrays of `count` pointers to [m, n] fp32;
+ *            new_momenta[k] may be momenta[k] itself. What the reducers of (1)
+ *            and (2) write is read in place: grad_scale = 1 / W makes a mean of
+ *            their sum
+ *   weights, new_weights  host arrays of `count` pointers to [m, n] of `dtype`;
+ *            new_weights[k] may be weights[k] itself
+ *   update_dtype  says how exactly X is computed: as for an out of this type in
+ *            orthogonalize() (it is not rounded to it). With weights of bf16 it
+ *            is GC_BF16 for all that they hold
+ *   momentum 0 .. 1 (below 1)
+ *   lr_scale device fp32, read when the kernel runs, or NULL: a captured call
+ *            follows a schedule that the graph or the caller advances
+ *   ws       as in orthogonalize(), of (count, m, n, update_dtype); limits too
+ * A matrix whose u holds a NaN or an infinity gets weights of NaN. */
+int muon_step(const float* const* grads, int count, size_t m, size_t n,
+              const float* const* momenta, const void* const* weights, int dtype,
+              int update_dtype, const float* coefficients, int steps, float eps,
+              float grad_scale, float momentum, int nesterov, float lr,
+              const float* lr_scale, float weight_decay, float update_scale,
+              float* const* new_momenta, void* const* new_weights, void* ws,
+              size_t* ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
