@@ -14,12 +14,19 @@
 //
 // Precision. X is carried to 22 bits, as two planes of fp16; A and P are held
 // in one plane or two. The operands of the products are the first planes alone
-// (off by at most 2^-11 of a value) where the result is kept in bf16, else both (three
-// products each). a X never loses what the operands round away: its roundings
-// would grow with the small singular values, 3.4 times a step, up to 500 times,
-// while those of P X shrink with s^2. X is held times 2^12 and A times 2^12, P
-// times 2^10: entries are at most a singular value (s, s^2, ..) in size, and the
-// first ones, of a matrix of 4096 x 4096, near 2^-12 and 2^-18.
+// (off by at most 2^-11 of a value) where the result is kept in bf16, else both
+// (three products each). a X never loses what the operands round away: its
+// roundings would grow with the small singular values, 3.4 times a step, up to
+// 500 times, while those of P X shrink with s^2. The diagonals of A and P, near 1
+// and -3 where other entries are far below, are held apart in fp32 and enter by
+// themselves,
+//   (A^2)_ij = (O^2)_ij + (A_ii + A_jj) A_ij,  (A^2)_ii = (O^2)_ii + A_ii^2
+//   (a X + P X)_i = (a + P_ii) X_i + (what is off the diagonal of P) X
+// with O = A off its diagonal: rounded to 11 bits, they would scale whole rows. Of
+// 64 x 576 the result of one plane is then 5e-4 off 64 bits instead of 2e-3.
+// X is held times 2^12, A times 2^12, P times 2^10: entries are at most a singular
+// value (s, s^2, ..) in size, and the first ones, of a matrix of 4096 x 4096, near
+// 2^-12 and 2^-18.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -237,11 +244,14 @@ struct Waves {
 };
 
 // A symmetric product S = V V^T of the rows (by k: columns) of V, and what is
-// made of it: A = S (kSquare = false), or P = b A + c S of V = A.
+// made of it: A = S (kSquare = false), or P = b A + c A^2 of V, A off its
+// diagonal. Diagonals go to (and come from) arrays of their own, [matrix][side].
 struct SymmetricOut {
     Held to;
     bool both;  // planes
     float b, c;
+    const float* from_diagonal;  // of A, if kSquare
+    float* diagonal;
 };
 
 template <bool kKRows, bool kSquare, int T>
@@ -262,11 +272,14 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wa = wave % WA, wb = wave / WA;
     uint16_t* to = held_at(out.to, matrix, 0);
+    float* diagonal = out.diagonal + size_t(matrix) * out.to.rows;
+    const float* old = kSquare ? out.from_diagonal + size_t(matrix) * out.to.rows : nullptr;
 #pragma unroll
     for (int j = 0; j < P::RB; ++j) {
         const uint32_t b = tb * T + wb * (T / WB) + j * 32 + acc_col(lane);
         if (b >= out.to.rows)
             continue;
+        const float db = kSquare ? old[b] : 0.0f;
 #pragma unroll
         for (int i = 0; i < P::RA; ++i)
 #pragma unroll
@@ -284,12 +297,24 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
                     s.p0 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from);
                     if (out.both)
                         s.p1 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from + V.plane_stride);
-                    const vec_of<float, 4> A = join4(s);
+                    const vec_of<float, 4> A = join4(s), da = *reinterpret_cast<const vec_of<float, 4>*>(old + a);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = __builtin_fmaf(v[e], out.c * pow2(kPExp - 2 * kAExp), A[e] * (out.b * pow2(kPExp - kAExp)));
+                    for (int e = 0; e < 4; ++e) {
+                        // (on the diagonal A is 0 in the planes)
+                        const float own = a + e == b ? (out.b + out.c * db) * db * pow2(kPExp) : 0.0f;
+                        v[e] = __builtin_fmaf(v[e], out.c * pow2(kPExp - 2 * kAExp),
+                                              __builtin_fmaf(A[e], (out.b + out.c * (da[e] + db)) * pow2(kPExp - kAExp), own));
+                    }
                 } else {
                     v *= pow2(kAExp - 2 * kXExp);
+                }
+                if (ta == tb) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (a + e == b) {
+                            diagonal[b] = v[e] * pow2(kSquare ? -kPExp : -kAExp);
+                            v[e] = 0.0f;
+                        }
                 }
                 const Planes4 s = split4(v);
                 uint16_t* o = to + size_t(b) * out.to.ld + a;
@@ -310,9 +335,13 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
 }
 
 // P = b A of a step without a second power.
-__global__ __launch_bounds__(kThreads) void scale_kernel(Held A, Held P, bool both, float b, size_t chunks)
+__global__ __launch_bounds__(kThreads) void scale_kernel(Held A, Held P, bool both, float b, size_t chunks,
+                                                         const float* __restrict__ from_diagonal,
+                                                         float* __restrict__ diagonal, size_t diagonals)
 {
     const float f = b * pow2(kPExp - kAExp);
+    for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < diagonals; i += size_t(gridDim.x) * kThreads)
+        diagonal[i] = b * from_diagonal[i];
     for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < chunks; i += size_t(gridDim.x) * kThreads) {
         Planes4 s = {};
         s.p0 = *reinterpret_cast<const vec_of<f16_t, 4>*>(A.plane0 + i * 4);
@@ -369,6 +398,8 @@ __device__ __forceinline__ void write_last(const LastOut& o, uint32_t matrix, si
 struct UpdateOut {
     Held from, to;
     float a;
+    const float* diagonal;  // of P, [matrix][side]
+    uint32_t side;
 };
 
 template <bool kTall, bool kLast, int T>
@@ -398,12 +429,14 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
         keep = __builtin_fmaf(-lr, last.decay, 1.0f);
         factor = lr * last.scale * (1.0f / kXScale);
     }
+    const float* diagonal = out.diagonal + size_t(matrix) * out.side;
     const uint32_t rows = kLast ? last.m : out.from.rows, cols = kLast ? last.n : out.from.ld;
 #pragma unroll
     for (int j = 0; j < P::RB; ++j) {
         const uint32_t b = tb * T + wb * (T / WB) + j * 32 + acc_col(lane);
         if (b >= rows)
             continue;
+        const float of_row = kTall ? 0.0f : out.a + diagonal[b];
 #pragma unroll
         for (int i = 0; i < P::RA; ++i)
 #pragma unroll
@@ -415,10 +448,12 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
                 Planes4 s;
                 s.p0 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from + at);
                 s.p1 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from + out.from.plane_stride + at);
-                vec_of<float, 4> v = join4(s);
+                vec_of<float, 4> v = join4(s), self = vec_of<float, 4>{} + of_row;
+                if (kTall)
+                    self = *reinterpret_cast<const vec_of<float, 4>*>(diagonal + a) + out.a;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    v[e] = __builtin_fmaf(v[e], out.a, acc.v[i][j][4 * q + e] * pow2(-kPExp));
+                    v[e] = __builtin_fmaf(v[e], self[e], acc.v[i][j][4 * q + e] * pow2(-kPExp));
                 if (kLast) {
                     if (last.dtype == GC_F32)
                         write_last<float>(last, matrix, b, a, v, keep, factor);
@@ -446,7 +481,7 @@ struct Layout {
     size_t m, n, small;     // small: the side of A
     bool tall, both;        // both: products of both planes
     Held x[2], A, P;        // their plane0: an offset into the workspace
-    size_t parts, zero, zeros, total;  // bytes
+    size_t parts, diagonals[2], zero, zeros, total;  // bytes; diagonals of A and P
     uint32_t nparts;
 };
 
@@ -481,6 +516,8 @@ Layout layout_of(size_t count, size_t m, size_t n, bool both)
     L.x[1] = hold(rows, cols, 2);
     L.A = hold(side, side, both ? 2 : 1);
     L.P = hold(side, side, both ? 2 : 1);
+    L.diagonals[0] = take(count * side * sizeof(float));
+    L.diagonals[1] = take(count * side * sizeof(float));
     L.zeros = used - L.zero;
     L.total = used;
     return L;
@@ -588,25 +625,29 @@ void launch_update(const Layout& L, size_t count, const UpdateOut& out, const La
 
 // The iteration, from X_0 in L.x[0] on.
 template <bool kTall>
-void iterate(const Layout& L, size_t count, const float* coefficients, int steps, const LastOut& last,
+void iterate(const Layout& L, size_t count, const float* coefficients, int steps, const LastOut& last, char* ws,
              hipStream_t stream)
 {
+    float* of_a = reinterpret_cast<float*>(ws + L.diagonals[0]);
+    float* of_p = reinterpret_cast<float*>(ws + L.diagonals[1]);
     for (int s = 0; s < steps; ++s) {
         const float a = coefficients[3 * s], b = coefficients[3 * s + 1], c = coefficients[3 * s + 2];
         const Held &from = L.x[s & 1], &to = L.x[(s + 1) & 1];
         launch_symmetric<kTall, false>(from, L.small, kTall ? from.rows : from.ld, count,
-                                       SymmetricOut{L.A, L.both, 0.0f, 0.0f}, stream);
+                                       SymmetricOut{L.A, L.both, 0.0f, 0.0f, nullptr, of_a}, stream);
         if (c != 0.0f) {
-            launch_symmetric<false, true>(L.A, L.small, L.A.ld, count, SymmetricOut{L.P, L.both, b, c}, stream);
+            launch_symmetric<false, true>(L.A, L.small, L.A.ld, count, SymmetricOut{L.P, L.both, b, c, of_a, of_p},
+                                          stream);
         } else {
             const size_t chunks = L.A.plane_stride / 4;
             hipLaunchKernelGGL(scale_kernel, dim3(unsigned(std::min<size_t>(ceil_div(chunks, kThreads), 2048))),
-                               dim3(kThreads), 0, stream, L.A, L.P, L.both, b, chunks);
+                               dim3(kThreads), 0, stream, L.A, L.P, L.both, b, chunks, of_a, of_p,
+                               count * L.A.rows);
         }
         if (s + 1 < steps)
-            launch_update<kTall, false>(L, count, UpdateOut{from, to, a}, last, stream);
+            launch_update<kTall, false>(L, count, UpdateOut{from, to, a, of_p, L.P.rows}, last, stream);
         else
-            launch_update<kTall, true>(L, count, UpdateOut{from, to, a}, last, stream);
+            launch_update<kTall, true>(L, count, UpdateOut{from, to, a, of_p, L.P.rows}, last, stream);
     }
 }
 
@@ -683,9 +724,9 @@ int run_call(const Call& c, const Layout& L, const PtrTable<T>& x, const PtrTabl
                        dim3(unsigned(std::min<size_t>(ceil_div(chunks, kThreads * 4), kMaxParts)), unsigned(c.count)),
                        dim3(kThreads), 0, stream, x, new_momenta, mo, c.m, c.n, c.eps, parts, L.nparts, L.x[0]);
     if (L.tall)
-        iterate<true>(L, c.count, c.coefficients, c.steps, last, stream);
+        iterate<true>(L, c.count, c.coefficients, c.steps, last, ws, stream);
     else
-        iterate<false>(L, c.count, c.coefficients, c.steps, last, stream);
+        iterate<false>(L, c.count, c.coefficients, c.steps, last, ws, stream);
     return check_launch(c.what);
 }
 
