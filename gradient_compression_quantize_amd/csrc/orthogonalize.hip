@@ -141,28 +141,33 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(PtrTable<T> x, PtrTable<
         zero[i] = u32x4{0, 0, 0, 0};
 }
 
-// Two planes of a value: x = p0 + 2^-11 p1 to 2^-22 of it.
-struct Planes4 {
-    vec_of<f16_t, 4> p0, p1;
+// Eight values as two planes: x = p0 + 2^-11 p1 to 2^-22 of it.
+typedef vec_of<float, 8> f32x8;
+
+struct Planes8 {
+    f16x8 p0, p1;
 };
 
-__device__ __forceinline__ Planes4 split4(vec_of<float, 4> v)
+__device__ __forceinline__ Planes8 split8(f32x8 v)
 {
-    Planes4 s;
-    s.p0 = __builtin_convertvector(v, vec_of<f16_t, 4>);
-    s.p1 = __builtin_convertvector((v - __builtin_convertvector(s.p0, vec_of<float, 4>)) * 0x1p11f, vec_of<f16_t, 4>);
+    Planes8 s;
+    s.p0 = __builtin_convertvector(v, f16x8);
+    s.p1 = __builtin_convertvector((v - __builtin_convertvector(s.p0, f32x8)) * 0x1p11f, f16x8);
     return s;
 }
 
-__device__ __forceinline__ vec_of<float, 4> join4(Planes4 s)
+__device__ __forceinline__ f32x8 join8(Planes8 s)
 {
-    const vec_of<float, 4> lo = __builtin_convertvector(s.p1, vec_of<float, 4>);
-    vec_of<float, 4> v = __builtin_convertvector(s.p0, vec_of<float, 4>);
+    const f32x8 lo = __builtin_convertvector(s.p1, f32x8);
+    f32x8 v = __builtin_convertvector(s.p0, f32x8);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 8; ++e)
         v[e] = __builtin_fmaf(lo[e], 0x1p-11f, v[e]);
     return v;
 }
+
+__device__ __forceinline__ f16x8 load_plane(const uint16_t* p) { return *reinterpret_cast<const f16x8*>(p); }
+__device__ __forceinline__ void store_plane(uint16_t* p, f16x8 v) { *reinterpret_cast<f16x8*>(p) = v; }
 
 // A matrix of the workspace, of each of `count`: [rows][ld], two planes of all
 // of them one behind the other.
@@ -207,15 +212,10 @@ __global__ __launch_bounds__(kThreads) void first_kernel(PtrTable<T> x, PtrTable
             for (int e = 0; e < 8; ++e)
                 v[e] = float(double(v[e]) * factor);
         }
-        const Planes4 lo = split4(v.lo), hi = split4(v.hi);
+        const Planes8 s = split8(v);
         uint16_t* o = held_at(to, k, 0) + r * to.ld + c;
-        vec_of<f16_t, 8> w;
-        w.lo = lo.p0;
-        w.hi = hi.p0;
-        *reinterpret_cast<vec_of<f16_t, 8>*>(o) = w;
-        w.lo = lo.p1;
-        w.hi = hi.p1;
-        *reinterpret_cast<vec_of<f16_t, 8>*>(o + to.plane_stride) = w;
+        store_plane(o, s.p0);
+        store_plane(o + to.plane_stride, s.p1);
     }
 }
 
@@ -243,6 +243,101 @@ struct Waves {
     static constexpr int a = 2, b = T == 256 ? 4 : 2, threads = a * b * kWave;
 };
 
+// A wave's part of a tile as rows: 32 rows of b at a time go through the wave's
+// own part of the LDS that the product has left, fp32, as an image of 32 rows of
+// kCols values in 16-byte chunks that an XOR of the row spreads over the banks.
+// A lane then holds 8 values of a row, so that what is loaded and stored beside
+// them is 16 bytes a lane and whole rows of the part: as the matrix cores leave
+// them, 4 values of 32 rows each, the update of 4096 x 4096 took 221 us instead
+// of XXX.
+template <int T>
+struct PartRows {
+    using W = Waves<T>;
+    static constexpr int kCols = T / W::a, kRowsB = T / W::b;  // of a wave
+    static constexpr int kChunks = kCols / 4;
+    static constexpr int kLanes = kCols / 8, kStep = kWave / kLanes, kPasses = 32 / kStep;
+    // (an address of LDS throughout: as a generic one the choice of the buffer
+    // would become a table, and LDS has no addresses to put there)
+    typedef __attribute__((address_space(3))) float lds_f32;
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+    lds_f32* image;
+    uint32_t a, b;  // where the wave's part starts
+    int lane;
+
+    __device__ __forceinline__ PartRows(const TileBuffers& lds, uint32_t a_first, uint32_t b_first)
+    {
+        static_assert(32 * kCols * 4 <= T * kStageK * 2, "an image fits a buffer");
+        static_assert(W::a * W::b <= 2 * kBuffers, "a buffer for each wave");
+        lane = threadIdx.x & (kWave - 1);
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        image = (lds_f32*)lds.a[0];
+#pragma unroll
+        for (int k = 1; k < W::a * W::b; ++k) {
+            lds_f32* const p = (lds_f32*)(k < kBuffers ? lds.a[k % kBuffers] : lds.b[k % kBuffers]);
+            image = wave == k ? p : image;
+        }
+        a = a_first + wave % W::a * kCols;
+        b = b_first + wave / W::a * kRowsB;
+    }
+
+    __device__ __forceinline__ lds_f32* chunk(int row, int c) const
+    {
+        return image + row * kCols + ((c ^ (row & (kChunks - 1))) << 2);
+    }
+
+    // Products [i][j] of all i into the image.
+    template <typename Acc>
+    __device__ __forceinline__ void fill(const Acc& acc, int j) const
+    {
+        const int row = int(acc_col(lane));
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f32x4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = acc.v[i][j][4 * q + e];
+                *(lds_f32x4*)chunk(row, i * 8 + 2 * q + (lane >> 5)) = v;
+            }
+        wave_lds_sync();
+    }
+
+    // Row and column (from the part's) of this lane's values in a pass.
+    __device__ __forceinline__ int row(int pass) const { return pass * kStep + lane / kLanes; }
+    __device__ __forceinline__ int col() const { return lane % kLanes * 8; }
+
+    __device__ __forceinline__ f32x8 get(int pass) const
+    {
+        const int c = col() / 4;
+        f32x8 v;
+        v.lo = *(const lds_f32x4*)chunk(row(pass), c);
+        v.hi = *(const lds_f32x4*)chunk(row(pass), c + 1);
+        return v;
+    }
+
+    __device__ __forceinline__ void put(int pass, f32x8 v) const
+    {
+        const int c = col() / 4;
+        *(lds_f32x4*)chunk(row(pass), c) = v.lo;
+        *(lds_f32x4*)chunk(row(pass), c + 1) = v.hi;
+    }
+
+    // The image's transpose: 8 rows of b from 8 (lane % 4) on, of one column, 16
+    // columns a pass.
+    static constexpr int kTurnedPasses = kCols / 16;
+    __device__ __forceinline__ int turned_col(int pass) const { return pass * 16 + lane / 4; }
+    __device__ __forceinline__ f32x8 get_turned(int pass) const
+    {
+        const int c = turned_col(pass), first = lane % 4 * 8;
+        f32x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = chunk(first + e, c >> 2)[c & 3];
+        return v;
+    }
+};
+
 // A symmetric product S = V V^T of the rows (by k: columns) of V, and what is
 // made of it: A = S (kSquare = false), or P = b A + c A^2 of V, A off its
 // diagonal. Diagonals go to (and come from) arrays of their own, [matrix][side].
@@ -268,69 +363,84 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
     typename P::Acc acc;
     P::run(V, V, sh, ta * T, tb * T, 0, sh.turns * sh.segments, lds, acc);
 
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int wa = wave % WA, wb = wave / WA;
+    const PartRows<T> part(lds, ta * T, tb * T);
     uint16_t* to = held_at(out.to, matrix, 0);
     float* diagonal = out.diagonal + size_t(matrix) * out.to.rows;
     const float* old = kSquare ? out.from_diagonal + size_t(matrix) * out.to.rows : nullptr;
+    const uint32_t side = out.to.rows, a = part.a + part.col();
+    const bool in_a = a < side;
+    f32x8 da = {};
+    if (kSquare && in_a)
+        da = *reinterpret_cast<const f32x8*>(old + a);
 #pragma unroll
     for (int j = 0; j < P::RB; ++j) {
-        const uint32_t b = tb * T + wb * (T / WB) + j * 32 + acc_col(lane);
-        if (b >= out.to.rows)
-            continue;
-        const float db = kSquare ? old[b] : 0.0f;
+        Planes8 A[PartRows<T>::kPasses];
+        float db[PartRows<T>::kPasses];
+        if (kSquare) {
 #pragma unroll
-        for (int i = 0; i < P::RA; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t a = ta * T + wa * (T / WA) + i * 32 + acc_row(4 * q, lane);
-                if (a >= out.to.rows)
-                    continue;
-                vec_of<float, 4> v;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = acc.v[i][j][4 * q + e];
-                if (kSquare) {
+            for (int p = 0; p < PartRows<T>::kPasses; ++p) {
+                const uint32_t b = part.b + j * 32 + part.row(p);
+                A[p] = Planes8{};
+                db[p] = 0.0f;
+                if (in_a && b < side) {
                     const uint16_t* from = V.plane0 + size_t(b) * V.ld + a;
-                    Planes4 s = {};
-                    s.p0 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from);
+                    A[p].p0 = load_plane(from);
                     if (out.both)
-                        s.p1 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from + V.plane_stride);
-                    const vec_of<float, 4> A = join4(s), da = *reinterpret_cast<const vec_of<float, 4>*>(old + a);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // (on the diagonal A is 0 in the planes)
-                        const float own = a + e == b ? (out.b + out.c * db) * db * pow2(kPExp) : 0.0f;
-                        v[e] = __builtin_fmaf(v[e], out.c * pow2(kPExp - 2 * kAExp),
-                                              __builtin_fmaf(A[e], (out.b + out.c * (da[e] + db)) * pow2(kPExp - kAExp), own));
-                    }
-                } else {
-                    v *= pow2(kAExp - 2 * kXExp);
-                }
-                if (ta == tb) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (a + e == b) {
-                            diagonal[b] = v[e] * pow2(kSquare ? -kPExp : -kAExp);
-                            v[e] = 0.0f;
-                        }
-                }
-                const Planes4 s = split4(v);
-                uint16_t* o = to + size_t(b) * out.to.ld + a;
-                *reinterpret_cast<vec_of<f16_t, 4>*>(o) = s.p0;
-                if (out.both)
-                    *reinterpret_cast<vec_of<f16_t, 4>*>(o + out.to.plane_stride) = s.p1;
-                if (ta == tb)
-                    continue;
-                uint16_t* mirror = to + size_t(a) * out.to.ld + b;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    mirror[size_t(e) * out.to.ld] = __builtin_bit_cast(uint16_t, f16_t(s.p0[e]));
-                    if (out.both)
-                        mirror[out.to.plane_stride + size_t(e) * out.to.ld] = __builtin_bit_cast(uint16_t, f16_t(s.p1[e]));
+                        A[p].p1 = load_plane(from + V.plane_stride);
+                    db[p] = old[b];
                 }
             }
+        }
+        part.fill(acc, j);
+#pragma unroll
+        for (int p = 0; p < PartRows<T>::kPasses; ++p) {
+            const uint32_t b = part.b + j * 32 + part.row(p);
+            f32x8 v = part.get(p);
+            if (kSquare) {
+                const f32x8 x = join8(A[p]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // (on the diagonal A is 0 in the planes)
+                    const float own = a + e == b ? (out.b + out.c * db[p]) * db[p] * pow2(kPExp) : 0.0f;
+                    const float times = (out.b + out.c * (da[e] + db[p])) * pow2(kPExp - kAExp);
+                    v[e] = __builtin_fmaf(v[e], out.c * pow2(kPExp - 2 * kAExp), __builtin_fmaf(x[e], times, own));
+                }
+            } else {
+                v *= pow2(kAExp - 2 * kXExp);
+            }
+            if (ta == tb) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (a + e == b && b < side) {
+                        diagonal[b] = v[e] * pow2(kSquare ? -kPExp : -kAExp);
+                        v[e] = 0.0f;
+                    }
+            } else {
+                part.put(p, v);
+            }
+            if (in_a && b < side) {
+                const Planes8 s = split8(v);
+                uint16_t* o = to + size_t(b) * out.to.ld + a;
+                store_plane(o, s.p0);
+                if (out.both)
+                    store_plane(o + out.to.plane_stride, s.p1);
+            }
+        }
+        wave_lds_sync();
+        if (ta != tb) {
+#pragma unroll
+            for (int p = 0; p < PartRows<T>::kTurnedPasses; ++p) {
+                const uint32_t row = part.a + part.turned_col(p), col = part.b + j * 32 + part.lane % 4 * 8;
+                const Planes8 s = split8(part.get_turned(p));
+                if (row < side && col < side) {
+                    uint16_t* o = to + size_t(row) * out.to.ld + col;
+                    store_plane(o, s.p0);
+                    if (out.both)
+                        store_plane(o + out.to.plane_stride, s.p1);
+                }
+            }
+            wave_lds_sync();
+        }
     }
 }
 
@@ -343,14 +453,14 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(Held A, Held P, bool bo
     for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < diagonals; i += size_t(gridDim.x) * kThreads)
         diagonal[i] = b * from_diagonal[i];
     for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < chunks; i += size_t(gridDim.x) * kThreads) {
-        Planes4 s = {};
-        s.p0 = *reinterpret_cast<const vec_of<f16_t, 4>*>(A.plane0 + i * 4);
+        Planes8 s = {};
+        s.p0 = load_plane(A.plane0 + i * 8);
         if (both)
-            s.p1 = *reinterpret_cast<const vec_of<f16_t, 4>*>(A.plane0 + A.plane_stride + i * 4);
-        s = split4(join4(s) * f);
-        *reinterpret_cast<vec_of<f16_t, 4>*>(P.plane0 + i * 4) = s.p0;
+            s.p1 = load_plane(A.plane0 + A.plane_stride + i * 8);
+        s = split8(join8(s) * f);
+        store_plane(P.plane0 + i * 8, s.p0);
         if (both)
-            *reinterpret_cast<vec_of<f16_t, 4>*>(P.plane0 + P.plane_stride + i * 4) = s.p1;
+            store_plane(P.plane0 + P.plane_stride + i * 8, s.p1);
     }
 }
 
@@ -366,31 +476,29 @@ struct LastOut {
 };
 
 template <typename T>
-__device__ __forceinline__ void write_last(const LastOut& o, uint32_t matrix, size_t r, uint32_t c, vec_of<float, 4> x,
+__device__ __forceinline__ void write_last(const LastOut& o, uint32_t matrix, size_t r, uint32_t c, f32x8 x,
                                            float keep, float factor)
 {
     const size_t at = r * o.n + c;
     T* to = static_cast<T*>(const_cast<void*>(o.out.p[matrix])) + at;
     const T* w = o.update ? static_cast<const T*>(o.weights.p[matrix]) + at : nullptr;
-    typedef T Vec __attribute__((ext_vector_type(4)));
+    typedef T Vec __attribute__((ext_vector_type(8)));
     typedef Vec VecAny __attribute__((aligned(sizeof(T))));
-    if (c + 4 <= o.n) {
-        x *= factor;
+    x *= factor;
+    if (c + 8 <= o.n) {
         if (w) {
-            const vec_of<float, 4> old = __builtin_convertvector(*reinterpret_cast<const VecAny*>(w), vec_of<float, 4>);
+            const f32x8 old = __builtin_convertvector(*reinterpret_cast<const VecAny*>(w), f32x8);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 8; ++e)
                 x[e] = __builtin_fmaf(old[e], keep, -x[e]);
         }
         *reinterpret_cast<VecAny*>(to) = __builtin_convertvector(x, Vec);
         return;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (c + e < o.n) {
-            const float v = x[e] * factor;
-            to[e] = T(w ? __builtin_fmaf(float(w[e]), keep, -v) : v);
-        }
+    for (int e = 0; e < 8; ++e)
+        if (c + e < o.n)
+            to[e] = T(w ? __builtin_fmaf(float(w[e]), keep, -x[e]) : x[e]);
 }
 
 // out[b][a] = X[b][a] * a_coef + sum over k of A(a, k) B(b, k): of a wide X, A
@@ -418,9 +526,7 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
     typename P::Acc acc;
     P::run(A, B, sh, ta * T, tb * T, 0, sh.turns * sh.segments, lds, acc);
 
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int wa = wave % WA, wb = wave / WA;
+    const PartRows<T> part(lds, ta * T, tb * T);
     const uint16_t* from = held_at(out.from, matrix, 0);
     uint16_t* to = kLast ? nullptr : held_at(out.to, matrix, 0);
     float keep = 1.0f, factor = last.scale * (1.0f / kXScale);
@@ -431,42 +537,54 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
     }
     const float* diagonal = out.diagonal + size_t(matrix) * out.side;
     const uint32_t rows = kLast ? last.m : out.from.rows, cols = kLast ? last.n : out.from.ld;
+    const uint32_t a = part.a + part.col();
+    const bool in_a = a < cols;
+    f32x8 of_col = {};
+    if (kTall && in_a)
+        of_col = *reinterpret_cast<const f32x8*>(diagonal + a) + out.a;
 #pragma unroll
     for (int j = 0; j < P::RB; ++j) {
-        const uint32_t b = tb * T + wb * (T / WB) + j * 32 + acc_col(lane);
-        if (b >= rows)
-            continue;
-        const float of_row = kTall ? 0.0f : out.a + diagonal[b];
+        Planes8 X[PartRows<T>::kPasses];
+        float of_row[PartRows<T>::kPasses];
 #pragma unroll
-        for (int i = 0; i < P::RA; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t a = ta * T + wa * (T / WA) + i * 32 + acc_row(4 * q, lane);
-                if (a >= cols)
-                    continue;
-                const size_t at = size_t(b) * out.from.ld + a;
-                Planes4 s;
-                s.p0 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from + at);
-                s.p1 = *reinterpret_cast<const vec_of<f16_t, 4>*>(from + out.from.plane_stride + at);
-                vec_of<float, 4> v = join4(s), self = vec_of<float, 4>{} + of_row;
-                if (kTall)
-                    self = *reinterpret_cast<const vec_of<float, 4>*>(diagonal + a) + out.a;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = __builtin_fmaf(v[e], self[e], acc.v[i][j][4 * q + e] * pow2(-kPExp));
-                if (kLast) {
-                    if (last.dtype == GC_F32)
-                        write_last<float>(last, matrix, b, a, v, keep, factor);
-                    else if (last.dtype == GC_BF16)
-                        write_last<bf16_t>(last, matrix, b, a, v, keep, factor);
-                    else
-                        write_last<f16_t>(last, matrix, b, a, v, keep, factor);
-                } else {
-                    s = split4(v);
-                    *reinterpret_cast<vec_of<f16_t, 4>*>(to + at) = s.p0;
-                    *reinterpret_cast<vec_of<f16_t, 4>*>(to + out.to.plane_stride + at) = s.p1;
-                }
+        for (int p = 0; p < PartRows<T>::kPasses; ++p) {
+            const uint32_t b = part.b + j * 32 + part.row(p);
+            X[p] = Planes8{};
+            of_row[p] = 0.0f;
+            if (in_a && b < rows) {
+                const uint16_t* at = from + size_t(b) * out.from.ld + a;
+                X[p].p0 = load_plane(at);
+                X[p].p1 = load_plane(at + out.from.plane_stride);
+                of_row[p] = kTall ? 0.0f : diagonal[b];
             }
+        }
+        part.fill(acc, j);
+#pragma unroll
+        for (int p = 0; p < PartRows<T>::kPasses; ++p) {
+            const uint32_t b = part.b + j * 32 + part.row(p);
+            const f32x8 x = join8(X[p]);
+            f32x8 v = part.get(p);
+            const float self = out.a + of_row[p];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = __builtin_fmaf(x[e], kTall ? of_col[e] : self, v[e] * pow2(-kPExp));
+            if (!in_a || b >= rows)
+                continue;
+            if (kLast) {
+                if (last.dtype == GC_F32)
+                    write_last<float>(last, matrix, b, a, v, keep, factor);
+                else if (last.dtype == GC_BF16)
+                    write_last<bf16_t>(last, matrix, b, a, v, keep, factor);
+                else
+                    write_last<f16_t>(last, matrix, b, a, v, keep, factor);
+            } else {
+                const Planes8 s = split8(v);
+                uint16_t* o = to + size_t(b) * out.to.ld + a;
+                store_plane(o, s.p0);
+                store_plane(o + out.to.plane_stride, s.p1);
+            }
+        }
+        wave_lds_sync();
     }
 }
 
@@ -639,7 +757,7 @@ void iterate(const Layout& L, size_t count, const float* coefficients, int steps
             launch_symmetric<false, true>(L.A, L.small, L.A.ld, count, SymmetricOut{L.P, L.both, b, c, of_a, of_p},
                                           stream);
         } else {
-            const size_t chunks = L.A.plane_stride / 4;
+            const size_t chunks = L.A.plane_stride / 8;
             hipLaunchKernelGGL(scale_kernel, dim3(unsigned(std::min<size_t>(ceil_div(chunks, kThreads), 2048))),
                                dim3(kThreads), 0, stream, L.A, L.P, L.both, b, chunks, of_a, of_p,
                                count * L.A.rows);
