@@ -31,7 +31,8 @@
 //
 // Measured on 8192 x 64000 x 4096 bf16: 1.13 to 1.27 PFLOP/s (torch's library
 // product of that shape: 1.50). The matrix cores are busy 62 to 70% of the
-// cycles, and power holds the clock near 1.7 GHz: the first form, two stages of
+// cycles, and power holds the clock near 1.7 GHz (4096 x 4096 x 4096 fp16: 1.0 to
+// 1.1 PFLOP/s of random values, 1.7 of zeros): the first form, two stages of
 // 64 k with the reads of one stage behind its barrier, kept them busy 46% at
 // 2.16 GHz and was a tenth slower. Tiles of 128 x 128, two to a compute unit,
 // were a fifth slower; four waves of 128 x 128 outputs each half as fast;
@@ -92,15 +93,21 @@ inline void set_pairs(ProductShape& sh, int planes_a, int planes_b)
 }
 
 // What one lane and wave move of an operand's stage, T rows (or columns) wide.
-template <bool kKRows, int T, int kWaves>
+// kPlain: every row of every stage of an operand by k may be read (else the last
+// one that may be stands for those behind it).
+template <bool kKRows, int T, int kWaves, bool kPlain = false>
 struct StageLoader {
     static constexpr int kLoads = T / 16 / kWaves;  // 1 KB wave loads
     static_assert(kLoads >= 1, "every wave moves at least one load");
     static constexpr int kChunks = T / 8;                // by k: 16-byte chunks of a row
     static constexpr int kRowsPerLoad = 1024 / (2 * T);  // by k
-    uint32_t off[kLoads];  // by rows: byte offset of each load from the tile's first row; by k: of its columns alone
-    uint32_t row;          // by k: the first load's row
-    size_t origin;         // by rows: values before the tile's first row
+    static constexpr bool kClamped = kKRows && !kPlain;
+    // byte offset of each load: by rows from the tile's first row, by k from
+    // the stage's first row (clamped: of its columns alone)
+    uint32_t off[kLoads];
+    uint32_t row;   // by k: the first load's row
+    uint32_t step;  // bytes from stage to stage
+    size_t origin;  // by rows: values before the tile's first row
     int wave;
 
     // XOR on the chunk index of LDS row `row`, so that what is read in one
@@ -116,12 +123,14 @@ struct StageLoader {
     {
         wave = wave_;
         origin = kKRows ? 0 : size_t(first) * m.ld;
+        step = 2 * kStageK * (kKRows ? m.ld : 1);
         row = wave * kLoads * kRowsPerLoad + lane / kChunks;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             if (kKRows) {
                 const uint32_t chunk = (lane % kChunks) ^ swizzle(row + j * kRowsPerLoad);
-                off[j] = min(first + chunk * 8, m.extent - 8) * 2;
+                off[j] = min(first + chunk * 8, m.extent - 8) * 2 +
+                         (kClamped ? 0 : __umul24(row + j * kRowsPerLoad, m.ld * 2));
             } else {
                 const uint32_t r = (wave * kLoads + j) * 16 + lane / 4;
                 const uint32_t chunk = (lane & 3) ^ swizzle(r);
@@ -131,26 +140,34 @@ struct StageLoader {
         }
     }
 
-    // Where the stage from k0 on of plane p starts, as a descriptor of `bytes`
-    // bytes: of none, its loads fetch nothing.
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage(const MatOperand& m, const uint16_t* p, uint32_t k0,
-                                                            uint32_t bytes) const
+    // The turn from k0 on of plane p.
+    __device__ __forceinline__ const uint16_t* turn(const MatOperand& m, const uint16_t* p, uint32_t k0) const
     {
-        // (by k: not past the last row)
-        const uint16_t* base = p + (kKRows ? size_t(min(k0, m.krows - 1)) * m.ld : origin + k0);
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, bytes, 0x00020000);
+        return p + (kKRows ? size_t(k0) * m.ld : origin + k0);
     }
 
-    // Enqueues load j of the stage into lds.
-    __device__ __forceinline__ void load(const MatOperand& m, __amdgpu_buffer_rsrc_t at, uint32_t k0, int j,
-                                         uint16_t* lds) const
+    // A descriptor of `bytes` bytes from p on: of none, its loads fetch nothing.
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const uint16_t* p, uint32_t bytes)
     {
-        // by k: the last row of the stage that may be read; rows of a stage
-        // and the bytes of a row fit 24 bits
-        const uint32_t last = m.krows - 1 - min(k0, m.krows - 1);
-        const uint32_t o = kKRows ? __umul24(min(row + j * kRowsPerLoad, last), m.ld * 2) + off[j] : off[j];
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            at, (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + j) * 512), 16, o, 0, 0, 0);
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, bytes, 0x00020000);
+    }
+
+    // Enqueues load j of stage s of the turn from k0 on, which starts at p (and
+    // in `at`), into lds.
+    __device__ __forceinline__ void load(const MatOperand& m, const uint16_t* p, uint32_t bytes,
+                                         __amdgpu_buffer_rsrc_t at, uint32_t k0, int s, int j, uint16_t* lds) const
+    {
+        const auto to = (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + j) * 512);
+        if (kClamped) {
+            // not past the last row that may be read; rows of a stage and the
+            // bytes of a row fit 24 bits
+            const uint32_t k = k0 + s * kStageK, first = min(k, m.krows - 1), last = m.krows - 1 - first;
+            const uint32_t o = __umul24(min(row + j * kRowsPerLoad, last), m.ld * 2) + off[j];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(view(p + size_t(first - k0) * m.ld, bytes), to, 16, o, 0, 0, 0);
+        } else {
+            // (an offset in the instruction itself would move the place in LDS too)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(at, to, 16, off[j], s * step, 0, 0);
+        }
     }
 };
 
@@ -206,13 +223,14 @@ struct TileBuffers {
     const TileBuffers name = {{name##_a0, name##_a1, name##_a2, name##_a3},                                  \
                               {name##_b0, name##_b1, name##_b2, name##_b3}}
 
-// kF16: fp16 operands, else bf16.
-template <bool kF16, bool kAK, bool kBK, int TA, int TB, int WA, int WB>
+// kF16: fp16 operands, else bf16. kPlain: as of StageLoader, and planes that add
+// up as they are: no sum of segments is scaled.
+template <bool kF16, bool kAK, bool kBK, int TA, int TB, int WA, int WB, bool kPlain = false>
 struct TileProduct {
     static constexpr int kWaves = WA * WB;
     static constexpr int RA = TA / WA / 32, RB = TB / WB / 32;  // 32 x 32 products of a wave
-    using LoadA = StageLoader<kAK, TA, kWaves>;
-    using LoadB = StageLoader<kBK, TB, kWaves>;
+    using LoadA = StageLoader<kAK, TA, kWaves, kPlain>;
+    using LoadB = StageLoader<kBK, TB, kWaves, kPlain>;
 
     struct Acc {
         f32x16 v[RA][RB];
@@ -243,43 +261,49 @@ struct TileProduct {
         if (t0 >= t1)
             return;
 
-        // the stage that is fetched next: its place in the planes, and how
-        // many are left
+        // the turn that is fetched next: its place in the planes, and how many
+        // are left. Set once a turn: scalar instructions of every stage are
+        // what all waves go through behind its barrier before their first
+        // product.
         const uint32_t k_end = sh.turns * kTurnK;
-        uint32_t seg = t0 / sh.turns, k0 = (t0 - seg * sh.turns) * kTurnK, left = (t1 - t0) * kBuffers;
+        uint32_t seg = t0 / sh.turns, k0 = (t0 - seg * sh.turns) * kTurnK, left = t1 - t0;
         struct Fetch {
             __amdgpu_buffer_rsrc_t a, b;
-            uint32_t k0;
+            const uint16_t *pa, *pb;
+            uint32_t k0, bytes;
         };
-        const auto next_stage = [&]() {
-            const uint32_t pa = (sh.pair_a >> (2 * seg)) & 3, pb = (sh.pair_b >> (2 * seg)) & 3;
+        const auto next_turn = [&]() {
+            const uint32_t i = (sh.pair_a >> (2 * seg)) & 3, j = (sh.pair_b >> (2 * seg)) & 3;
+            Fetch f;
+            f.pa = ga.turn(A, A.plane0 + i * A.plane_stride, k0);
+            f.pb = gb.turn(B, B.plane0 + j * B.plane_stride, k0);
             // (readfirstlane keeps what the compiler would select in vector
             // registers in scalar ones)
-            const uint32_t bytes = __builtin_amdgcn_readfirstlane(left ? 0xFFFFFFFFu : 0u);
-            const Fetch f = {ga.stage(A, A.plane0 + pa * A.plane_stride, k0, bytes),
-                             gb.stage(B, B.plane0 + pb * B.plane_stride, k0, bytes), k0};
-            left -= bytes & 1;
-            k0 += kStageK;
+            f.bytes = __builtin_amdgcn_readfirstlane(left ? 0xFFFFFFFFu : 0u);
+            f.k0 = k0;
+            f.a = LoadA::view(f.pa, f.bytes);
+            f.b = LoadB::view(f.pb, f.bytes);
+            left -= f.bytes & 1;
+            k0 += kTurnK;
             const uint32_t over = __builtin_amdgcn_readfirstlane(k0 == k_end ? 1u : 0u);
             seg += over;
             k0 -= over * k_end;
             return f;
         };
         constexpr int kLoads = LoadA::kLoads + LoadB::kLoads;
-        const auto load = [&](const Fetch& f, int j, int buffer) {
+        const auto load = [&](const Fetch& f, int s, int j) {
             if (j < LoadA::kLoads)
-                ga.load(A, f.a, f.k0, j, lds.a[buffer]);
+                ga.load(A, f.pa, f.bytes, f.a, f.k0, s, j, lds.a[s]);
             else if (j < kLoads)
-                gb.load(B, f.b, f.k0, j - LoadA::kLoads, lds.b[buffer]);
+                gb.load(B, f.pb, f.bytes, f.b, f.k0, s, j - LoadA::kLoads, lds.b[s]);
         };
 
+        Fetch f = next_turn();
 #pragma unroll
-        for (int s = 0; s < kBuffers - 1; ++s) {
-            const Fetch f = next_stage();
+        for (int s = 0; s < kBuffers - 1; ++s)
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
-                load(f, j, s);
-        }
+                load(f, s, j);
         wait_loads<2 * kLoads>();
         s16x8 a[2][RA], b[2][RB];
 #pragma unroll
@@ -291,14 +315,13 @@ struct TileProduct {
 
         const uint32_t fold = sh.fold * sh.turns;
         for (uint32_t t = t0; t < t1; ++t) {
-            if (t == fold && t > t0)
+            if (!kPlain && t == fold && t > t0)
                 scale(acc);
 #pragma unroll
             for (int s = 0; s < kBuffers; ++s) {
                 // behind the barrier stage s + 1 is in LDS for everybody, and
                 // nobody reads the buffer of s - 1 any more, which s + 3 takes
                 wait_loads<kLoads>();
-                const Fetch f = next_stage();
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     const int from = kk == 0 ? s : (s + 1) % kBuffers;
@@ -313,7 +336,7 @@ struct TileProduct {
                         constexpr int kSteps = 2 * (RA > RB ? RA : RB), kEach = (kLoads + kSteps - 1) / kSteps;
 #pragma unroll
                         for (int e = 0; e < kEach; ++e)
-                            load(f, (kk * (RA > RB ? RA : RB) + i) * kEach + e, (s + kBuffers - 1) % kBuffers);
+                            load(f, (s + kBuffers - 1) % kBuffers, (kk * (RA > RB ? RA : RB) + i) * kEach + e);
                         if (i < RA) {
 #pragma unroll
                             for (int j = 0; j < RB; ++j)
@@ -322,9 +345,12 @@ struct TileProduct {
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
+                // the stages behind the last one of this turn are the next one's
+                if (s == 0)
+                    f = next_turn();
             }
         }
-        if (t1 <= fold)
+        if (!kPlain && t1 <= fold)
             scale(acc);
         wait_loads<0>();
     }

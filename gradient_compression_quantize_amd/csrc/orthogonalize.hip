@@ -12,8 +12,8 @@
 // scaled update, or the new weights). A tall matrix is never transposed: its
 // products read it by k (mfma_product.h).
 //
-// Precision. X is carried to 22 bits, as two planes of fp16; A and P are held
-// in one plane or two. The operands of the products are the first planes alone
+// Precision. X is carried to 22 bits, as two planes of fp16 that add up to it; A
+// and P are held in one plane or two. The operands of the products are the first planes alone
 // (off by at most 2^-11 of a value) where the result is kept in bf16, else both
 // (three products each). a X never loses what the operands round away: its
 // roundings would grow with the small singular values, 3.4 times a step, up to
@@ -24,9 +24,10 @@
 //   (a X + P X)_i = (a + P_ii) X_i + (what is off the diagonal of P) X
 // with O = A off its diagonal: rounded to 11 bits, they would scale whole rows. Of
 // 64 x 576 the result of one plane is then 5e-4 off 64 bits instead of 2e-3.
-// X is held times 2^12, A times 2^12, P times 2^10: entries are at most a singular
-// value (s, s^2, ..) in size, and the first ones, of a matrix of 4096 x 4096, near
-// 2^-12 and 2^-18.
+// X is held times 2^14, A times 2^12, P times 2^10: entries are at most a singular
+// value (s, s^2, ..) in size, and the first ones of X, of 4096 x 4096, near 2^-12.
+// Second planes end at 2^-39 in X, at 2^-37 in A and 2^-35 in P, where they only
+// are factors of something below 1 next to a X.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -37,8 +38,7 @@
 namespace gcq {
 namespace {
 
-constexpr int kXExp = 12, kAExp = 12, kPExp = 10;
-constexpr float kXScale = 4096.0f;
+constexpr int kXExp = 14, kAExp = 12, kPExp = 10;
 
 // 2^e
 constexpr float pow2(int e)
@@ -141,8 +141,9 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(PtrTable<T> x, PtrTable<
         zero[i] = u32x4{0, 0, 0, 0};
 }
 
-// Eight values as two planes: x = p0 + 2^-11 p1 to 2^-22 of it.
+// Eight values as two planes: x = p0 + p1 to 2^-22 of it.
 typedef vec_of<float, 8> f32x8;
+typedef vec_of<f16_t, 4> f16x4;
 
 struct Planes8 {
     f16x8 p0, p1;
@@ -152,18 +153,13 @@ __device__ __forceinline__ Planes8 split8(f32x8 v)
 {
     Planes8 s;
     s.p0 = __builtin_convertvector(v, f16x8);
-    s.p1 = __builtin_convertvector((v - __builtin_convertvector(s.p0, f32x8)) * 0x1p11f, f16x8);
+    s.p1 = __builtin_convertvector(v - __builtin_convertvector(s.p0, f32x8), f16x8);
     return s;
 }
 
 __device__ __forceinline__ f32x8 join8(Planes8 s)
 {
-    const f32x8 lo = __builtin_convertvector(s.p1, f32x8);
-    f32x8 v = __builtin_convertvector(s.p0, f32x8);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] = __builtin_fmaf(lo[e], 0x1p-11f, v[e]);
-    return v;
+    return __builtin_convertvector(s.p0, f32x8) + __builtin_convertvector(s.p1, f32x8);
 }
 
 __device__ __forceinline__ f16x8 load_plane(const uint16_t* p) { return *reinterpret_cast<const f16x8*>(p); }
@@ -193,7 +189,7 @@ __global__ __launch_bounds__(kThreads) void first_kernel(PtrTable<T> x, PtrTable
     for (uint32_t i = threadIdx.x; i < nparts; i += kThreads)
         sum += parts[k * nparts + i];
     sum = workgroup_sum(sum);
-    const double factor = double(kXScale) / (sqrt(sum) + double(eps));
+    const double factor = double(pow2(kXExp)) / (sqrt(sum) + double(eps));
     const uint32_t chunks = to.ld / 8;
     const size_t total = size_t(to.rows) * chunks;
     for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < total; i += size_t(gridDim.x) * kThreads) {
@@ -243,46 +239,52 @@ struct Waves {
     static constexpr int a = 2, b = T == 256 ? 4 : 2, threads = a * b * kWave;
 };
 
-// A wave's part of a tile as rows: 32 rows of b at a time go through the wave's
-// own part of the LDS that the product has left, fp32, as an image of 32 rows of
-// kCols values in 16-byte chunks that an XOR of the row spreads over the banks.
-// A lane then holds 8 values of a row, so that what is loaded and stored beside
-// them is 16 bytes a lane and whole rows of the part: as the matrix cores leave
-// them, 4 values of 32 rows each, the update of 4096 x 4096 took 221 us instead
-// of XXX.
+// What a wave's products leave through: its part of the tile, 32 rows of b at a
+// time, turned in the LDS that the product has left, so that a lane loads and
+// stores 16 bytes of a row and a wave whole rows of its part. As the matrix cores
+// leave them, 4 values of 32 rows each, the update of 4096 x 4096 took 221 us
+// instead of 141.
 template <int T>
-struct PartRows {
+struct Part {
     using W = Waves<T>;
     static constexpr int kCols = T / W::a, kRowsB = T / W::b;  // of a wave
-    static constexpr int kChunks = kCols / 4;
-    static constexpr int kLanes = kCols / 8, kStep = kWave / kLanes, kPasses = 32 / kStep;
-    // (an address of LDS throughout: as a generic one the choice of the buffer
+    // (addresses of LDS throughout: as a generic one the choice of the buffer
     // would become a table, and LDS has no addresses to put there)
-    typedef __attribute__((address_space(3))) float lds_f32;
-    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
-    lds_f32* image;
+    typedef __attribute__((address_space(3))) uint16_t lds_u16;
+    lds_u16* buffer;
     uint32_t a, b;  // where the wave's part starts
     int lane;
 
-    __device__ __forceinline__ PartRows(const TileBuffers& lds, uint32_t a_first, uint32_t b_first)
+    __device__ __forceinline__ Part(const TileBuffers& lds, uint32_t a_first, uint32_t b_first)
     {
-        static_assert(32 * kCols * 4 <= T * kStageK * 2, "an image fits a buffer");
         static_assert(W::a * W::b <= 2 * kBuffers, "a buffer for each wave");
+        static_assert(32 * kCols * 4 <= T * kStageK * 2, "32 rows of 4 bytes a value fit a buffer");
         lane = threadIdx.x & (kWave - 1);
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-        image = (lds_f32*)lds.a[0];
+        buffer = (lds_u16*)lds.a[0];
 #pragma unroll
         for (int k = 1; k < W::a * W::b; ++k) {
-            lds_f32* const p = (lds_f32*)(k < kBuffers ? lds.a[k % kBuffers] : lds.b[k % kBuffers]);
-            image = wave == k ? p : image;
+            lds_u16* const p = (lds_u16*)(k < kBuffers ? lds.a[k % kBuffers] : lds.b[k % kBuffers]);
+            buffer = wave == k ? p : buffer;
         }
         a = a_first + wave % W::a * kCols;
         b = b_first + wave / W::a * kRowsB;
     }
+};
 
-    __device__ __forceinline__ lds_f32* chunk(int row, int c) const
+// The part as fp32, to be combined with what a lane loads beside it: 16-byte
+// chunks that an XOR of the row spreads over the banks.
+template <int T>
+struct PartRows : Part<T> {
+    using Part<T>::kCols, Part<T>::buffer, Part<T>::lane;
+    static constexpr int kChunks = kCols / 4;
+    static constexpr int kLanes = kCols / 8, kStep = kWave / kLanes, kPasses = 32 / kStep;
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+    using Part<T>::Part;
+
+    __device__ __forceinline__ lds_f32x4* chunk(int row, int c) const
     {
-        return image + row * kCols + ((c ^ (row & (kChunks - 1))) << 2);
+        return (lds_f32x4*)(buffer + 2 * row * kCols + ((c ^ (row & (kChunks - 1))) << 3));
     }
 
     // Products [i][j] of all i into the image.
@@ -298,7 +300,7 @@ struct PartRows {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     v[e] = acc.v[i][j][4 * q + e];
-                *(lds_f32x4*)chunk(row, i * 8 + 2 * q + (lane >> 5)) = v;
+                *chunk(row, i * 8 + 2 * q + (lane >> 5)) = v;
             }
         wave_lds_sync();
     }
@@ -309,32 +311,147 @@ struct PartRows {
 
     __device__ __forceinline__ f32x8 get(int pass) const
     {
-        const int c = col() / 4;
         f32x8 v;
-        v.lo = *(const lds_f32x4*)chunk(row(pass), c);
-        v.hi = *(const lds_f32x4*)chunk(row(pass), c + 1);
+        v.lo = *chunk(row(pass), col() / 4);
+        v.hi = *chunk(row(pass), col() / 4 + 1);
         return v;
     }
+};
 
-    __device__ __forceinline__ void put(int pass, f32x8 v) const
+// The part as fp16, one plane or two one behind the other, made in the layout of
+// the matrix cores: rows of it are then only copied, and those of its transpose
+// come out of the transposing load (mfma_product.h).
+template <int T>
+struct PartPlanes : Part<T> {
+    using Part<T>::kCols, Part<T>::buffer, Part<T>::lane;
+    static constexpr int kChunks = kCols / 8, kPlane = 32 * kCols;  // chunks of 16 bytes a row
+    static constexpr int kStep = kWave / kChunks, kPasses = 32 / kStep;
+    typedef __attribute__((address_space(3))) f16x8 lds_f16x8;
+    typedef __attribute__((address_space(3))) f16x4 lds_f16x4;
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    using Part<T>::Part;
+
+    __device__ __forceinline__ typename Part<T>::lds_u16* at(int plane, int row, int col) const
     {
-        const int c = col() / 4;
-        *(lds_f32x4*)chunk(row(pass), c) = v.lo;
-        *(lds_f32x4*)chunk(row(pass), c + 1) = v.hi;
+        return buffer + plane * kPlane + row * kCols + (((col >> 3) ^ (row & (kChunks - 1))) << 3) + (col & 7);
     }
 
-    // The image's transpose: 8 rows of b from 8 (lane % 4) on, of one column, 16
-    // columns a pass.
-    static constexpr int kTurnedPasses = kCols / 16;
-    __device__ __forceinline__ int turned_col(int pass) const { return pass * 16 + lane / 4; }
-    __device__ __forceinline__ f32x8 get_turned(int pass) const
+    // The 32 rows of a matrix of `rows` x `cols` from row b0 on into the image.
+    __device__ __forceinline__ void bring(const uint16_t* plane0, size_t plane_stride, uint32_t ld, int planes,
+                                          uint32_t b0, uint32_t rows, uint32_t cols) const
     {
-        const int c = turned_col(pass), first = lane % 4 * 8;
-        f32x8 v;
+        const uint32_t a = this->a + col();
+        for (int plane = 0; plane < planes; ++plane) {
+            const uint16_t* from = plane0 + plane * plane_stride + a;
+            f16x8 v[kPasses];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = chunk(first + e, c >> 2)[c & 3];
-        return v;
+            for (int p = 0; p < kPasses; ++p) {
+                v[p] = f16x8{};
+                if (a < cols && b0 + row(p) < rows)
+                    v[p] = load_plane(from + size_t(b0 + row(p)) * ld);
+            }
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p)
+                *eight(plane, p) = v[p];
+        }
+        wave_lds_sync();
+    }
+
+    // The image into those rows.
+    __device__ __forceinline__ void leave(uint16_t* plane0, size_t plane_stride, uint32_t ld, int planes, uint32_t b0,
+                                          uint32_t rows, uint32_t cols) const
+    {
+        const uint32_t a = this->a + col();
+        for (int plane = 0; plane < planes; ++plane) {
+            uint16_t* to = plane0 + plane * plane_stride + a;
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) {
+                const f16x8 v = *eight(plane, p);
+                if (a < cols && b0 + row(p) < rows)
+                    store_plane(to + size_t(b0 + row(p)) * ld, v);
+            }
+        }
+    }
+
+    // The four values that the matrix cores leave this lane in [i][.], q.
+    __device__ __forceinline__ lds_f16x4* quad(int plane, int i, int q) const
+    {
+        return (lds_f16x4*)at(plane, int(acc_col(lane)), i * 32 + 8 * q + 4 * (lane >> 5));
+    }
+
+    // Those of all q: out of the image, and into it.
+    __device__ __forceinline__ void read(f32x4 (&v)[4], int i, bool both) const
+    {
+        f16x4 p0[4], p1[4] = {};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            p0[q] = *quad(0, i, q);
+            if (both)
+                p1[q] = *quad(1, i, q);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            v[q] = __builtin_convertvector(p0[q], f32x4) + __builtin_convertvector(p1[q], f32x4);
+    }
+
+    __device__ __forceinline__ void write(const f32x4 (&v)[4], int i, bool both) const
+    {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const f16x4 p0 = __builtin_convertvector(v[q], f16x4);
+            *quad(0, i, q) = p0;
+            if (both)
+                *quad(1, i, q) = __builtin_convertvector(v[q] - __builtin_convertvector(p0, f32x4), f16x4);
+        }
+    }
+
+    // Row and column of this lane's eight values in a pass over the rows.
+    __device__ __forceinline__ int row(int pass) const { return pass * kStep + lane / kChunks; }
+    __device__ __forceinline__ int col() const { return lane % kChunks * 8; }
+    __device__ __forceinline__ lds_f16x8* eight(int plane, int pass) const
+    {
+        return (lds_f16x8*)at(plane, row(pass), col());
+    }
+
+    // Of the transpose: column turned_col(), rows turned_row() .. + 7.
+    static constexpr int kTurnedPasses = kCols / 16;
+    __device__ __forceinline__ int turned_col(int pass) const { return pass * 16 + (lane & 15); }
+    __device__ __forceinline__ int turned_row() const { return lane / 16 * 8; }
+    __device__ __forceinline__ f16x8 turned(int plane, int pass) const
+    {
+        const int r = turned_row() + (lane >> 2 & 3), c = pass * 16 + 4 * (lane & 3);
+        union {
+            s16x4 h[2];
+            f16x8 v;
+        } u;
+        u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at(plane, r, c));
+        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at(plane, r + 4, c));
+        return u.v;
+    }
+};
+
+// A value for each column of a wave's part (0 behind the last), in LDS.
+template <int T>
+struct Columns {
+    static constexpr int kCols = T / Waves<T>::a, kAll = Waves<T>::a * Waves<T>::b * kCols;
+    typedef __attribute__((address_space(3))) float lds_f32;
+    typedef __attribute__((address_space(3))) const f32x4 lds_f32x4;
+    lds_f32* own;
+    int lane;
+
+    __device__ __forceinline__ Columns(float (&lds)[kAll], const float* p, uint32_t a, uint32_t cols)
+    {
+        lane = threadIdx.x & (kWave - 1);
+        own = (lds_f32*)lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * kCols;
+        for (int c = lane; c < kCols; c += kWave)
+            own[c] = a + c < cols ? p[a + c] : 0.0f;
+        wave_lds_sync();
+    }
+
+    // At the columns of the products that the matrix cores leave this lane.
+    __device__ __forceinline__ f32x4 quad(int i, int q) const
+    {
+        return *(lds_f32x4*)(own + i * 32 + 8 * q + 4 * (lane >> 5));
     }
 };
 
@@ -354,7 +471,7 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
                                                                          ProductShape sh, Tiles tiles, SymmetricOut out)
 {
     constexpr int WA = Waves<T>::a, WB = Waves<T>::b;
-    using P = TileProduct<true, kKRows, kKRows, T, T, WA, WB>;
+    using P = TileProduct<true, kKRows, kKRows, T, T, WA, WB, true>;
     GCQ_TILE_BUFFERS(lds, T, T);
     const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), matrix = id / tiles.per_matrix;
     uint32_t ta, tb;
@@ -363,84 +480,70 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
     typename P::Acc acc;
     P::run(V, V, sh, ta * T, tb * T, 0, sh.turns * sh.segments, lds, acc);
 
-    const PartRows<T> part(lds, ta * T, tb * T);
+    using Rows = PartPlanes<T>;
+    const Rows part(lds, ta * T, tb * T);
     uint16_t* to = held_at(out.to, matrix, 0);
-    float* diagonal = out.diagonal + size_t(matrix) * out.to.rows;
-    const float* old = kSquare ? out.from_diagonal + size_t(matrix) * out.to.rows : nullptr;
-    const uint32_t side = out.to.rows, a = part.a + part.col();
-    const bool in_a = a < side;
-    f32x8 da = {};
-    if (kSquare && in_a)
-        da = *reinterpret_cast<const f32x8*>(old + a);
+    const uint32_t side = out.to.rows;
+    float* diagonal = out.diagonal + size_t(matrix) * side;
+    const float* old = kSquare ? out.from_diagonal + size_t(matrix) * side : nullptr;
+    const int planes = out.both ? 2 : 1;
+    __shared__ float of_columns[Columns<T>::kAll];
+    const Columns<T> of_col(of_columns, old, part.a, kSquare ? side : 0);  // A's diagonal
 #pragma unroll
     for (int j = 0; j < P::RB; ++j) {
-        Planes8 A[PartRows<T>::kPasses];
-        float db[PartRows<T>::kPasses];
-        if (kSquare) {
+        const uint32_t b0 = part.b + j * 32, b = b0 + acc_col(part.lane);
+        if (kSquare)  // A's part of V
+            part.bring(V.plane0, V.plane_stride, V.ld, planes, b0, side, side);
+        const float db = kSquare && b < side ? old[b] : 0.0f;
 #pragma unroll
-            for (int p = 0; p < PartRows<T>::kPasses; ++p) {
-                const uint32_t b = part.b + j * 32 + part.row(p);
-                A[p] = Planes8{};
-                db[p] = 0.0f;
-                if (in_a && b < side) {
-                    const uint16_t* from = V.plane0 + size_t(b) * V.ld + a;
-                    A[p].p0 = load_plane(from);
-                    if (out.both)
-                        A[p].p1 = load_plane(from + V.plane_stride);
-                    db[p] = old[b];
-                }
-            }
-        }
-        part.fill(acc, j);
+        for (int i = 0; i < P::RA; ++i) {
+            f32x4 v[4];
 #pragma unroll
-        for (int p = 0; p < PartRows<T>::kPasses; ++p) {
-            const uint32_t b = part.b + j * 32 + part.row(p);
-            f32x8 v = part.get(p);
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[q][e] = acc.v[i][j][4 * q + e] * (kSquare ? out.c * pow2(kPExp - 2 * kAExp) : pow2(kAExp - 2 * kXExp));
             if (kSquare) {
-                const f32x8 x = join8(A[p]);
+                const float own = (out.b + out.c * db) * pow2(kPExp - kAExp), each = out.c * pow2(kPExp - kAExp);
+                f32x4 A[4];
+                part.read(A, i, out.both);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // (on the diagonal A is 0 in the planes)
-                    const float own = a + e == b ? (out.b + out.c * db[p]) * db[p] * pow2(kPExp) : 0.0f;
-                    const float times = (out.b + out.c * (da[e] + db[p])) * pow2(kPExp - kAExp);
-                    v[e] = __builtin_fmaf(v[e], out.c * pow2(kPExp - 2 * kAExp), __builtin_fmaf(x[e], times, own));
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 da = of_col.quad(i, q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[q][e] = __builtin_fmaf(A[q][e], __builtin_fmaf(each, da[e], own), v[q][e]);
                 }
-            } else {
-                v *= pow2(kAExp - 2 * kXExp);
             }
             if (ta == tb) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (a + e == b && b < side) {
-                        diagonal[b] = v[e] * pow2(kSquare ? -kPExp : -kAExp);
-                        v[e] = 0.0f;
-                    }
-            } else {
-                part.put(p, v);
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (part.a + i * 32 + acc_row(4 * q + e, part.lane) == b && b < side) {
+                            // (A is 0 there in the planes)
+                            const float more = kSquare ? (out.b + out.c * db) * db : 0.0f;
+                            diagonal[b] = __builtin_fmaf(v[q][e], pow2(kSquare ? -kPExp : -kAExp), more);
+                            v[q][e] = 0.0f;
+                        }
             }
-            if (in_a && b < side) {
-                const Planes8 s = split8(v);
-                uint16_t* o = to + size_t(b) * out.to.ld + a;
-                store_plane(o, s.p0);
-                if (out.both)
-                    store_plane(o + out.to.plane_stride, s.p1);
+            part.write(v, i, out.both);
+        }
+        wave_lds_sync();
+        part.leave(to, out.to.plane_stride, out.to.ld, planes, b0, side, side);
+        if (ta != tb) {
+            for (int plane = 0; plane < planes; ++plane) {
+                uint16_t* p = to + plane * out.to.plane_stride + b0 + part.turned_row();
+#pragma unroll
+                for (int k = 0; k < Rows::kTurnedPasses; ++k) {
+                    const uint32_t row = part.a + part.turned_col(k);
+                    const f16x8 v = part.turned(plane, k);
+                    if (row < side && b0 + part.turned_row() < side)
+                        store_plane(p + size_t(row) * out.to.ld, v);
+                }
             }
         }
         wave_lds_sync();
-        if (ta != tb) {
-#pragma unroll
-            for (int p = 0; p < PartRows<T>::kTurnedPasses; ++p) {
-                const uint32_t row = part.a + part.turned_col(p), col = part.b + j * 32 + part.lane % 4 * 8;
-                const Planes8 s = split8(part.get_turned(p));
-                if (row < side && col < side) {
-                    uint16_t* o = to + size_t(row) * out.to.ld + col;
-                    store_plane(o, s.p0);
-                    if (out.both)
-                        store_plane(o + out.to.plane_stride, s.p1);
-                }
-            }
-            wave_lds_sync();
-        }
     }
 }
 
@@ -516,7 +619,7 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
                                                                       UpdateOut out, LastOut last)
 {
     constexpr int WA = Waves<T>::a, WB = Waves<T>::b;
-    using P = TileProduct<true, !kTall, false, T, T, WA, WB>;
+    using P = TileProduct<true, !kTall, false, T, T, WA, WB, true>;
     GCQ_TILE_BUFFERS(lds, T, T);
     const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), matrix = id / tiles.per_matrix;
     uint32_t ta, tb;
@@ -526,63 +629,62 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
     typename P::Acc acc;
     P::run(A, B, sh, ta * T, tb * T, 0, sh.turns * sh.segments, lds, acc);
 
-    const PartRows<T> part(lds, ta * T, tb * T);
+    const PartPlanes<T> part(lds, ta * T, tb * T);
     const uint16_t* from = held_at(out.from, matrix, 0);
-    uint16_t* to = kLast ? nullptr : held_at(out.to, matrix, 0);
-    float keep = 1.0f, factor = last.scale * (1.0f / kXScale);
+    const float* diagonal = out.diagonal + size_t(matrix) * out.side;
+    const uint32_t rows = out.from.rows, cols = out.from.ld;
+    __shared__ float of_columns[Columns<T>::kAll];
+    const Columns<T> of_col(of_columns, diagonal, part.a, kTall ? cols : 0);
+    const PartRows<T> whole(lds, ta * T, tb * T);
+    float keep = 1.0f, factor = last.scale * pow2(-kXExp);
     if (kLast && last.update) {
         const float lr = last.lr_scale ? last.lr * *last.lr_scale : last.lr;
         keep = __builtin_fmaf(-lr, last.decay, 1.0f);
-        factor = lr * last.scale * (1.0f / kXScale);
+        factor = lr * last.scale * pow2(-kXExp);
     }
-    const float* diagonal = out.diagonal + size_t(matrix) * out.side;
-    const uint32_t rows = kLast ? last.m : out.from.rows, cols = kLast ? last.n : out.from.ld;
-    const uint32_t a = part.a + part.col();
-    const bool in_a = a < cols;
-    f32x8 of_col = {};
-    if (kTall && in_a)
-        of_col = *reinterpret_cast<const f32x8*>(diagonal + a) + out.a;
 #pragma unroll
     for (int j = 0; j < P::RB; ++j) {
-        Planes8 X[PartRows<T>::kPasses];
-        float of_row[PartRows<T>::kPasses];
+        const uint32_t b0 = part.b + j * 32, b = b0 + acc_col(part.lane);
+        part.bring(from, out.from.plane_stride, cols, 2, b0, rows, cols);
+        const float of_row = out.a + (!kTall && b < rows ? diagonal[b] : 0.0f);
 #pragma unroll
-        for (int p = 0; p < PartRows<T>::kPasses; ++p) {
-            const uint32_t b = part.b + j * 32 + part.row(p);
-            X[p] = Planes8{};
-            of_row[p] = 0.0f;
-            if (in_a && b < rows) {
-                const uint16_t* at = from + size_t(b) * out.from.ld + a;
-                X[p].p0 = load_plane(at);
-                X[p].p1 = load_plane(at + out.from.plane_stride);
-                of_row[p] = kTall ? 0.0f : diagonal[b];
+        for (int i = 0; i < P::RA; ++i) {
+            f32x4 v[4];
+            part.read(v, i, true);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x4 of_cols = kTall ? of_col.quad(i, q) : f32x4{};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float self = kTall ? of_cols[e] + out.a : of_row;
+                    v[q][e] = __builtin_fmaf(v[q][e], self, acc.v[i][j][4 * q + e] * pow2(-kPExp));
+                    if (kLast)
+                        acc.v[i][j][4 * q + e] = v[q][e];
+                }
             }
+            if (!kLast)
+                part.write(v, i, true);
         }
-        part.fill(acc, j);
+        wave_lds_sync();
+        if (!kLast) {
+            part.leave(held_at(out.to, matrix, 0), out.to.plane_stride, cols, 2, b0, rows, cols);
+            wave_lds_sync();
+            continue;
+        }
+        whole.fill(acc, j);
+        const uint32_t a = whole.a + whole.col();
 #pragma unroll
         for (int p = 0; p < PartRows<T>::kPasses; ++p) {
-            const uint32_t b = part.b + j * 32 + part.row(p);
-            const f32x8 x = join8(X[p]);
-            f32x8 v = part.get(p);
-            const float self = out.a + of_row[p];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = __builtin_fmaf(x[e], kTall ? of_col[e] : self, v[e] * pow2(-kPExp));
-            if (!in_a || b >= rows)
+            const uint32_t row = b0 + whole.row(p);
+            const f32x8 v = whole.get(p);
+            if (a >= last.n || row >= last.m)
                 continue;
-            if (kLast) {
-                if (last.dtype == GC_F32)
-                    write_last<float>(last, matrix, b, a, v, keep, factor);
-                else if (last.dtype == GC_BF16)
-                    write_last<bf16_t>(last, matrix, b, a, v, keep, factor);
-                else
-                    write_last<f16_t>(last, matrix, b, a, v, keep, factor);
-            } else {
-                const Planes8 s = split8(v);
-                uint16_t* o = to + size_t(b) * out.to.ld + a;
-                store_plane(o, s.p0);
-                store_plane(o + out.to.plane_stride, s.p1);
-            }
+            if (last.dtype == GC_F32)
+                write_last<float>(last, matrix, row, a, v, keep, factor);
+            else if (last.dtype == GC_BF16)
+                write_last<bf16_t>(last, matrix, row, a, v, keep, factor);
+            else
+                write_last<f16_t>(last, matrix, row, a, v, keep, factor);
         }
         wave_lds_sync();
     }
