@@ -40,16 +40,14 @@ namespace {
 
 constexpr int kXExp = 14, kAExp = 12, kPExp = 10;
 
-// 2^e
-constexpr float pow2(int e)
+constexpr float power_of_two(int e)
 {
-    float r = 1.0f;
-    for (; e > 0; --e)
-        r *= 2.0f;
-    for (; e < 0; ++e)
-        r *= 0.5f;
-    return r;
+    return e == 0 ? 1.0f : e > 0 ? 2.0f * power_of_two(e - 1) : 0.5f * power_of_two(e + 1);
 }
+
+// 2^kExp: as a constant (a call with constant arguments stays a call).
+template <int kExp>
+constexpr float pow2 = power_of_two(kExp);
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -120,13 +118,22 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(PtrTable<T> x, PtrTable<
         vec_of<float, 8> v = load8(src, i, values);
         if (kMomentum) {
             const vec_of<float, 8> old = load8(momenta.p[k], i, values);
-            float* to = const_cast<float*>(new_momenta.p[k]) + i;
+            vec_of<float, 8> now;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float g = v[e] * mo.grad_scale, m = mix(g, old[e], mo.beta);
-                if (i + e < values)
-                    to[e] = m;
-                v[e] = mo.nesterov ? mix(g, m, mo.beta) : m;
+                const float g = v[e] * mo.grad_scale;
+                now[e] = mix(g, old[e], mo.beta);
+                v[e] = mo.nesterov ? mix(g, now[e], mo.beta) : now[e];
+            }
+            float* to = const_cast<float*>(new_momenta.p[k]) + i;
+            typedef vec_of<float, 8> VecAny __attribute__((aligned(4)));
+            if (i + 8 <= values) {
+                *reinterpret_cast<VecAny*>(to) = now;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (i + e < values)
+                        to[e] = now[e];
             }
         }
 #pragma unroll
@@ -189,7 +196,7 @@ __global__ __launch_bounds__(kThreads) void first_kernel(PtrTable<T> x, PtrTable
     for (uint32_t i = threadIdx.x; i < nparts; i += kThreads)
         sum += parts[k * nparts + i];
     sum = workgroup_sum(sum);
-    const double factor = double(pow2(kXExp)) / (sqrt(sum) + double(eps));
+    const double factor = double(pow2<kXExp>) / (sqrt(sum) + double(eps));
     const uint32_t chunks = to.ld / 8;
     const size_t total = size_t(to.rows) * chunks;
     for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < total; i += size_t(gridDim.x) * kThreads) {
@@ -502,9 +509,9 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
             for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    v[q][e] = acc.v[i][j][4 * q + e] * (kSquare ? out.c * pow2(kPExp - 2 * kAExp) : pow2(kAExp - 2 * kXExp));
+                    v[q][e] = acc.v[i][j][4 * q + e] * (kSquare ? out.c * pow2<kPExp - 2 * kAExp> : pow2<kAExp - 2 * kXExp>);
             if (kSquare) {
-                const float own = (out.b + out.c * db) * pow2(kPExp - kAExp), each = out.c * pow2(kPExp - kAExp);
+                const float own = (out.b + out.c * db) * pow2<kPExp - kAExp>, each = out.c * pow2<kPExp - kAExp>;
                 f32x4 A[4];
                 part.read(A, i, out.both);
 #pragma unroll
@@ -523,7 +530,7 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
                         if (part.a + i * 32 + acc_row(4 * q + e, part.lane) == b && b < side) {
                             // (A is 0 there in the planes)
                             const float more = kSquare ? (out.b + out.c * db) * db : 0.0f;
-                            diagonal[b] = __builtin_fmaf(v[q][e], pow2(kSquare ? -kPExp : -kAExp), more);
+                            diagonal[b] = __builtin_fmaf(v[q][e], pow2<kSquare ? -kPExp : -kAExp>, more);
                             v[q][e] = 0.0f;
                         }
             }
@@ -552,7 +559,7 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(Held A, Held P, bool bo
                                                          const float* __restrict__ from_diagonal,
                                                          float* __restrict__ diagonal, size_t diagonals)
 {
-    const float f = b * pow2(kPExp - kAExp);
+    const float f = b * pow2<kPExp - kAExp>;
     for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < diagonals; i += size_t(gridDim.x) * kThreads)
         diagonal[i] = b * from_diagonal[i];
     for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < chunks; i += size_t(gridDim.x) * kThreads) {
@@ -604,6 +611,14 @@ __device__ __forceinline__ void write_last(const LastOut& o, uint32_t matrix, si
             to[e] = T(w ? __builtin_fmaf(float(w[e]), keep, -x[e]) : x[e]);
 }
 
+}  // namespace
+}  // namespace gcq
+
+#include "orthogonalize_resident.h"
+
+namespace gcq {
+namespace {
+
 // out[b][a] = X[b][a] * a_coef + sum over k of A(a, k) B(b, k): of a wide X, A
 // is X by k and B is P; of a tall one, A is P and B is X. kLast: the last step.
 struct UpdateOut {
@@ -636,11 +651,11 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
     __shared__ float of_columns[Columns<T>::kAll];
     const Columns<T> of_col(of_columns, diagonal, part.a, kTall ? cols : 0);
     const PartRows<T> whole(lds, ta * T, tb * T);
-    float keep = 1.0f, factor = last.scale * pow2(-kXExp);
+    float keep = 1.0f, factor = last.scale * pow2<-kXExp>;
     if (kLast && last.update) {
         const float lr = last.lr_scale ? last.lr * *last.lr_scale : last.lr;
         keep = __builtin_fmaf(-lr, last.decay, 1.0f);
-        factor = lr * last.scale * pow2(-kXExp);
+        factor = lr * last.scale * pow2<-kXExp>;
     }
 #pragma unroll
     for (int j = 0; j < P::RB; ++j) {
@@ -657,7 +672,7 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float self = kTall ? of_cols[e] + out.a : of_row;
-                    v[q][e] = __builtin_fmaf(v[q][e], self, acc.v[i][j][4 * q + e] * pow2(-kPExp));
+                    v[q][e] = __builtin_fmaf(v[q][e], self, acc.v[i][j][4 * q + e] * pow2<-kPExp>);
                     if (kLast)
                         acc.v[i][j][4 * q + e] = v[q][e];
                 }
@@ -695,11 +710,10 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
 size_t round_up(size_t a, size_t b) { return ceil_div(a, b) * b; }
 
 constexpr size_t kMaxSide = size_t(1) << 20, kMaxSmallSide = size_t(1) << 15, kMaxTiles = size_t(1) << 22;
-constexpr int kMaxSteps = 64;
-
 struct Layout {
     size_t m, n, small;     // small: the side of A
     bool tall, both;        // both: products of both planes
+    bool resident;          // one workgroup a matrix, without a workspace
     Held x[2], A, P;        // their plane0: an offset into the workspace
     size_t parts, diagonals[2], zero, zeros, total;  // bytes; diagonals of A and P
     uint32_t nparts;
@@ -713,6 +727,9 @@ Layout layout_of(size_t count, size_t m, size_t n, bool both)
     L.tall = m > n;
     L.both = both;
     L.small = std::min(m, n);
+    L.resident = with_resident(L.small, std::max(m, n), both, [](auto, auto, auto) {});
+    if (L.resident)
+        return L;
     const size_t rows = round_up(m, kTurnK), cols = round_up(n, kTurnK), side = round_up(L.small, kTurnK);
     size_t used = 0;
     const auto take = [&](size_t bytes) {
@@ -911,6 +928,8 @@ int check_call(const Call& c, Layout& L)
         return refuse(c, "eps must not be negative");
     if (!aligned16(c.ws) || *c.ws_bytes < L.total)
         return refuse(c, "workspace too small or not 16-byte aligned");
+    if (L.resident)
+        return GC_OK;
     place(L.x[0], static_cast<char*>(c.ws));
     place(L.x[1], static_cast<char*>(c.ws));
     place(L.A, static_cast<char*>(c.ws));
@@ -930,19 +949,67 @@ bool take_pointers(PtrTable<T>& t, const void* const* p, size_t count, size_t by
     return true;
 }
 
+// What a call reads: matrices of `dtype`, or gradients and momenta.
+struct In {
+    PtrTable<void> x;
+    int dtype;
+    bool momentum;
+    PtrTable<float> momenta, new_momenta;
+    Momentum mo;
+};
+
+int run_resident(const Call& c, const Layout& L, const In& in, const LastOut& last, hipStream_t stream)
+{
+    ResidentIn r{};
+    r.x = in.x;
+    r.momenta = in.momenta;
+    r.new_momenta = in.new_momenta;
+    r.mo = in.mo;
+    r.dtype = in.dtype;
+    r.momentum = in.momentum;
+    r.tall = L.tall;
+    r.m = uint32_t(L.m);
+    r.n = uint32_t(L.n);
+    r.eps = c.eps;
+    Coefficients coef{};
+    for (int k = 0; k < 3 * c.steps; ++k)
+        coef.v[k / 3][k % 3] = c.coefficients[k];
+    with_resident(L.small, std::max(L.m, L.n), L.both, [&](auto RB, auto NB, auto planes) {
+        hipLaunchKernelGGL((resident_kernel<decltype(RB)::value, decltype(NB)::value, decltype(planes)::value>),
+                           dim3(unsigned(c.count)), dim3(kResidentWaves * kWave), 0, stream, r, coef, c.steps, last);
+    });
+    return check_launch(c.what);
+}
+
 template <typename T, bool kMomentum>
-int run_call(const Call& c, const Layout& L, const PtrTable<T>& x, const PtrTable<float>& momenta,
-             const PtrTable<float>& new_momenta, const Momentum& mo, const LastOut& last, hipStream_t stream)
+void launch_first(const Call& c, const Layout& L, const In& in, hipStream_t stream)
 {
     char* ws = static_cast<char*>(c.ws);
     double* parts = reinterpret_cast<double*>(ws + L.parts);
+    PtrTable<T> x{};
+    for (size_t k = 0; k < c.count; ++k)
+        x.p[k] = static_cast<const T*>(in.x.p[k]);
     hipLaunchKernelGGL((norm_kernel<T, kMomentum>), dim3(L.nparts, unsigned(c.count)), dim3(kThreads), 0, stream, x,
-                       momenta, new_momenta, mo, c.m * c.n, parts, reinterpret_cast<u32x4*>(ws + L.zero),
+                       in.momenta, in.new_momenta, in.mo, c.m * c.n, parts, reinterpret_cast<u32x4*>(ws + L.zero),
                        leaves_padding(L, c.count) ? L.zeros / 16 : 0);
     const size_t chunks = L.x[0].matrix_stride / 8;
     hipLaunchKernelGGL((first_kernel<T, kMomentum>),
                        dim3(unsigned(std::min<size_t>(ceil_div(chunks, kThreads * 4), kMaxParts)), unsigned(c.count)),
-                       dim3(kThreads), 0, stream, x, new_momenta, mo, c.m, c.n, c.eps, parts, L.nparts, L.x[0]);
+                       dim3(kThreads), 0, stream, x, in.new_momenta, in.mo, c.m, c.n, c.eps, parts, L.nparts, L.x[0]);
+}
+
+int run_call(const Call& c, const Layout& L, const In& in, const LastOut& last, hipStream_t stream)
+{
+    if (L.resident)
+        return run_resident(c, L, in, last, stream);
+    if (in.momentum)
+        launch_first<float, true>(c, L, in, stream);
+    else
+        with_dtype(in.dtype, [&](auto e) {
+            launch_first<decltype(e), false>(c, L, in, stream);
+            return 0;
+        });
+    char* ws = static_cast<char*>(c.ws);
     if (L.tall)
         iterate<true>(L, c.count, c.coefficients, c.steps, last, ws, stream);
     else
@@ -968,22 +1035,17 @@ GCQ_API int orthogonalize(const void* const* x, int count, size_t m, size_t n, i
         return refuse(c, "unknown dtype");
     if (m == 0 || n == 0)
         return GC_OK;
-    PtrTable<void> from{};
+    In in{};
     LastOut last{};
-    if (!take_pointers(from, x, c.count, dtype_bytes(dtype)) ||
+    if (!take_pointers(in.x, x, c.count, dtype_bytes(dtype)) ||
         !take_pointers(last.out, out, c.count, dtype_bytes(out_dtype)))
         return refuse(c, "a matrix is NULL or misaligned");
     last.dtype = out_dtype;
     last.m = uint32_t(m);
     last.n = uint32_t(n);
     last.scale = scale;
-    return with_dtype(dtype, [&](auto e) {
-        using T = decltype(e);
-        PtrTable<T> typed{};
-        for (size_t k = 0; k < c.count; ++k)
-            typed.p[k] = static_cast<const T*>(from.p[k]);
-        return run_call<T, false>(c, L, typed, PtrTable<float>{}, PtrTable<float>{}, Momentum{}, last, stream);
-    });
+    in.dtype = dtype;
+    return run_call(c, L, in, last, stream);
 }
 
 GCQ_API int muon_step(const float* const* grads, int count, size_t m, size_t n, const float* const* momenta,
@@ -1009,11 +1071,11 @@ GCQ_API int muon_step(const float* const* grads, int count, size_t m, size_t n, 
         return refuse(c, "lr_scale is misaligned");
     if (m == 0 || n == 0)
         return GC_OK;
-    PtrTable<float> g{}, m0{}, m1{};
+    In in{};
     LastOut last{};
-    if (!take_pointers(g, reinterpret_cast<const void* const*>(grads), c.count, 4) ||
-        !take_pointers(m0, reinterpret_cast<const void* const*>(momenta), c.count, 4) ||
-        !take_pointers(m1, reinterpret_cast<const void* const*>(new_momenta), c.count, 4) ||
+    if (!take_pointers(in.x, reinterpret_cast<const void* const*>(grads), c.count, 4) ||
+        !take_pointers(in.momenta, reinterpret_cast<const void* const*>(momenta), c.count, 4) ||
+        !take_pointers(in.new_momenta, reinterpret_cast<const void* const*>(new_momenta), c.count, 4) ||
         !take_pointers(last.weights, weights, c.count, b) || !take_pointers(last.out, new_weights, c.count, b))
         return refuse(c, "a matrix is NULL or misaligned");
     last.dtype = dtype;
@@ -1024,5 +1086,8 @@ GCQ_API int muon_step(const float* const* grads, int count, size_t m, size_t n, 
     last.lr = lr;
     last.decay = weight_decay;
     last.lr_scale = lr_scale;
-    return run_call<float, true>(c, L, g, m0, m1, Momentum{grad_scale, momentum, nesterov != 0}, last, stream);
+    in.dtype = GC_F32;
+    in.momentum = true;
+    in.mo = Momentum{grad_scale, momentum, nesterov != 0};
+    return run_call(c, L, in, last, stream);
 }

@@ -119,7 +119,10 @@ def run(gcq, xs, out_dtype, series=QUINTIC, place=lambda v: v, **kw):
 
 
 SHAPES = [(1, 1, 1), (2, 1, 7), (1, 5, 1), (3, 3, 5), (1, 64, 64), (1, 64, 576), (2, 65, 63), (1, 100, 300),
-          (2, 128, 128), (3, 129, 257), (1, 300, 100), (2, 513, 40), (1, 10, 1000), (1, 700, 640), (5, 257, 700)]
+          (2, 128, 128), (3, 129, 257), (1, 300, 100), (2, 513, 40), (1, 10, 1000), (1, 700, 640), (5, 257, 700),
+          # what one workgroup holds: each of its kinds, at its edges
+          (64, 17, 20), (3, 32, 256), (2, 33, 31), (1, 1024, 32), (2, 24, 1000), (1, 64, 256), (7, 257, 64), (1, 50, 1024),
+          (2, 128, 256), (1, 200, 70), (1, 65, 129), (1, 31, 1025), (1, 129, 129)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)

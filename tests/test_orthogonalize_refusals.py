@@ -31,7 +31,7 @@ ONE = floats(1.5, -0.5, 0.0)
 
 
 def orth(lib, size=None, **kw):
-    a = dict(x=pointers(FAKE, FAKE), count=2, m=8, n=16, dt=0, coef=ONE, steps=1, eps=1e-7, scale=1.0,
+    a = dict(x=pointers(FAKE, FAKE), count=2, m=256, n=300, dt=0, coef=ONE, steps=1, eps=1e-7, scale=1.0,
              out=pointers(FAKE, FAKE), odt=1, ws=FAKE) | kw
     n = ctypes.c_size_t(1 << 30 if size is None else size)
     rc = lib.orthogonalize(a["x"], a["count"], a["m"], a["n"], a["dt"], a["coef"], a["steps"], a["eps"], a["scale"],
@@ -64,6 +64,8 @@ def test_workspace_sizes():
     assert gcq.orthogonalize_ws_bytes(1, 4096, 4096, torch.float32) > one
     assert gcq.muon_step_ws_bytes(3, 100, 70, torch.float32) == gcq.orthogonalize_ws_bytes(3, 100, 70, torch.float32)
     assert gcq.orthogonalize_ws_bytes(1, 0, 5, torch.float32) > 0
+    # what one workgroup holds needs none to speak of
+    assert gcq.orthogonalize_ws_bytes(64, 64, 576, torch.bfloat16) == 256
     # sizes past 32 bits
     assert gcq.orthogonalize_ws_bytes(64, 2 ** 15, 2 ** 15, torch.bfloat16) > 64 * 8 * 2 ** 30
     with pytest.raises(gcq.GcqError, match="1 .. 64"):
@@ -72,7 +74,7 @@ def test_workspace_sizes():
 
 def step(lib, size=None, **kw):
     p = pointers(FAKE)
-    a = dict(g=p, count=1, m=8, n=16, m0=p, w=p, dt=0, udt=0, coef=ONE, steps=1, eps=1e-7, gs=1.0, beta=0.9, nest=1,
+    a = dict(g=p, count=1, m=256, n=300, m0=p, w=p, dt=0, udt=0, coef=ONE, steps=1, eps=1e-7, gs=1.0, beta=0.9, nest=1,
              lr=0.1, ls=FAKE, wd=0.0, us=1.0, m1=p, w1=p, ws=FAKE) | kw
     n = ctypes.c_size_t(1 << 30 if size is None else size)
     rc = lib.muon_step(a["g"], a["count"], a["m"], a["n"], a["m0"], a["w"], a["dt"], a["udt"], a["coef"], a["steps"],
@@ -121,7 +123,7 @@ def test_binding_checks():
     with pytest.raises(ValueError, match="ws too small"):
         gcq.orthogonalize([d(4, 8)], [d(4, 8)], d(0, dtype=torch.uint8), stream=S)
     with pytest.raises(gcq.GcqError, match="workspace too small"):
-        gcq.orthogonalize([d(4, 8)], [d(4, 8)], d(64, dtype=torch.uint8), stream=S)
+        gcq.orthogonalize([d(200, 300)], [d(200, 300)], d(64, dtype=torch.uint8), stream=S)
     with pytest.raises(ValueError, match="momenta differ in size"):
         gcq.muon_step([d(4, 8)], [d(4, 9)], [d(4, 8)], ws, stream=S)
     with pytest.raises(ValueError, match="new_weights differ in number"):
