@@ -967,7 +967,6 @@ int run_resident(const Call& c, const Layout& L, const In& in, const LastOut& la
     r.mo = in.mo;
     r.dtype = in.dtype;
     r.momentum = in.momentum;
-    r.tall = L.tall;
     r.m = uint32_t(L.m);
     r.n = uint32_t(L.n);
     r.eps = c.eps;
@@ -975,8 +974,15 @@ int run_resident(const Call& c, const Layout& L, const In& in, const LastOut& la
     for (int k = 0; k < 3 * c.steps; ++k)
         coef.v[k / 3][k % 3] = c.coefficients[k];
     with_resident(L.small, std::max(L.m, L.n), L.both, [&](auto RB, auto NB, auto planes) {
-        hipLaunchKernelGGL((resident_kernel<decltype(RB)::value, decltype(NB)::value, decltype(planes)::value>),
-                           dim3(unsigned(c.count)), dim3(kResidentWaves * kWave), 0, stream, r, coef, c.steps, last);
+        const auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3(unsigned(c.count)), dim3(kResidentWaves * kWave), 0, stream, r, coef,
+                               c.steps, last);
+        };
+        constexpr int kRB = decltype(RB)::value, kNB = decltype(NB)::value, kPlanes = decltype(planes)::value;
+        if (L.tall)
+            launch(resident_kernel<kRB, kNB, kPlanes, true>);
+        else
+            launch(resident_kernel<kRB, kNB, kPlanes, false>);
     });
     return check_launch(c.what);
 }

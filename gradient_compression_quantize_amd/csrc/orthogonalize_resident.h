@@ -8,10 +8,12 @@
 // 576 took 89 us with them.
 //
 // The smaller side r is padded to RP = 32, 64 or 128, the other one, c, to blocks
-// of 32. LDS holds X transposed, [c][RP]: the update reads it by rows, the product
-// X X' through the transposing load. Each wave owns every eighth block column of
-// X; the blocks of A are split over the waves, over c too where there are fewer of
-// them than waves.
+// of 32, and each wave owns every eighth 32 of c. Of a block, a lane holds 4
+// values of a row side by side (16 bytes of the matrix at a time), and LDS the
+// matrix as it lies: where a product needs it the other way, it reads it through
+// the transposing load (a tall one in A = X' X, a wide one in P X). The blocks of
+// A are split over the waves, over c too where there are fewer of them than
+// waves.
 #pragma once
 
 #include "mfma_product.h"
@@ -27,18 +29,18 @@ struct Coefficients {
     float v[kMaxSteps][3];
 };
 
-// A matrix of fp16 in LDS, rows of RP values, in 16-byte chunks that an XOR of
-// the row spreads over the 64 banks.
-template <int RP>
+// A matrix of fp16 in LDS, rows of kLength values, in 16-byte chunks that an XOR
+// of the row spreads over the 64 banks.
+template <int kLength>
 struct LdsMatrix {
-    static constexpr int kChunks = RP / 8, kRowsOfBanks = 16 / kChunks;
+    static constexpr int kChunks = kLength / 8, kSpread = kChunks < 16 ? kChunks : 16, kRowsOfBanks = 16 / kSpread;
     typedef __attribute__((address_space(3))) uint16_t lds_u16;
     lds_u16* p;
 
     __device__ __forceinline__ lds_u16* at(int row, int col) const
     {
-        const int chunk = (col >> 3) ^ ((row / kRowsOfBanks) & (kChunks - 1));
-        return p + row * RP + chunk * 8 + (col & 7);
+        const int chunk = (col >> 3) ^ ((row / kRowsOfBanks) & (kSpread - 1));
+        return p + row * kLength + chunk * 8 + (col & 7);
     }
 
     // Fragment of 32 rows x 16 k, the k of a row side by side.
@@ -77,9 +79,9 @@ struct LdsMatrix {
 };
 
 // One plane of a matrix or two that add up to it.
-template <int RP, int kPlanes>
+template <int kLength, int kPlanes>
 struct LdsPlanes {
-    LdsMatrix<RP> plane[kPlanes];
+    LdsMatrix<kLength> plane[kPlanes];
 
     __device__ __forceinline__ void set(int row, int col, f32x4 v) const
     {
@@ -119,7 +121,7 @@ struct ResidentIn {
     PtrTable<float> momenta, new_momenta;
     Momentum mo;
     int dtype;
-    bool momentum, tall;
+    bool momentum;
     uint32_t m, n;
     float eps;
 };
@@ -135,26 +137,27 @@ __device__ __forceinline__ uint16_t to16(float v, bool bf16)
     return bf16 ? __builtin_bit_cast(uint16_t, bf16_t(v)) : __builtin_bit_cast(uint16_t, f16_t(v));
 }
 
-// RB: RP / 32; NB: block columns of a wave.
-template <int RB, int NB, int kPlanes>
+// RB: RP / 32; NB: 32s of c a wave owns; kTall: c is the number of rows.
+template <int RB, int NB, int kPlanes, bool kTall>
 __global__ __launch_bounds__(kResidentWaves* kWave, 2) void resident_kernel(ResidentIn in, Coefficients coef, int steps,
                                                                             LastOut last)
 {
-    constexpr int RP = 32 * RB, kXRows = kResidentWaves * NB * 32;
+    constexpr int RP = 32 * RB, CP = kResidentWaves * NB * 32;
     // of A: a wave's blocks, and how many waves share one
     constexpr int kBlocks = RB * RB, kSplit = kBlocks < kResidentWaves ? kResidentWaves / kBlocks : 1;
     constexpr int kOwn = kBlocks > kResidentWaves ? kBlocks / kResidentWaves : 1;
     constexpr int kSums = (kSplit - 1) * kBlocks * 1024 * 4, kAP = 2 * kPlanes * RP * RP * 2;
-    __shared__ uint16_t lds_x[kPlanes * kXRows * RP];
+    __shared__ uint16_t lds_x[kPlanes * CP * RP];
     // A and P, and before them the sums of the waves that share a block
     __shared__ uint16_t lds_ap[(kSums > kAP ? kSums : kAP) / 2];
     __shared__ __attribute__((aligned(16))) float diagonal_a[RP], diagonal_p[RP];
     __shared__ double norm_parts[kResidentWaves];
     typedef __attribute__((address_space(3))) uint16_t lds_u16;
-    LdsPlanes<RP, kPlanes> X, A, P;
+    LdsPlanes<kTall ? RP : CP, kPlanes> X;
+    LdsPlanes<RP, kPlanes> A, P;
 #pragma unroll
     for (int k = 0; k < kPlanes; ++k) {
-        X.plane[k].p = (lds_u16*)lds_x + k * kXRows * RP;
+        X.plane[k].p = (lds_u16*)lds_x + k * CP * RP;
         A.plane[k].p = (lds_u16*)lds_ap + k * RP * RP;
         P.plane[k].p = (lds_u16*)lds_ap + (kPlanes + k) * RP * RP;
     }
@@ -168,95 +171,159 @@ __global__ __launch_bounds__(kResidentWaves* kWave, 2) void resident_kernel(Resi
     const void* const weights = last.weights.p[matrix];
     void* const out = const_cast<void*>(last.out.p[matrix]);
     const Momentum mo = in.mo;
-    const bool tall = in.tall, momentum = in.momentum, moves = last.update;
+    const bool momentum = in.momentum, moves = last.update;
     const int in_dtype = in.dtype, out_dtype = last.dtype;
+    const uint32_t m = in.m, n = in.n;
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t r = tall ? in.n : in.m, c = tall ? in.m : in.n;
-    const int blocks = int((c + 31) / 32);
-
-    // The values of block (nb, i) from or to a matrix of values of 16 or 32 bits,
-    // by buffer instructions: one that does not exist lies behind the last,
-    // where loads give 0 and stores do nothing, so that there are no branches
-    // and all loads are on their way together. Their places are found anew each
-    // time: kept, they would take as many registers as the values.
-    f32x16 x[NB][RB];
-    const auto view = [&](const void* p, bool wide) {
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, r * c * (wide ? 4 : 2), 0x00020000);
+    const int blocks = int(((kTall ? m : n) + 31) / 32);
+    const auto owns = [&](int nb) { return nb * kResidentWaves + wave < blocks; };
+    // Row of this lane's values in block (nb, i), and column of its quad q.
+    const auto row_of = [&](int nb, int i, int l) {
+        return (kTall ? nb * kResidentWaves + wave : i) * 32 + int(acc_col(l));
     };
-    const auto each_of = [&](int nb, int i, auto f) {
+    const auto col_of = [&](int nb, int i, int q, int l) {
+        return (kTall ? i : nb * kResidentWaves + wave) * 32 + int(acc_row(4 * q, l));
+    };
+
+    // The values of block (nb, i) from or to a matrix in memory, by buffer
+    // instructions: one that does not exist lies behind the last, where loads
+    // give 0 and stores do nothing, so that there are no branches and all loads
+    // are on their way together. Four at a time where each row holds whole
+    // quads. Places are found anew each time: kept, they would take as many
+    // registers as the values.
+    const auto each_quad = [&](int nb, int i, auto f) {
         int l = lane;
         asm volatile("" : "+v"(l));
-        const uint32_t col = (nb * kResidentWaves + wave) * 32 + acc_col(l);
+        const uint32_t row = row_of(nb, i, l);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const uint32_t row = i * 32 + acc_row(e, l);
-            f(e, col < c && row < r ? (tall ? col * r + row : row * c + col) : 1u << 28);
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t col = col_of(nb, i, q, l);
+            f(q, row < m && col < n ? row * n + col : 1u << 28, n - col);
         }
     };
     const auto get = [&](const void* p, int dtype, int nb, int i, f32x16& v) {
-        const auto from = view(p, dtype == GC_F32);
-        if (dtype == GC_F32)
-            each_of(nb, i, [&](int e, uint32_t at) {
-                v[e] = u2f(__builtin_amdgcn_raw_buffer_load_b32(from, at * 4, 0, 0));
+        const bool wide = dtype == GC_F32, bf16 = dtype == GC_BF16;
+        const auto at = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, m * n * (wide ? 4 : 2), 0x00020000);
+        const bool whole = n % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 3) == 0;
+        if (wide && whole)
+            each_quad(nb, i, [&](int q, uint32_t first, uint32_t) {
+                const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(at, first * 4, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[4 * q + e] = u2f(w[e]);
+            });
+        else if (whole)
+            each_quad(nb, i, [&](int q, uint32_t first, uint32_t) {
+                const auto w = __builtin_amdgcn_raw_buffer_load_b64(at, first * 2, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[4 * q + e] = from16(uint16_t(w[e / 2] >> 16 * (e % 2)), bf16);
             });
         else
-            each_of(nb, i, [&](int e, uint32_t at) {
-                v[e] = from16(__builtin_amdgcn_raw_buffer_load_b16(from, at * 2, 0, 0), dtype == GC_BF16);
+            each_quad(nb, i, [&](int q, uint32_t first, uint32_t left) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t one = uint32_t(e) < left ? first + e : 1u << 28;
+                    v[4 * q + e] = wide ? u2f(__builtin_amdgcn_raw_buffer_load_b32(at, one * 4, 0, 0))
+                                        : from16(__builtin_amdgcn_raw_buffer_load_b16(at, one * 2, 0, 0), bf16);
+                }
             });
     };
     const auto put = [&](void* p, int dtype, int nb, int i, const f32x16& v) {
-        const auto to = view(p, dtype == GC_F32);
-        if (dtype == GC_F32)
-            each_of(nb, i, [&](int e, uint32_t at) { __builtin_amdgcn_raw_buffer_store_b32(f2u(v[e]), to, at * 4, 0, 0); });
+        const bool wide = dtype == GC_F32, bf16 = dtype == GC_BF16;
+        const auto at = __builtin_amdgcn_make_buffer_rsrc(p, 0, m * n * (wide ? 4 : 2), 0x00020000);
+        const bool whole = n % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 3) == 0;
+        if (wide && whole)
+            each_quad(nb, i, [&](int q, uint32_t first, uint32_t) {
+                u32x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = f2u(v[4 * q + e]);
+                __builtin_amdgcn_raw_buffer_store_b128(w, at, first * 4, 0, 0);
+            });
+        else if (whole)
+            each_quad(nb, i, [&](int q, uint32_t first, uint32_t) {
+                vec_of<uint32_t, 2> w;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    w[e] = to16(v[4 * q + 2 * e], bf16) | uint32_t(to16(v[4 * q + 2 * e + 1], bf16)) << 16;
+                __builtin_amdgcn_raw_buffer_store_b64(w, at, first * 2, 0, 0);
+            });
         else
-            each_of(nb, i, [&](int e, uint32_t at) {
-                __builtin_amdgcn_raw_buffer_store_b16(to16(v[e], dtype == GC_BF16), to, at * 2, 0, 0);
+            each_quad(nb, i, [&](int q, uint32_t first, uint32_t left) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t one = uint32_t(e) < left ? first + e : 1u << 28;
+                    if (wide)
+                        __builtin_amdgcn_raw_buffer_store_b32(f2u(v[4 * q + e]), at, one * 4, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b16(to16(v[4 * q + e], bf16), at, one * 2, 0, 0);
+                }
             });
     };
-    // One block column at a time, the others moving up: 16 RB loads are on their
-    // way together, and the code of all NB, which the first waves to come by have
-    // to fetch, is that of one.
+
+    // One or two 32s of c at a time, the others moving up: their loads are on
+    // their way together, and the code of all NB, which the first waves to come
+    // by have to fetch, is that of these.
+    constexpr int kAtOnce = NB > 1 ? 2 : 1;
+    f32x16 x[NB][RB];
     const auto columns = [&](auto f) {
 #pragma unroll 1
-        for (int nb = 0; nb < NB; ++nb) {
-            f32x16 v[RB];
+        for (int nb = 0; nb < NB; nb += kAtOnce) {
+            f32x16 v[kAtOnce][RB];
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
-                v[i] = x[0][i];
-            f(nb, v);
+            for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                    v[k][i] = x[k][i];
+            if (owns(nb))
+                f(nb, v);
 #pragma unroll
             for (int k = 0; k < NB; ++k)
 #pragma unroll
                 for (int i = 0; i < RB; ++i)
-                    x[k][i] = k + 1 < NB ? x[k + 1 < NB ? k + 1 : 0][i] : v[i];
+                    x[k][i] = k + kAtOnce < NB ? x[(k + kAtOnce) % NB][i] : v[(k + kAtOnce) % NB % kAtOnce][i];
         }
     };
-    double sum = 0.0;
-    columns([&](int nb, f32x16 (&v)[RB]) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < RB; ++i)
-            get(from, in_dtype, nb, i, v[i]);
-        if (momentum) {
-            f32x16 m[RB];  // (new momenta may be the old ones: all of them are read first)
+            x[nb][i] = f32x16{};
+    double sum = 0.0;
+    columns([&](int nb, f32x16 (&v)[kAtOnce][RB]) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
 #pragma unroll
             for (int i = 0; i < RB; ++i)
-                get(m0, GC_F32, nb, i, m[i]);
+                get(from, in_dtype, nb + k, i, v[k][i]);
+        if (momentum) {
+            f32x16 old[kAtOnce][RB];  // (new momenta may be the old ones: all are read first)
 #pragma unroll
-            for (int i = 0; i < RB; ++i) {
+            for (int k = 0; k < kAtOnce; ++k)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float g = v[i][e] * mo.grad_scale;
-                    m[i][e] = mix(g, m[i][e], mo.beta);
-                    v[i][e] = mo.nesterov ? mix(g, m[i][e], mo.beta) : m[i][e];
+                for (int i = 0; i < RB; ++i)
+                    get(m0, GC_F32, nb + k, i, old[k][i]);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float g = v[k][i][e] * mo.grad_scale, now = mix(g, old[k][i][e], mo.beta);
+                        old[k][i][e] = now;
+                        v[k][i][e] = mo.nesterov ? mix(g, now, mo.beta) : now;
+                    }
+                    put(m1, GC_F32, nb + k, i, old[k][i]);
                 }
-                put(m1, GC_F32, nb, i, m[i]);
-            }
         }
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
+        for (int k = 0; k < kAtOnce; ++k)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                sum = __builtin_fma(double(v[i][e]), double(v[i][e]), sum);
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    sum = __builtin_fma(double(v[k][i][e]), double(v[k][i][e]), sum);
     });
 #pragma unroll
     for (int off = kWave / 2; off > 0; off >>= 1)
@@ -294,12 +361,13 @@ __global__ __launch_bounds__(kResidentWaves* kWave, 2) void resident_kernel(Resi
         // X into LDS
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
+            if (owns(nb)) {
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
+                for (int i = 0; i < RB; ++i)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    X.set((nb * kResidentWaves + wave) * 32 + int(acc_col(lane)), i * 32 + int(acc_row(4 * q, lane)),
-                          quad_of(x[nb][i], q));
+                    for (int q = 0; q < 4; ++q)
+                        X.set(row_of(nb, i, lane), col_of(nb, i, q, lane), quad_of(x[nb][i], q));
+            }
         __syncthreads();
 
         // A = X X'
@@ -315,8 +383,11 @@ __global__ __launch_bounds__(kResidentWaves* kWave, 2) void resident_kernel(Resi
                 s16x8 fa[kPlanes], fb[kPlanes];
 #pragma unroll
                 for (int p = 0; p < kPlanes; ++p) {
-                    fa[p] = X.plane[p].by_k(block(o) / RB * 32, 16 * k, lane);
-                    fb[p] = X.plane[p].by_k(block(o) % RB * 32, 16 * k, lane);
+                    const auto of = [&](int first) {
+                        return kTall ? X.plane[p].by_k(first, 16 * k, lane) : X.plane[p].by_rows(first, 16 * k, lane);
+                    };
+                    fa[p] = of(block(o) / RB * 32);
+                    fb[p] = of(block(o) % RB * 32);
                 }
                 acc[o] = multiply_planes<kPlanes>(fa, fb, acc[o]);
             }
@@ -414,12 +485,16 @@ __global__ __launch_bounds__(kResidentWaves* kWave, 2) void resident_kernel(Resi
         }
         __syncthreads();
 
-        // X = a X + P X
+        // X = a X + P X (X P of a tall one)
 #pragma unroll
         for (int i = 0; i < RB; ++i)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const f32x4 d = *reinterpret_cast<const f32x4*>(diagonal_p + i * 32 + acc_row(4 * q, lane));
+                f32x4 d;
+                if (kTall)
+                    d = *reinterpret_cast<const f32x4*>(diagonal_p + i * 32 + acc_row(4 * q, lane));
+                else
+                    d = f32x4{} + diagonal_p[i * 32 + acc_col(lane)];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float self = (ca + d[e]) * pow2<kPExp>;
@@ -438,25 +513,26 @@ __global__ __launch_bounds__(kResidentWaves* kWave, 2) void resident_kernel(Resi
                     fp[i][p] = P.plane[p].by_rows(i * 32, k, lane);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
+                if (!owns(nb))
+                    break;
+                const int first = (nb * kResidentWaves + wave) * 32;
                 s16x8 fx[kPlanes];
 #pragma unroll
                 for (int p = 0; p < kPlanes; ++p)
-                    fx[p] = X.plane[p].by_rows((nb * kResidentWaves + wave) * 32, k, lane);
+                    fx[p] = kTall ? X.plane[p].by_rows(first, k, lane) : X.plane[p].by_k(first, k, lane);
 #pragma unroll
                 for (int i = 0; i < RB; ++i)
-                    x[nb][i] = multiply_planes<kPlanes>(fp[i], fx, x[nb][i]);
+                    x[nb][i] = kTall ? multiply_planes<kPlanes>(fp[i], fx, x[nb][i])
+                                     : multiply_planes<kPlanes>(fx, fp[i], x[nb][i]);
             }
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int i = 0; i < RB; ++i)
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    x[nb][i][e] *= pow2<-kPExp>;
-        // (each wave writes again only the rows of X that it alone has read in
-        // the update; the others are done with all of them since the barrier
-        // behind A)
+                x[nb][i] *= pow2<-kPExp>;
+        // (each wave writes again only the part of X that it alone has read in
+        // the update; the others are done with it since the barrier behind A)
     }
 
     float keep = 0.0f, times = last.scale * pow2<-kXExp>;
@@ -465,20 +541,24 @@ __global__ __launch_bounds__(kResidentWaves* kWave, 2) void resident_kernel(Resi
         keep = __builtin_fmaf(-lr, last.decay, 1.0f);
         times = -lr * last.scale * pow2<-kXExp>;
     }
-    columns([&](int nb, f32x16 (&v)[RB]) {
-        f32x16 w[RB] = {};
+    columns([&](int nb, f32x16 (&v)[kAtOnce][RB]) {
+        f32x16 w[kAtOnce][RB] = {};
         if (moves) {
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
-                get(weights, out_dtype, nb, i, w[i]);
+            for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                    get(weights, out_dtype, nb + k, i, w[k][i]);
         }
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
+        for (int k = 0; k < kAtOnce; ++k)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                v[i][e] = moves ? __builtin_fmaf(w[i][e], keep, v[i][e] * times) : v[i][e] * times;
-            put(out, out_dtype, nb, i, v[i]);
-        }
+            for (int i = 0; i < RB; ++i) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    v[k][i][e] = moves ? __builtin_fmaf(w[k][i][e], keep, v[k][i][e] * times) : v[k][i][e] * times;
+                put(out, out_dtype, nb + k, i, v[k][i]);
+            }
     });
 }
 
