@@ -239,6 +239,7 @@ __device__ __forceinline__ void triangle_of(uint32_t id, uint32_t& ta, uint32_t&
 struct Tiles {
     uint32_t per_matrix;
     uint32_t a, b;  // of a product that is not symmetric
+    float* slab;    // of one over several ranges of k: what each leaves
 };
 
 template <int T>
@@ -480,13 +481,33 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
     constexpr int WA = Waves<T>::a, WB = Waves<T>::b;
     using P = TileProduct<true, kKRows, kKRows, T, T, WA, WB, true>;
     GCQ_TILE_BUFFERS(lds, T, T);
-    const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), matrix = id / tiles.per_matrix;
+    const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), range = id / tiles.per_matrix;
+    const uint32_t matrix = range / sh.splits, split = range - matrix * sh.splits;
     uint32_t ta, tb;
-    triangle_of(id - matrix * tiles.per_matrix, ta, tb);
+    triangle_of(id - range * tiles.per_matrix, ta, tb);
     V.plane0 += matrix * matrix_stride;
+    const uint32_t turns = sh.turns * sh.segments;
     typename P::Acc acc;
-    P::run(V, V, sh, ta * T, tb * T, 0, sh.turns * sh.segments, lds, acc);
+    P::run(V, V, sh, ta * T, tb * T, uint32_t(uint64_t(turns) * split / sh.splits),
+           uint32_t(uint64_t(turns) * (split + 1) / sh.splits), lds, acc);
 
+    if (!kSquare && sh.splits > 1) {  // the sums as the lanes hold them, for join_kernel
+        const int lane = threadIdx.x & (kWave - 1);
+        f32x4* to = reinterpret_cast<f32x4*>(tiles.slab) + (size_t(id) * (WA * WB) + threadIdx.x / kWave) * (P::RA * P::RB * 256);
+#pragma unroll
+        for (int i = 0; i < P::RA; ++i)
+#pragma unroll
+            for (int j = 0; j < P::RB; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    f32x4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = acc.v[i][j][4 * q + e];
+                    to[((i * P::RB + j) * 4 + q) * kWave + lane] = v;
+                }
+        return;
+    }
     using Rows = PartPlanes<T>;
     const Rows part(lds, ta * T, tb * T);
     uint16_t* to = held_at(out.to, matrix, 0);
@@ -552,6 +573,57 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
         }
         wave_lds_sync();
     }
+}
+
+// A of what the ranges of k have left: one workgroup for each 32 x 32 block of each
+// tile adds its 4 KB of every range, in their order.
+template <int T>
+__global__ __launch_bounds__(kThreads) void join_kernel(const f32x4* __restrict__ slab, uint32_t splits, Tiles tiles,
+                                                        SymmetricOut out)
+{
+    constexpr int WA = Waves<T>::a, WB = Waves<T>::b, RA = T / WA / 32, RB = T / WB / 32, kBlocks = WA * WB * RA * RB;
+    __shared__ float turned[32][33];
+    const uint32_t tile_id = blockIdx.x / kBlocks, block = blockIdx.x - tile_id * kBlocks;
+    const uint32_t matrix = tile_id / tiles.per_matrix, tile = tile_id - matrix * tiles.per_matrix;
+    uint32_t ta, tb;
+    triangle_of(tile, ta, tb);
+    const f32x4* from = slab + (size_t(matrix) * splits * tiles.per_matrix + tile) * (kBlocks * 256) + block * 256 + threadIdx.x;
+    const size_t stride = size_t(tiles.per_matrix) * (kBlocks * 256);
+    f32x4 v = {};
+#pragma unroll 8
+    for (uint32_t s = 0; s < splits; ++s)
+        v += from[s * stride];
+    v *= pow2<kAExp - 2 * kXExp>;
+
+    const uint32_t wave = block / (RA * RB), in = block % (RA * RB), lane = threadIdx.x & (kWave - 1);
+    const uint32_t a0 = ta * T + wave % WA * (T / WA) + in / RB * 32, b0 = tb * T + wave / WA * (T / WB) + in % RB * 32;
+    const uint32_t side = out.to.rows;
+    if (a0 >= side || b0 >= side)
+        return;
+    const uint32_t a = acc_row(threadIdx.x / kWave * 4, lane), b = acc_col(lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (a0 + a + e == b0 + b) {
+            out.diagonal[size_t(matrix) * side + b0 + b] = v[e] * pow2<-kAExp>;
+            v[e] = 0.0f;
+        }
+    const auto store = [&](uint32_t row, uint32_t col, f32x4 x) {
+        uint16_t* p = held_at(out.to, matrix, 0) + size_t(row) * out.to.ld + col;
+        const f16x4 p0 = __builtin_convertvector(x, f16x4);
+        *reinterpret_cast<f16x4*>(p) = p0;
+        if (out.both)
+            *reinterpret_cast<f16x4*>(p + out.to.plane_stride) =
+                __builtin_convertvector(x - __builtin_convertvector(p0, f32x4), f16x4);
+    };
+    store(b0 + b, a0 + a, v);
+    if (ta == tb)
+        return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        turned[a + e][b] = v[e];
+    __syncthreads();
+    const uint32_t row = threadIdx.x / 8, col = threadIdx.x % 8 * 4;
+    store(a0 + row, b0 + col, f32x4{turned[row][col], turned[row][col + 1], turned[row][col + 2], turned[row][col + 3]});
 }
 
 // P = b A of a step without a second power.
@@ -710,10 +782,102 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
 size_t round_up(size_t a, size_t b) { return ceil_div(a, b) * b; }
 
 constexpr size_t kMaxSide = size_t(1) << 20, kMaxSmallSide = size_t(1) << 15, kMaxTiles = size_t(1) << 22;
+void place(Held& h, char* ws) { h.plane0 = reinterpret_cast<uint16_t*>(ws + reinterpret_cast<size_t>(h.plane0)); }
+
+MatOperand operand(const Held& h)
+{
+    MatOperand o{};
+    o.plane0 = h.plane0;
+    o.plane_stride = h.plane_stride;
+    o.ld = h.ld;
+    return o;
+}
+
+size_t triangle_tiles(size_t side, size_t t) { return ceil_div(side, t) * (ceil_div(side, t) + 1) / 2; }
+size_t all_tiles(size_t a, size_t b, size_t t) { return ceil_div(a, t) * ceil_div(b, t); }
+
+// How a product goes: its tiles, and over how many ranges of k.
+struct Plan {
+    int tile;
+    uint32_t splits;
+};
+
+// Microseconds of `tiles` tiles of T over `turns` turns of 128 k, from what a turn
+// was measured to take (random values, 4096 and 16384 k): alone on a compute unit
+// with half of the chip's at work 2.8 (T = 256), 1.05 (128), 0.75 (64), with all of
+// them 3.9, 1.3 and 0.85; two of 128 to a compute unit 2.8, four of 64 2.5. Tiles
+// of 256 then come in rounds, the others fill in as places become free.
+double tiles_cost(int T, double tiles, double turns)
+{
+    const double cus = 256.0, places = T == 256 ? cus : T == 128 ? 2.0 * cus : 4.0 * cus;
+    const double few = T == 256 ? 2.8 : T == 128 ? 1.05 : 0.75, one = T == 256 ? 3.9 : T == 128 ? 1.3 : 0.85;
+    const double full = T == 256 ? 3.9 : T == 128 ? 2.8 : 2.5, end = T == 256 ? 8.0 : T == 128 ? 4.0 : 3.0;
+    double turn, rounds = 1.0;
+    if (tiles <= cus / 2)
+        turn = few;
+    else if (tiles <= cus)
+        turn = few + (one - few) * (tiles / (cus / 2) - 1.0);
+    else if (tiles <= places)
+        turn = one + (full - one) * (tiles - cus) / (places - cus);
+    else {
+        turn = full;
+        rounds = T == 256 ? std::ceil(tiles / places) : tiles / places + 0.25;
+    }
+    return rounds * (turns * turn + end);
+}
+
+// Of the tiles of 256, 128 and 64, and of 1, 2, 4 .. ranges of at least four
+// turns each, what costs least: several ranges leave their sums in memory
+// (written and read at some 4 TB/s) for another launch (5 us). 64 x 16384, one
+// tile of 128 turns, takes XXX us in one range.
+template <typename Tiles>
+Plan plan_of(size_t count, size_t turns, bool may_split, Tiles tiles)
+{
+    Plan best{};
+    double least = 0.0;
+    for (int T = 256; T >= 64; T /= 2) {
+        const double n = double(count * tiles(T));
+        for (uint32_t s = 1; s == 1 || (may_split && s * 4 <= turns && n * s <= 1024.0); s *= 2) {
+            const double t = tiles_cost(T, n * s, double(ceil_div(turns, s))) +
+                             (s > 1 ? 5.0 + n * s * T * T * 8.0 / 4e6 : 0.0);
+            if (best.tile == 0 || t < least) {
+                best = Plan{T, s};
+                least = t;
+            }
+        }
+    }
+    return best;
+}
+
+size_t turns_of(size_t k, bool both) { return k / kTurnK * (both ? 3 : 1); }
+
+// Calls f with the tile as an integral constant.
+template <typename F>
+void with_tile(int tile, F f)
+{
+    if (tile == 256)
+        f(std::integral_constant<int, 256>());
+    else if (tile == 128)
+        f(std::integral_constant<int, 128>());
+    else
+        f(std::integral_constant<int, 64>());
+}
+
+ProductShape shape_of(size_t k, bool both)
+{
+    ProductShape sh{};
+    sh.turns = uint32_t(k / kTurnK);
+    set_pairs(sh, both ? 2 : 1, both ? 2 : 1);
+    sh.splits = 1;
+    return sh;
+}
+
 struct Layout {
     size_t m, n, small;     // small: the side of A
     bool tall, both;        // both: products of both planes
     bool resident;          // one workgroup a matrix, without a workspace
+    Plan gram, square, update;
+    size_t slab;            // of gram's ranges
     Held x[2], A, P;        // their plane0: an offset into the workspace
     size_t parts, diagonals[2], zero, zeros, total;  // bytes; diagonals of A and P
     uint32_t nparts;
@@ -756,83 +920,42 @@ Layout layout_of(size_t count, size_t m, size_t n, bool both)
     L.diagonals[0] = take(count * side * sizeof(float));
     L.diagonals[1] = take(count * side * sizeof(float));
     L.zeros = used - L.zero;
+    L.gram = plan_of(count, turns_of(L.tall ? rows : cols, both), true, [&](int T) { return triangle_tiles(L.small, T); });
+    L.square = plan_of(count, turns_of(side, both), false, [&](int T) { return triangle_tiles(L.small, T); });
+    L.update = plan_of(count, turns_of(side, both), false, [&](int T) { return all_tiles(m, n, T); });
+    const size_t T = L.gram.tile;
+    L.slab = take(L.gram.splits > 1 ? count * L.gram.splits * triangle_tiles(L.small, T) * T * T * 4 : 0);
+    // Tiles of 64 leave padding unwritten (128 is what it goes by), which then
+    // has to be zero from the start.
+    const auto half = [](size_t v) { return round_up(v, 64) % kTurnK != 0; };
+    const bool leaves = ((L.gram.tile == 64 || L.square.tile == 64) && half(L.small)) ||
+                        (L.update.tile == 64 && (half(m) || half(n)));
+    L.zeros = leaves ? L.zeros : 0;
     L.total = used;
     return L;
 }
 
-void place(Held& h, char* ws) { h.plane0 = reinterpret_cast<uint16_t*>(ws + reinterpret_cast<size_t>(h.plane0)); }
-
-MatOperand operand(const Held& h)
-{
-    MatOperand o{};
-    o.plane0 = h.plane0;
-    o.plane_stride = h.plane_stride;
-    o.ld = h.ld;
-    return o;
-}
-
-size_t triangle_tiles(size_t side, size_t t) { return ceil_div(side, t) * (ceil_div(side, t) + 1) / 2; }
-size_t all_tiles(size_t a, size_t b, size_t t) { return ceil_div(a, t) * ceil_div(b, t); }
-
-// Tiles of 256 x 256 as long as there are enough of them to fill half of the
-// chip, else of 128 x 128, else of 64 x 64.
-constexpr size_t kHalfOfChip = 128;
-
-int symmetric_tile(size_t count, size_t side)
-{
-    return count * triangle_tiles(side, 256) >= kHalfOfChip   ? 256
-           : count * triangle_tiles(side, 128) >= kHalfOfChip ? 128
-                                                              : 64;
-}
-
-int update_tile(size_t count, size_t m, size_t n)
-{
-    return count * all_tiles(m, n, 256) >= kHalfOfChip ? 256 : count * all_tiles(m, n, 128) >= kHalfOfChip ? 128 : 64;
-}
-
-// Calls f with the tile as an integral constant.
-template <typename F>
-void with_tile(int tile, F f)
-{
-    if (tile == 256)
-        f(std::integral_constant<int, 256>());
-    else if (tile == 128)
-        f(std::integral_constant<int, 128>());
-    else
-        f(std::integral_constant<int, 64>());
-}
-
-// Whether tiles of 64 leave padding unwritten (128 is what it goes by), which
-// then has to be zero from the start.
-bool leaves_padding(const Layout& L, size_t count)
-{
-    const auto half = [](size_t v) { return round_up(v, 64) % kTurnK != 0; };
-    return (symmetric_tile(count, L.small) == 64 && half(L.small)) ||
-           (update_tile(count, L.m, L.n) == 64 && (half(L.m) || half(L.n)));
-}
-
-ProductShape shape_of(size_t k, bool both)
-{
-    ProductShape sh{};
-    sh.turns = uint32_t(k / kTurnK);
-    set_pairs(sh, both ? 2 : 1, both ? 2 : 1);
-    sh.splits = 1;
-    return sh;
-}
 
 template <bool kKRows, bool kSquare>
-void launch_symmetric(const Held& v, size_t side, size_t k, size_t count, const SymmetricOut& out, hipStream_t stream)
+void launch_symmetric(const Held& v, const Plan& plan, size_t side, size_t k, size_t count, const SymmetricOut& out,
+                      float* slab, hipStream_t stream)
 {
     MatOperand o = operand(v);
     o.extent = kKRows ? v.ld : v.rows;
     o.krows = v.rows;
-    const ProductShape sh = shape_of(k, out.both);
-    with_tile(symmetric_tile(count, side), [&](auto t) {
+    ProductShape sh = shape_of(k, out.both);
+    sh.splits = plan.splits;
+    with_tile(plan.tile, [&](auto t) {
         constexpr int T = decltype(t)::value;
         Tiles tiles{};
         tiles.per_matrix = uint32_t(triangle_tiles(side, T));
-        hipLaunchKernelGGL((symmetric_kernel<kKRows, kSquare, T>), dim3(unsigned(tiles.per_matrix * count)),
+        tiles.slab = slab;
+        const size_t all = tiles.per_matrix * count;
+        hipLaunchKernelGGL((symmetric_kernel<kKRows, kSquare, T>), dim3(unsigned(all * plan.splits)),
                            dim3(Waves<T>::threads), 0, stream, o, v.matrix_stride, sh, tiles, out);
+        if (plan.splits > 1)
+            hipLaunchKernelGGL(join_kernel<T>, dim3(unsigned(all * (T / 32) * (T / 32))), dim3(kThreads), 0, stream,
+                               reinterpret_cast<const f32x4*>(slab), plan.splits, tiles, out);
     });
 }
 
@@ -844,7 +967,7 @@ void launch_update(const Layout& L, size_t count, const UpdateOut& out, const La
     X.krows = out.from.rows;
     P.extent = L.P.rows;
     const ProductShape sh = shape_of(L.P.ld, L.both);
-    with_tile(update_tile(count, L.m, L.n), [&](auto t) {
+    with_tile(L.update.tile, [&](auto t) {
         constexpr int T = decltype(t)::value;
         Tiles tiles{};
         tiles.a = uint32_t(ceil_div(L.n, T));
@@ -870,11 +993,12 @@ void iterate(const Layout& L, size_t count, const float* coefficients, int steps
     for (int s = 0; s < steps; ++s) {
         const float a = coefficients[3 * s], b = coefficients[3 * s + 1], c = coefficients[3 * s + 2];
         const Held &from = L.x[s & 1], &to = L.x[(s + 1) & 1];
-        launch_symmetric<kTall, false>(from, L.small, kTall ? from.rows : from.ld, count,
-                                       SymmetricOut{L.A, L.both, 0.0f, 0.0f, nullptr, of_a}, stream);
+        launch_symmetric<kTall, false>(from, L.gram, L.small, kTall ? from.rows : from.ld, count,
+                                       SymmetricOut{L.A, L.both, 0.0f, 0.0f, nullptr, of_a},
+                                       reinterpret_cast<float*>(ws + L.slab), stream);
         if (c != 0.0f) {
-            launch_symmetric<false, true>(L.A, L.small, L.A.ld, count, SymmetricOut{L.P, L.both, b, c, of_a, of_p},
-                                          stream);
+            launch_symmetric<false, true>(L.A, L.square, L.small, L.A.ld, count,
+                                          SymmetricOut{L.P, L.both, b, c, of_a, of_p}, nullptr, stream);
         } else {
             const size_t chunks = L.A.plane_stride / 8;
             hipLaunchKernelGGL(scale_kernel, dim3(unsigned(std::min<size_t>(ceil_div(chunks, kThreads), 2048))),
@@ -997,7 +1121,7 @@ void launch_first(const Call& c, const Layout& L, const In& in, hipStream_t stre
         x.p[k] = static_cast<const T*>(in.x.p[k]);
     hipLaunchKernelGGL((norm_kernel<T, kMomentum>), dim3(L.nparts, unsigned(c.count)), dim3(kThreads), 0, stream, x,
                        in.momenta, in.new_momenta, in.mo, c.m * c.n, parts, reinterpret_cast<u32x4*>(ws + L.zero),
-                       leaves_padding(L, c.count) ? L.zeros / 16 : 0);
+                       L.zeros / 16);
     const size_t chunks = L.x[0].matrix_stride / 8;
     hipLaunchKernelGGL((first_kernel<T, kMomentum>),
                        dim3(unsigned(std::min<size_t>(ceil_div(chunks, kThreads * 4), kMaxParts)), unsigned(c.count)),

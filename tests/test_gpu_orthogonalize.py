@@ -147,7 +147,8 @@ def test_series(gcq, series, shape, t):
 
 # (larger tiles, ragged edges of theirs, more rounds than one of the chip)
 @pytest.mark.parametrize("shape", [(16, 1000, 1100), (16, 1100, 1000), (40, 700, 513), (12, 520, 1500), (64, 300, 290),
-                                   (1, 300, 20000), (1, 20000, 300)], ids=str)
+                                   (1, 300, 20000), (1, 20000, 300), (2, 130, 9000), (1, 16384, 256), (1, 520, 5003),
+                                   (1, 1500, 2600)], ids=str)
 @pytest.mark.parametrize("t", [F32, BF16], ids=str)
 def test_many_tiles(gcq, shape, t):
     announce(f"orthogonalize {shape} {t}")
