@@ -301,10 +301,19 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void layer_norm_grad_ker
 
 // ---- host side --------------------------------------------------------------------
 
-// Waves of one forward launch, each with a contiguous range of rows.
-constexpr size_t kForwardWaves = 256 * 8;
+// Teams of one forward launch, each with a contiguous range of rows: 64 waves a
+// compute unit in all, twice what it holds, so that some start while others end.
+// 16384 x 4096 bf16: 52.0 us, against 58.4, 60.3 and 56.2 with 8, 16 and 32 and 54.5
+// with 128; 4096 x 8192 with dropout 57.6 (65.7, 58.5, 59.1, 61.4). Teams of 16 waves
+// do with 32: 4096 x 12288 68.9 (118 with 8, 67.1 with 16, 76.2 with 64).
+constexpr size_t forward_teams(int team)
+{
+    return 256 * (team == 1024 ? 32 : 64) / (team / kWave);
+}
 
-// Strips of the backward launch, each of which leaves a partial row.
+// Strips of the backward launch, each of which leaves a partial row. With 1024 (512
+// for teams of several waves) 16384 x 4096 bf16 takes 88.9 us instead of 83.2 and
+// 4095 x 1001 fp32 34.4 instead of 24.6; with 256, the latter 26.6.
 constexpr size_t kWaveStrips = 512, kTeamStrips = 256;
 
 // At least four rows a strip.
@@ -384,7 +393,7 @@ GCQ_API int layer_norm(const void* x, const void* y, int dtype, size_t rows, siz
         with_team<T>(d, [&](auto team, auto vecs) {
             constexpr int kTeam = decltype(team)::value, kVecs = decltype(vecs)::value;
             constexpr int kWg = kTeam < 256 ? 256 : kTeam;
-            const size_t teams = std::min(rows, kForwardWaves / (kTeam / kWave));
+            const size_t teams = std::min(rows, forward_teams(kTeam));
             const dim3 grid(unsigned(ceil_div(teams, kWg / kTeam)));
             const auto launch = [&](auto kernel) {
                 hipLaunchKernelGGL(kernel, grid, dim3(kWg), 0, stream, static_cast<const T*>(x),
