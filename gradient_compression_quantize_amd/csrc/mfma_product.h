@@ -94,13 +94,17 @@ inline void set_pairs(ProductShape& sh, int planes_a, int planes_b)
 
 // What one lane and wave move of an operand's stage, T rows (or columns) wide.
 // kPlain: every row of every stage of an operand by k may be read (else the last
-// one that may be stands for those behind it).
-template <bool kKRows, int T, int kWaves, bool kPlain = false>
+// one that may be stands for those behind it). kPaired (of kPlain): rows hold 16
+// values of the first plane, then those of the second, and so on, and a stage is 16
+// values of k of both.
+template <bool kKRows, int T, int kWaves, bool kPlain = false, bool kPaired = false>
 struct StageLoader {
+    static_assert(kPlain || !kPaired, "paired planes are plain");
     static constexpr int kLoads = T / 16 / kWaves;  // 1 KB wave loads
     static_assert(kLoads >= 1, "every wave moves at least one load");
-    static constexpr int kChunks = T / 8;                // by k: 16-byte chunks of a row
-    static constexpr int kRowsPerLoad = 1024 / (2 * T);  // by k
+    static constexpr int kWidth = kPaired ? 2 * T : T;        // by k: values of a row
+    static constexpr int kChunks = kWidth / 8;                // its 16-byte chunks
+    static constexpr int kRowsPerLoad = 1024 / (2 * kWidth);
     static constexpr bool kClamped = kKRows && !kPlain;
     // byte offset of each load: by rows from the tile's first row, by k from
     // the stage's first row (clamped: of its columns alone)
@@ -116,21 +120,21 @@ struct StageLoader {
     // covering 32 banks alone left it at half of SQ_LDS_IDX_ACTIVE.
     static __device__ __forceinline__ uint32_t swizzle(uint32_t row)
     {
-        return kKRows ? 4 * (row & (T >= 128 ? 3 : 1)) : (row >> 2) & 3;
+        return kKRows ? 4 * (row & (kWidth >= 128 ? 3 : 1)) : (row >> 2) & 3;
     }
 
     __device__ __forceinline__ void init(const MatOperand& m, uint32_t first, int wave_, int lane)
     {
         wave = wave_;
         origin = kKRows ? 0 : size_t(first) * m.ld;
-        step = 2 * kStageK * (kKRows ? m.ld : 1);
+        step = 2 * kStageK * (kKRows ? m.ld / (kPaired ? 2 : 1) : 1);
         row = wave * kLoads * kRowsPerLoad + lane / kChunks;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             if (kKRows) {
-                const uint32_t chunk = (lane % kChunks) ^ swizzle(row + j * kRowsPerLoad);
-                off[j] = min(first + chunk * 8, m.extent - 8) * 2 +
-                         (kClamped ? 0 : __umul24(row + j * kRowsPerLoad, m.ld * 2));
+                const uint32_t r = row + j * kRowsPerLoad, chunk = (lane % kChunks) ^ swizzle(r);
+                constexpr uint32_t kOf = kPaired ? 2 : 1;
+                off[j] = min(kOf * first + chunk * 8, kOf * m.extent - 8) * 2 + (kClamped ? 0 : __umul24(r, m.ld * 2));
             } else {
                 const uint32_t r = (wave * kLoads + j) * 16 + lane / 4;
                 const uint32_t chunk = (lane & 3) ^ swizzle(r);
@@ -143,7 +147,7 @@ struct StageLoader {
     // The turn from k0 on of plane p.
     __device__ __forceinline__ const uint16_t* turn(const MatOperand& m, const uint16_t* p, uint32_t k0) const
     {
-        return p + (kKRows ? size_t(k0) * m.ld : origin + k0);
+        return p + (kKRows ? size_t(k0) * m.ld : origin + (kPaired ? 2 * k0 : k0));
     }
 
     // A descriptor of `bytes` bytes from p on: of none, its loads fetch nothing.
@@ -173,8 +177,11 @@ struct StageLoader {
 
 // Fragments of 32 rows (or columns) x 16 k: lane l holds row l % 32, k values
 // 8 (l / 32) .. + 7.
-template <bool kKRows, int T>
+template <bool kKRows, int T, bool kPaired = false>
 struct FragmentReader {
+    using Stage = StageLoader<kKRows, T, 1, kPaired, kPaired>;
+    static constexpr int kRow = 2 * Stage::kWidth;  // by k: bytes of a row
+
     uint32_t base;  // byte offset of this lane at fragment 0, k 0
 
     __device__ __forceinline__ void init(uint32_t first, int lane)
@@ -182,27 +189,28 @@ struct FragmentReader {
         if (kKRows) {
             const uint32_t g = lane >> 4, j = lane & 15;
             const uint32_t row = 8 * (g >> 1) + (j >> 2);
-            const uint32_t col = first + 16 * (g & 1) + 4 * (j & 3);
-            base = row * (2 * T) + (((col >> 3) ^ StageLoader<true, T, 1>::swizzle(row)) << 4) + ((col & 4) << 1);
+            const uint32_t col = (first + 16 * (g & 1)) * (kPaired ? 2 : 1) + 4 * (j & 3);
+            base = row * kRow + (((col >> 3) ^ Stage::swizzle(row)) << 4) + ((col & 4) << 1);
         } else {
             const uint32_t row = first + (lane & 31);
-            base = row * (2 * kStageK) + (((lane >> 5) ^ StageLoader<false, T, 1>::swizzle(row)) << 4);
+            base = row * (2 * kStageK) + (((lane >> 5) ^ Stage::swizzle(row)) << 4);
         }
     }
 
-    // Fragment f (32 f rows on), k values 16 kk on.
+    // Fragment f (32 f rows on), k values 16 kk on (kPaired: plane kk).
     __device__ __forceinline__ s16x8 read(const uint16_t* lds, int f, int kk) const
     {
         if (kKRows) {
             typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-            // 4 f chunks on: the XOR reaches bits 2 and 3 of the chunk, which 4 f meets too
-            const char* p = reinterpret_cast<const char*>(lds) + (base ^ (uint32_t(f) << 6)) + kk * 16 * (2 * T);
+            // 4 f chunks on (8 f): the XOR reaches bits 2 and 3 of the chunk, which 4 f meets too
+            const char* p = reinterpret_cast<const char*>(lds) + (base ^ (uint32_t(f) << (kPaired ? 7 : 6))) +
+                            kk * (kPaired ? 32 : 16 * kRow);
             union {
                 s16x4 h[2];
                 s16x8 v;
             } u;
             u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p));
-            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * (2 * T)));
+            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * kRow));
             return u.v;
         }
         const char* p = reinterpret_cast<const char*>(lds) + (base ^ (uint32_t(kk) << 5)) + f * (32 * 2 * kStageK);
@@ -224,13 +232,18 @@ struct TileBuffers {
                               {name##_b0, name##_b1, name##_b2, name##_b3}}
 
 // kF16: fp16 operands, else bf16. kPlain: as of StageLoader, and planes that add
-// up as they are: no sum of segments is scaled.
-template <bool kF16, bool kAK, bool kBK, int TA, int TB, int WA, int WB, bool kPlain = false>
+// up as they are: no sum of segments is scaled. kPaired: of two such planes in both
+// operands all pairs but that of two second ones, as one segment: its turns are
+// of kTurnK / 2 values of k, whose planes are fetched and read out of LDS once for
+// all three products: 512 tiles of 128 x 128 over 2048 k in 116 us, 145 as three
+// segments; 256 of 256 x 256 in 181 and 191.
+template <bool kF16, bool kAK, bool kBK, int TA, int TB, int WA, int WB, bool kPlain = false, bool kPaired = false>
 struct TileProduct {
     static constexpr int kWaves = WA * WB;
     static constexpr int RA = TA / WA / 32, RB = TB / WB / 32;  // 32 x 32 products of a wave
-    using LoadA = StageLoader<kAK, TA, kWaves, kPlain>;
-    using LoadB = StageLoader<kBK, TB, kWaves, kPlain>;
+    using LoadA = StageLoader<kAK, TA, kWaves, kPlain, kPaired>;
+    using LoadB = StageLoader<kBK, TB, kWaves, kPlain, kPaired>;
+    static constexpr int kOfTurn = kPaired ? kTurnK / 2 : kTurnK;
 
     struct Acc {
         f32x16 v[RA][RB];
@@ -249,8 +262,8 @@ struct TileProduct {
         LoadB gb;
         ga.init(A, a0, wave, lane);
         gb.init(B, b0, wave, lane);
-        FragmentReader<kAK, TA> fa;
-        FragmentReader<kBK, TB> fb;
+        FragmentReader<kAK, TA, kPaired> fa;
+        FragmentReader<kBK, TB, kPaired> fb;
         fa.init(wa * (TA / WA), lane);
         fb.init(wb * (TB / WB), lane);
 #pragma unroll
@@ -265,8 +278,8 @@ struct TileProduct {
         // are left. Set once a turn: scalar instructions of every stage are
         // what all waves go through behind its barrier before their first
         // product.
-        const uint32_t k_end = sh.turns * kTurnK;
-        uint32_t seg = t0 / sh.turns, k0 = (t0 - seg * sh.turns) * kTurnK, left = t1 - t0;
+        const uint32_t k_end = sh.turns * kOfTurn;
+        uint32_t seg = t0 / sh.turns, k0 = (t0 - seg * sh.turns) * kOfTurn, left = t1 - t0;
         struct Fetch {
             __amdgpu_buffer_rsrc_t a, b;
             const uint16_t *pa, *pb;
@@ -284,7 +297,7 @@ struct TileProduct {
             f.a = LoadA::view(f.pa, f.bytes);
             f.b = LoadB::view(f.pb, f.bytes);
             left -= f.bytes & 1;
-            k0 += kTurnK;
+            k0 += kOfTurn;
             const uint32_t over = __builtin_amdgcn_readfirstlane(k0 == k_end ? 1u : 0u);
             seg += over;
             k0 -= over * k_end;
@@ -305,6 +318,52 @@ struct TileProduct {
             for (int j = 0; j < kLoads; ++j)
                 load(f, s, j);
         wait_loads<2 * kLoads>();
+        if constexpr (kPaired) {
+            // Fragments of a second plane come in under the products of the two
+            // first ones, those of the next stage's first planes under the third
+            // products (b's beside those in use).
+            s16x8 a[2][RA], b[3][RB];
+#pragma unroll
+            for (int j = 0; j < RB; ++j)
+                b[0][j] = fb.read(lds.b[0], j, 0);
+#pragma unroll
+            for (int i = 0; i < RA; ++i)
+                a[0][i] = fa.read(lds.a[0], i, 0);
+            for (uint32_t t = t0; t < t1; ++t) {
+#pragma unroll
+                for (int s = 0; s < kBuffers; ++s) {
+                    wait_loads<kLoads>();
+                    constexpr int kSteps = 3 * (RA > RB ? RA : RB), kEach = (kLoads + kSteps - 1) / kSteps;
+                    const int now = s & 1, next = now ^ 1, to = (s + 1) % kBuffers;
+#pragma unroll
+                    for (int phase = 0; phase < 3; ++phase)
+#pragma unroll
+                        for (int i = 0; i < (RA > RB ? RA : RB); ++i) {
+                            if (phase == 0 && i < RB)
+                                b[2][i] = fb.read(lds.b[s], i, 1);
+                            if (phase == 0 && i < RA)
+                                a[1][i] = fa.read(lds.a[s], i, 1);
+                            if (phase == 2 && i < RB)
+                                b[next][i] = fb.read(lds.b[to], i, 0);
+                            if (phase == 2 && i < RA)
+                                a[0][i] = fa.read(lds.a[to], i, 0);
+#pragma unroll
+                            for (int e = 0; e < kEach; ++e)
+                                load(f, (s + kBuffers - 1) % kBuffers, (phase * (RA > RB ? RA : RB) + i) * kEach + e);
+                            if (i < RA) {
+#pragma unroll
+                                for (int j = 0; j < RB; ++j)
+                                    acc.v[i][j] = multiply(a[phase == 2 ? 1 : 0][i], b[phase == 1 ? 2 : now][j], acc.v[i][j]);
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    if (s == 0)
+                        f = next_turn();
+                }
+            }
+            wait_loads<0>();
+            return;
+        }
         s16x8 a[2][RA], b[2][RB];
 #pragma unroll
         for (int j = 0; j < RB; ++j)

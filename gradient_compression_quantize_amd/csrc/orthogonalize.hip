@@ -172,24 +172,30 @@ __device__ __forceinline__ f32x8 join8(Planes8 s)
 __device__ __forceinline__ f16x8 load_plane(const uint16_t* p) { return *reinterpret_cast<const f16x8*>(p); }
 __device__ __forceinline__ void store_plane(uint16_t* p, f16x8 v) { *reinterpret_cast<f16x8*>(p) = v; }
 
-// A matrix of the workspace, of each of `count`: [rows][ld], two planes of all
-// of them one behind the other.
+// A matrix of the workspace, of each of `count`: `rows` rows of ld values, which
+// hold `cols` values of the first plane, then those of the second if there is one
+// - or, where products read both, 16 of one and 16 of the other in turn.
 struct Held {
-    uint16_t* plane0;
-    size_t plane_stride, matrix_stride;
-    uint32_t ld, rows;
+    uint16_t* p;
+    size_t matrix_stride;
+    uint32_t ld, rows, cols;
 };
 
-__device__ __forceinline__ uint16_t* held_at(const Held& h, size_t matrix, int plane)
+__device__ __forceinline__ uint16_t* held_at(const Held& h, size_t matrix) { return h.p + matrix * h.matrix_stride; }
+
+// Where the value of a plane in column c is in its row (those up to the next
+// multiple of 16 follow it).
+__device__ __forceinline__ size_t held_in_row(const Held& h, bool both, uint32_t c, int plane)
 {
-    return h.plane0 + plane * h.plane_stride + matrix * h.matrix_stride;
+    return both ? size_t(c & ~15u) * 2 + plane * 16 + (c & 15) : size_t(plane) * h.cols + c;
 }
 
 // X_0 of each matrix, zeros behind its last row and column.
 template <typename T, bool kMomentum>
 __global__ __launch_bounds__(kThreads) void first_kernel(PtrTable<T> x, PtrTable<float> new_momenta, Momentum mo,
                                                          size_t m, size_t n, float eps,
-                                                         const double* __restrict__ parts, uint32_t nparts, Held to)
+                                                         const double* __restrict__ parts, uint32_t nparts, Held to,
+                                                         bool both)
 {
     const size_t k = blockIdx.y;
     double sum = 0.0;
@@ -197,7 +203,7 @@ __global__ __launch_bounds__(kThreads) void first_kernel(PtrTable<T> x, PtrTable
         sum += parts[k * nparts + i];
     sum = workgroup_sum(sum);
     const double factor = double(pow2<kXExp>) / (sqrt(sum) + double(eps));
-    const uint32_t chunks = to.ld / 8;
+    const uint32_t chunks = to.cols / 8;
     const size_t total = size_t(to.rows) * chunks;
     for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < total; i += size_t(gridDim.x) * kThreads) {
         const size_t r = i / chunks, c = (i - r * chunks) * 8;
@@ -216,9 +222,9 @@ __global__ __launch_bounds__(kThreads) void first_kernel(PtrTable<T> x, PtrTable
                 v[e] = float(double(v[e]) * factor);
         }
         const Planes8 s = split8(v);
-        uint16_t* o = held_at(to, k, 0) + r * to.ld + c;
-        store_plane(o, s.p0);
-        store_plane(o + to.plane_stride, s.p1);
+        uint16_t* o = held_at(to, k) + r * to.ld;
+        store_plane(o + held_in_row(to, both, uint32_t(c), 0), s.p0);
+        store_plane(o + held_in_row(to, both, uint32_t(c), 1), s.p1);
     }
 }
 
@@ -344,19 +350,18 @@ struct PartPlanes : Part<T> {
         return buffer + plane * kPlane + row * kCols + (((col >> 3) ^ (row & (kChunks - 1))) << 3) + (col & 7);
     }
 
-    // The 32 rows of a matrix of `rows` x `cols` from row b0 on into the image.
-    __device__ __forceinline__ void bring(const uint16_t* plane0, size_t plane_stride, uint32_t ld, int planes,
-                                          uint32_t b0, uint32_t rows, uint32_t cols) const
+    // The 32 rows of a matrix from row b0 on into the image, as far as they exist.
+    __device__ __forceinline__ void bring(const uint16_t* matrix, const Held& h, bool both, int planes, uint32_t b0) const
     {
         const uint32_t a = this->a + col();
         for (int plane = 0; plane < planes; ++plane) {
-            const uint16_t* from = plane0 + plane * plane_stride + a;
+            const uint16_t* from = matrix + held_in_row(h, both, a, plane);
             f16x8 v[kPasses];
 #pragma unroll
             for (int p = 0; p < kPasses; ++p) {
                 v[p] = f16x8{};
-                if (a < cols && b0 + row(p) < rows)
-                    v[p] = load_plane(from + size_t(b0 + row(p)) * ld);
+                if (a < h.cols && b0 + row(p) < h.rows)
+                    v[p] = load_plane(from + size_t(b0 + row(p)) * h.ld);
             }
 #pragma unroll
             for (int p = 0; p < kPasses; ++p)
@@ -366,17 +371,16 @@ struct PartPlanes : Part<T> {
     }
 
     // The image into those rows.
-    __device__ __forceinline__ void leave(uint16_t* plane0, size_t plane_stride, uint32_t ld, int planes, uint32_t b0,
-                                          uint32_t rows, uint32_t cols) const
+    __device__ __forceinline__ void leave(uint16_t* matrix, const Held& h, bool both, int planes, uint32_t b0) const
     {
         const uint32_t a = this->a + col();
         for (int plane = 0; plane < planes; ++plane) {
-            uint16_t* to = plane0 + plane * plane_stride + a;
+            uint16_t* to = matrix + held_in_row(h, both, a, plane);
 #pragma unroll
             for (int p = 0; p < kPasses; ++p) {
                 const f16x8 v = *eight(plane, p);
-                if (a < cols && b0 + row(p) < rows)
-                    store_plane(to + size_t(b0 + row(p)) * ld, v);
+                if (a < h.cols && b0 + row(p) < h.rows)
+                    store_plane(to + size_t(b0 + row(p)) * h.ld, v);
             }
         }
     }
@@ -474,12 +478,12 @@ struct SymmetricOut {
     float* diagonal;
 };
 
-template <bool kKRows, bool kSquare, int T>
+template <bool kKRows, bool kSquare, int T, bool kBoth>
 __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOperand V, size_t matrix_stride,
                                                                          ProductShape sh, Tiles tiles, SymmetricOut out)
 {
     constexpr int WA = Waves<T>::a, WB = Waves<T>::b;
-    using P = TileProduct<true, kKRows, kKRows, T, T, WA, WB, true>;
+    using P = TileProduct<true, kKRows, kKRows, T, T, WA, WB, true, kBoth>;
     GCQ_TILE_BUFFERS(lds, T, T);
     const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), range = id / tiles.per_matrix;
     const uint32_t matrix = range / sh.splits, split = range - matrix * sh.splits;
@@ -510,18 +514,18 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
     }
     using Rows = PartPlanes<T>;
     const Rows part(lds, ta * T, tb * T);
-    uint16_t* to = held_at(out.to, matrix, 0);
+    uint16_t* to = held_at(out.to, matrix);
     const uint32_t side = out.to.rows;
     float* diagonal = out.diagonal + size_t(matrix) * side;
     const float* old = kSquare ? out.from_diagonal + size_t(matrix) * side : nullptr;
-    const int planes = out.both ? 2 : 1;
+    constexpr int planes = kBoth ? 2 : 1;
     __shared__ float of_columns[Columns<T>::kAll];
     const Columns<T> of_col(of_columns, old, part.a, kSquare ? side : 0);  // A's diagonal
 #pragma unroll
     for (int j = 0; j < P::RB; ++j) {
         const uint32_t b0 = part.b + j * 32, b = b0 + acc_col(part.lane);
-        if (kSquare)  // A's part of V
-            part.bring(V.plane0, V.plane_stride, V.ld, planes, b0, side, side);
+        if (kSquare)  // A's part of V, which lies as P does
+            part.bring(V.plane0, out.to, kBoth, planes, b0);
         const float db = kSquare && b < side ? old[b] : 0.0f;
 #pragma unroll
         for (int i = 0; i < P::RA; ++i) {
@@ -534,7 +538,7 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
             if (kSquare) {
                 const float own = (out.b + out.c * db) * pow2<kPExp - kAExp>, each = out.c * pow2<kPExp - kAExp>;
                 f32x4 A[4];
-                part.read(A, i, out.both);
+                part.read(A, i, kBoth);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const f32x4 da = of_col.quad(i, q);
@@ -555,13 +559,13 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
                             v[q][e] = 0.0f;
                         }
             }
-            part.write(v, i, out.both);
+            part.write(v, i, kBoth);
         }
         wave_lds_sync();
-        part.leave(to, out.to.plane_stride, out.to.ld, planes, b0, side, side);
+        part.leave(to, out.to, kBoth, planes, b0);
         if (ta != tb) {
             for (int plane = 0; plane < planes; ++plane) {
-                uint16_t* p = to + plane * out.to.plane_stride + b0 + part.turned_row();
+                uint16_t* p = to + held_in_row(out.to, kBoth, b0 + part.turned_row(), plane);
 #pragma unroll
                 for (int k = 0; k < Rows::kTurnedPasses; ++k) {
                     const uint32_t row = part.a + part.turned_col(k);
@@ -608,11 +612,11 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const f32x4* __restrict_
             v[e] = 0.0f;
         }
     const auto store = [&](uint32_t row, uint32_t col, f32x4 x) {
-        uint16_t* p = held_at(out.to, matrix, 0) + size_t(row) * out.to.ld + col;
+        uint16_t* p = held_at(out.to, matrix) + size_t(row) * out.to.ld;
         const f16x4 p0 = __builtin_convertvector(x, f16x4);
-        *reinterpret_cast<f16x4*>(p) = p0;
+        *reinterpret_cast<f16x4*>(p + held_in_row(out.to, out.both, col, 0)) = p0;
         if (out.both)
-            *reinterpret_cast<f16x4*>(p + out.to.plane_stride) =
+            *reinterpret_cast<f16x4*>(p + held_in_row(out.to, true, col, 1)) =
                 __builtin_convertvector(x - __builtin_convertvector(p0, f32x4), f16x4);
     };
     store(b0 + b, a0 + a, v);
@@ -626,23 +630,27 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const f32x4* __restrict_
     store(a0 + row, b0 + col, f32x4{turned[row][col], turned[row][col + 1], turned[row][col + 2], turned[row][col + 3]});
 }
 
-// P = b A of a step without a second power.
-__global__ __launch_bounds__(kThreads) void scale_kernel(Held A, Held P, bool both, float b, size_t chunks,
+// P = b A of a step without a second power; `rows` of all matrices.
+__global__ __launch_bounds__(kThreads) void scale_kernel(Held A, Held P, bool both, float b, size_t rows,
                                                          const float* __restrict__ from_diagonal,
-                                                         float* __restrict__ diagonal, size_t diagonals)
+                                                         float* __restrict__ diagonal)
 {
     const float f = b * pow2<kPExp - kAExp>;
-    for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < diagonals; i += size_t(gridDim.x) * kThreads)
-        diagonal[i] = b * from_diagonal[i];
-    for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < chunks; i += size_t(gridDim.x) * kThreads) {
+    const size_t chunks = A.cols / 8, all = rows * chunks;
+    for (size_t i = size_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += size_t(gridDim.x) * kThreads) {
+        const size_t row = i / chunks, c = i - row * chunks;
+        if (c == 0)
+            diagonal[row] = b * from_diagonal[row];
+        const size_t at0 = row * A.ld + held_in_row(A, both, uint32_t(c) * 8, 0);
+        const size_t at1 = row * A.ld + held_in_row(A, both, uint32_t(c) * 8, 1);
         Planes8 s = {};
-        s.p0 = load_plane(A.plane0 + i * 8);
+        s.p0 = load_plane(A.p + at0);
         if (both)
-            s.p1 = load_plane(A.plane0 + A.plane_stride + i * 8);
+            s.p1 = load_plane(A.p + at1);
         s = split8(join8(s) * f);
-        store_plane(P.plane0 + i * 8, s.p0);
+        store_plane(P.p + at0, s.p0);
         if (both)
-            store_plane(P.plane0 + P.plane_stride + i * 8, s.p1);
+            store_plane(P.p + at1, s.p1);
     }
 }
 
@@ -700,13 +708,13 @@ struct UpdateOut {
     uint32_t side;
 };
 
-template <bool kTall, bool kLast, int T>
+template <bool kTall, bool kLast, int T, bool kBoth>
 __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand A, size_t a_stride, MatOperand B,
                                                                       size_t b_stride, ProductShape sh, Tiles tiles,
                                                                       UpdateOut out, LastOut last)
 {
     constexpr int WA = Waves<T>::a, WB = Waves<T>::b;
-    using P = TileProduct<true, !kTall, false, T, T, WA, WB, true>;
+    using P = TileProduct<true, !kTall, false, T, T, WA, WB, true, kBoth>;
     GCQ_TILE_BUFFERS(lds, T, T);
     const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), matrix = id / tiles.per_matrix;
     uint32_t ta, tb;
@@ -717,9 +725,9 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
     P::run(A, B, sh, ta * T, tb * T, 0, sh.turns * sh.segments, lds, acc);
 
     const PartPlanes<T> part(lds, ta * T, tb * T);
-    const uint16_t* from = held_at(out.from, matrix, 0);
+    const uint16_t* from = held_at(out.from, matrix);
     const float* diagonal = out.diagonal + size_t(matrix) * out.side;
-    const uint32_t rows = out.from.rows, cols = out.from.ld;
+    const uint32_t rows = out.from.rows, cols = out.from.cols;
     __shared__ float of_columns[Columns<T>::kAll];
     const Columns<T> of_col(of_columns, diagonal, part.a, kTall ? cols : 0);
     const PartRows<T> whole(lds, ta * T, tb * T);
@@ -732,7 +740,7 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
 #pragma unroll
     for (int j = 0; j < P::RB; ++j) {
         const uint32_t b0 = part.b + j * 32, b = b0 + acc_col(part.lane);
-        part.bring(from, out.from.plane_stride, cols, 2, b0, rows, cols);
+        part.bring(from, out.from, kBoth, 2, b0);
         const float of_row = out.a + (!kTall && b < rows ? diagonal[b] : 0.0f);
 #pragma unroll
         for (int i = 0; i < P::RA; ++i) {
@@ -754,7 +762,7 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
         }
         wave_lds_sync();
         if (!kLast) {
-            part.leave(held_at(out.to, matrix, 0), out.to.plane_stride, cols, 2, b0, rows, cols);
+            part.leave(held_at(out.to, matrix), out.to, kBoth, 2, b0);
             wave_lds_sync();
             continue;
         }
@@ -782,13 +790,12 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
 size_t round_up(size_t a, size_t b) { return ceil_div(a, b) * b; }
 
 constexpr size_t kMaxSide = size_t(1) << 20, kMaxSmallSide = size_t(1) << 15, kMaxTiles = size_t(1) << 22;
-void place(Held& h, char* ws) { h.plane0 = reinterpret_cast<uint16_t*>(ws + reinterpret_cast<size_t>(h.plane0)); }
+void place(Held& h, char* ws) { h.p = reinterpret_cast<uint16_t*>(ws + reinterpret_cast<size_t>(h.p)); }
 
 MatOperand operand(const Held& h)
 {
     MatOperand o{};
-    o.plane0 = h.plane0;
-    o.plane_stride = h.plane_stride;
+    o.plane0 = h.p;
     o.ld = h.ld;
     return o;
 }
@@ -849,25 +856,34 @@ Plan plan_of(size_t count, size_t turns, bool may_split, Tiles tiles)
     return best;
 }
 
-size_t turns_of(size_t k, bool both) { return k / kTurnK * (both ? 3 : 1); }
+// Turns of one plane that cost as much: of two, three products of what is fetched
+// twice.
+size_t turns_of(size_t k, bool both) { return k / kTurnK * (both ? 5 : 2) / 2; }
 
-// Calls f with the tile as an integral constant.
+// Calls f with the tile, and whether products are of both planes, as integral
+// constants.
 template <typename F>
-void with_tile(int tile, F f)
+void with_tile(int tile, bool both, F f)
 {
+    const auto with = [&](auto t) {
+        if (both)
+            f(t, std::true_type());
+        else
+            f(t, std::false_type());
+    };
     if (tile == 256)
-        f(std::integral_constant<int, 256>());
+        with(std::integral_constant<int, 256>());
     else if (tile == 128)
-        f(std::integral_constant<int, 128>());
+        with(std::integral_constant<int, 128>());
     else
-        f(std::integral_constant<int, 64>());
+        with(std::integral_constant<int, 64>());
 }
 
 ProductShape shape_of(size_t k, bool both)
 {
     ProductShape sh{};
-    sh.turns = uint32_t(k / kTurnK);
-    set_pairs(sh, both ? 2 : 1, both ? 2 : 1);
+    sh.turns = uint32_t(k / (both ? kTurnK / 2 : kTurnK));
+    sh.segments = 1;
     sh.splits = 1;
     return sh;
 }
@@ -878,7 +894,7 @@ struct Layout {
     bool resident;          // one workgroup a matrix, without a workspace
     Plan gram, square, update;
     size_t slab;            // of gram's ranges
-    Held x[2], A, P;        // their plane0: an offset into the workspace
+    Held x[2], A, P;        // their p: an offset into the workspace
     size_t parts, diagonals[2], zero, zeros, total;  // bytes; diagonals of A and P
     uint32_t nparts;
 };
@@ -901,13 +917,13 @@ Layout layout_of(size_t count, size_t m, size_t n, bool both)
         used += (bytes + 255) & ~size_t(255);
         return at;
     };
-    const auto hold = [&](size_t r, size_t ld, int planes) {
+    const auto hold = [&](size_t r, size_t cols, int planes) {
         Held h{};
-        h.matrix_stride = r * ld;
-        h.plane_stride = count * r * ld;
-        h.ld = uint32_t(ld);
+        h.matrix_stride = r * cols * planes;
+        h.ld = uint32_t(cols * planes);
+        h.cols = uint32_t(cols);
         h.rows = uint32_t(r);
-        h.plane0 = reinterpret_cast<uint16_t*>(take(planes * h.plane_stride * 2));
+        h.p = reinterpret_cast<uint16_t*>(take(count * h.matrix_stride * 2));
         return h;
     };
     L.nparts = uint32_t(std::min<size_t>(kMaxParts, ceil_div(m * n, kThreads * 8 * 4)));
@@ -941,17 +957,17 @@ void launch_symmetric(const Held& v, const Plan& plan, size_t side, size_t k, si
                       float* slab, hipStream_t stream)
 {
     MatOperand o = operand(v);
-    o.extent = kKRows ? v.ld : v.rows;
+    o.extent = kKRows ? v.cols : v.rows;
     o.krows = v.rows;
     ProductShape sh = shape_of(k, out.both);
     sh.splits = plan.splits;
-    with_tile(plan.tile, [&](auto t) {
+    with_tile(plan.tile, out.both, [&](auto t, auto both) {
         constexpr int T = decltype(t)::value;
         Tiles tiles{};
         tiles.per_matrix = uint32_t(triangle_tiles(side, T));
         tiles.slab = slab;
         const size_t all = tiles.per_matrix * count;
-        hipLaunchKernelGGL((symmetric_kernel<kKRows, kSquare, T>), dim3(unsigned(all * plan.splits)),
+        hipLaunchKernelGGL((symmetric_kernel<kKRows, kSquare, T, decltype(both)::value>), dim3(unsigned(all * plan.splits)),
                            dim3(Waves<T>::threads), 0, stream, o, v.matrix_stride, sh, tiles, out);
         if (plan.splits > 1)
             hipLaunchKernelGGL(join_kernel<T>, dim3(unsigned(all * (T / 32) * (T / 32))), dim3(kThreads), 0, stream,
@@ -963,22 +979,23 @@ template <bool kTall, bool kLast>
 void launch_update(const Layout& L, size_t count, const UpdateOut& out, const LastOut& last, hipStream_t stream)
 {
     MatOperand X = operand(out.from), P = operand(L.P);
-    X.extent = kTall ? out.from.rows : out.from.ld;
+    X.extent = kTall ? out.from.rows : out.from.cols;
     X.krows = out.from.rows;
     P.extent = L.P.rows;
-    const ProductShape sh = shape_of(L.P.ld, L.both);
-    with_tile(L.update.tile, [&](auto t) {
+    const ProductShape sh = shape_of(L.P.cols, L.both);
+    with_tile(L.update.tile, L.both, [&](auto t, auto both) {
         constexpr int T = decltype(t)::value;
+        constexpr bool kBoth = decltype(both)::value;
         Tiles tiles{};
         tiles.a = uint32_t(ceil_div(L.n, T));
         tiles.b = uint32_t(ceil_div(L.m, T));
         tiles.per_matrix = tiles.a * tiles.b;
         const dim3 grid(unsigned(tiles.per_matrix * count));
         if (kTall)
-            hipLaunchKernelGGL((update_kernel<kTall, kLast, T>), grid, dim3(Waves<T>::threads), 0, stream, P,
+            hipLaunchKernelGGL((update_kernel<kTall, kLast, T, kBoth>), grid, dim3(Waves<T>::threads), 0, stream, P,
                                L.P.matrix_stride, X, out.from.matrix_stride, sh, tiles, out, last);
         else
-            hipLaunchKernelGGL((update_kernel<kTall, kLast, T>), grid, dim3(Waves<T>::threads), 0, stream, X,
+            hipLaunchKernelGGL((update_kernel<kTall, kLast, T, kBoth>), grid, dim3(Waves<T>::threads), 0, stream, X,
                                out.from.matrix_stride, P, L.P.matrix_stride, sh, tiles, out, last);
     });
 }
@@ -993,17 +1010,16 @@ void iterate(const Layout& L, size_t count, const float* coefficients, int steps
     for (int s = 0; s < steps; ++s) {
         const float a = coefficients[3 * s], b = coefficients[3 * s + 1], c = coefficients[3 * s + 2];
         const Held &from = L.x[s & 1], &to = L.x[(s + 1) & 1];
-        launch_symmetric<kTall, false>(from, L.gram, L.small, kTall ? from.rows : from.ld, count,
+        launch_symmetric<kTall, false>(from, L.gram, L.small, kTall ? from.rows : from.cols, count,
                                        SymmetricOut{L.A, L.both, 0.0f, 0.0f, nullptr, of_a},
                                        reinterpret_cast<float*>(ws + L.slab), stream);
         if (c != 0.0f) {
-            launch_symmetric<false, true>(L.A, L.square, L.small, L.A.ld, count,
+            launch_symmetric<false, true>(L.A, L.square, L.small, L.A.cols, count,
                                           SymmetricOut{L.P, L.both, b, c, of_a, of_p}, nullptr, stream);
         } else {
-            const size_t chunks = L.A.plane_stride / 8;
-            hipLaunchKernelGGL(scale_kernel, dim3(unsigned(std::min<size_t>(ceil_div(chunks, kThreads), 2048))),
-                               dim3(kThreads), 0, stream, L.A, L.P, L.both, b, chunks, of_a, of_p,
-                               count * L.A.rows);
+            const size_t rows = count * L.A.rows;
+            hipLaunchKernelGGL(scale_kernel, dim3(unsigned(std::min<size_t>(ceil_div(rows * L.A.cols / 8, kThreads), 2048))),
+                               dim3(kThreads), 0, stream, L.A, L.P, L.both, b, rows, of_a, of_p);
         }
         if (s + 1 < steps)
             launch_update<kTall, false>(L, count, UpdateOut{from, to, a, of_p, L.P.rows}, last, stream);
@@ -1125,7 +1141,7 @@ void launch_first(const Call& c, const Layout& L, const In& in, hipStream_t stre
     const size_t chunks = L.x[0].matrix_stride / 8;
     hipLaunchKernelGGL((first_kernel<T, kMomentum>),
                        dim3(unsigned(std::min<size_t>(ceil_div(chunks, kThreads * 4), kMaxParts)), unsigned(c.count)),
-                       dim3(kThreads), 0, stream, x, in.new_momenta, in.mo, c.m, c.n, c.eps, parts, L.nparts, L.x[0]);
+                       dim3(kThreads), 0, stream, x, in.new_momenta, in.mo, c.m, c.n, c.eps, parts, L.nparts, L.x[0], L.both);
 }
 
 int run_call(const Call& c, const Layout& L, const In& in, const LastOut& last, hipStream_t stream)
