@@ -833,19 +833,23 @@ double tiles_cost(int T, double tiles, double turns)
     return rounds * (turns * turn + end);
 }
 
-// Of the tiles of 256, 128 and 64, and of 1, 2, 4 .. ranges of at least four
-// turns each, what costs least: several ranges leave their sums in memory
-// (written and read at some 4 TB/s) for another launch (5 us). 64 x 16384, one
-// tile of 128 turns, takes XXX us in one range.
+// Of the tiles of 256, 128 and 64, and of 1, 2, 4 .. ranges of at least four turns
+// each, what costs least. A turn of both planes is as long as 2.6 of one with
+// tiles of 256, 2.3 with smaller ones. Several ranges leave their sums in memory
+// (written and read at some 4 TB/s) for another launch (5 us): all five steps of 64
+// x 16384 take 100 us with 32 ranges, 445 with one, of 256 x 2304 112 and 146. With
+// tiles of one size alone: 4096 x 4096 1.53 ms with 256, 1.90 with 128, 2.93 with
+// 64; 768 x 768 383, 201 and 139 us; 48 of them 1054, 961 and 1159.
 template <typename Tiles>
-Plan plan_of(size_t count, size_t turns, bool may_split, Tiles tiles)
+Plan plan_of(size_t count, size_t k, bool both, bool may_split, Tiles tiles)
 {
     Plan best{};
     double least = 0.0;
+    const size_t turns = k / kTurnK * (both ? 2 : 1);
     for (int T = 256; T >= 64; T /= 2) {
-        const double n = double(count * tiles(T));
+        const double n = double(count * tiles(T)), turn = both ? (T == 256 ? 1.3 : 1.15) : 1.0;
         for (uint32_t s = 1; s == 1 || (may_split && s * 4 <= turns && n * s <= 1024.0); s *= 2) {
-            const double t = tiles_cost(T, n * s, double(ceil_div(turns, s))) +
+            const double t = tiles_cost(T, n * s, double(ceil_div(turns, s)) * turn) +
                              (s > 1 ? 5.0 + n * s * T * T * 8.0 / 4e6 : 0.0);
             if (best.tile == 0 || t < least) {
                 best = Plan{T, s};
@@ -855,10 +859,6 @@ Plan plan_of(size_t count, size_t turns, bool may_split, Tiles tiles)
     }
     return best;
 }
-
-// Turns of one plane that cost as much: of two, three products of what is fetched
-// twice.
-size_t turns_of(size_t k, bool both) { return k / kTurnK * (both ? 5 : 2) / 2; }
 
 // Calls f with the tile, and whether products are of both planes, as integral
 // constants.
@@ -936,9 +936,9 @@ Layout layout_of(size_t count, size_t m, size_t n, bool both)
     L.diagonals[0] = take(count * side * sizeof(float));
     L.diagonals[1] = take(count * side * sizeof(float));
     L.zeros = used - L.zero;
-    L.gram = plan_of(count, turns_of(L.tall ? rows : cols, both), true, [&](int T) { return triangle_tiles(L.small, T); });
-    L.square = plan_of(count, turns_of(side, both), false, [&](int T) { return triangle_tiles(L.small, T); });
-    L.update = plan_of(count, turns_of(side, both), false, [&](int T) { return all_tiles(m, n, T); });
+    L.gram = plan_of(count, L.tall ? rows : cols, both, true, [&](int T) { return triangle_tiles(L.small, T); });
+    L.square = plan_of(count, side, both, false, [&](int T) { return triangle_tiles(L.small, T); });
+    L.update = plan_of(count, side, both, false, [&](int T) { return all_tiles(m, n, T); });
     const size_t T = L.gram.tile;
     L.slab = take(L.gram.splits > 1 ? count * L.gram.splits * triangle_tiles(L.small, T) * T * T * 4 : 0);
     // Tiles of 64 leave padding unwritten (128 is what it goes by), which then
