@@ -116,11 +116,15 @@ struct StageLoader {
 
     // XOR on the chunk index of LDS row `row`, so that what is read in one
     // clock covers the 64 banks (256 bytes): by rows (64 bytes each) the same
-    // chunk of 16 rows, by k 64 bytes of 4 rows (of 2 where a row is 128 bytes). SQ_LDS_BANK_CONFLICT is zero;
-    // covering 32 banks alone left it at half of SQ_LDS_IDX_ACTIVE.
+    // chunk of 16 rows, by k 64 bytes of 4 rows, in halves that lie 64 bytes apart
+    // where planes are paired; rows of 128 bytes are two to the 256.
+    // SQ_LDS_BANK_CONFLICT is zero; covering 32 banks alone left it at half of
+    // SQ_LDS_IDX_ACTIVE.
     static __device__ __forceinline__ uint32_t swizzle(uint32_t row)
     {
-        return kKRows ? 4 * (row & (kWidth >= 128 ? 3 : 1)) : (row >> 2) & 3;
+        if (!kKRows)
+            return (row >> 2) & 3;
+        return kPaired ? 2 * (row & 1) + 4 * (row & 2) : kWidth >= 128 ? 4 * (row & 3) : 2 * (row & 2);
     }
 
     __device__ __forceinline__ void init(const MatOperand& m, uint32_t first, int wave_, int lane)
@@ -202,9 +206,10 @@ struct FragmentReader {
     {
         if (kKRows) {
             typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-            // 4 f chunks on (8 f): the XOR reaches bits 2 and 3 of the chunk, which 4 f meets too
-            const char* p = reinterpret_cast<const char*>(lds) + (base ^ (uint32_t(f) << (kPaired ? 7 : 6))) +
-                            kk * (kPaired ? 32 : 16 * kRow);
+            // 4 f chunks on (8 f, and 2 for the second plane): the XOR of the row
+            // reaches bits of the chunk that these meet too
+            const uint32_t at = kPaired ? base ^ (uint32_t(f) << 7 | uint32_t(kk) << 5) : base ^ (uint32_t(f) << 6);
+            const char* p = reinterpret_cast<const char*>(lds) + at + (kPaired ? 0 : kk * 16 * kRow);
             union {
                 s16x4 h[2];
                 s16x8 v;

@@ -281,6 +281,70 @@ def test_repeats_streams_and_graphs(gcq):
             assert torch.equal(c[1], replayed)
 
 
+def test_two_calls_at_once(gcq):
+    """On two streams, with workspaces of their own: what each gives alone. The
+    same matrix may be read twice."""
+    announce("orthogonalize two at once")
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for (m, n), (m2, n2) in (((600, 1500), (513, 700)), ((64, 500), (700, 600)), ((64, 200), (120, 250))):
+        calls = []
+        for k, (a, b) in enumerate(((m, n), (m2, n2))):
+            x = update(a, b, seed=k).to(gu.DEV)
+            outs = [torch.empty(a, b, dtype=BF16, device=gu.DEV) for _ in range(2)]
+            ws = torch.empty(gcq.orthogonalize_ws_bytes(2, a, b, BF16), dtype=torch.uint8, device=gu.DEV)
+            gcq.orthogonalize([x, x], outs, ws)
+            gu.sync()
+            assert torch.equal(outs[0], outs[1])
+            calls.append((x, outs, ws, outs[0].clone()))
+        for _ in range(4):
+            for k, (x, outs, ws, _) in enumerate(calls):
+                with torch.cuda.stream(s[k]):
+                    for o in outs:
+                        o.fill_(float("nan"))
+                    gcq.orthogonalize([x, x], outs, ws)
+        gu.sync()
+        for x, outs, ws, alone in calls:
+            assert torch.equal(outs[0], alone) and torch.equal(outs[1], alone)
+
+
+def test_past_32_bit_offsets(gcq):
+    """2^20 x 2100: more than 2^31 values, 2^32 bytes, 2^32 values of the planes.
+    One step, row by row: with |X| = 1 and u = 2^-11 a factor's rounding is at
+    most u, so that |dA| <= 2 u + 2^-24 sqrt(K) + u |A|, |dP| <= |b| |dA| + |c| (2 |A|
+    |dA| + 2 u |A|^2) + u |P|, and a row is off by |x| (|dP| + u |P|) and its rounding
+    (2^-22 of what is carried is far less)."""
+    announce("orthogonalize past 32 bits")
+    m, n, at_once = 1 << 20, 2100, 1 << 16
+    a, b, c = QUINTIC[0]
+    g = torch.Generator(device=gu.DEV).manual_seed(5)
+    right = torch.randn(4, n, generator=g, device=gu.DEV)
+    x = torch.empty(m, n, dtype=BF16, device=gu.DEV)
+    squares = 0.0
+    A = torch.zeros(n, n, dtype=torch.float64, device=gu.DEV)
+    for r in range(0, m, at_once):
+        rows = torch.randn(at_once, 4, generator=g, device=gu.DEV) @ right
+        x[r:r + at_once] = 0.1 * torch.randn(at_once, n, generator=g, device=gu.DEV) + rows
+        v = x[r:r + at_once].double()
+        A += v.t().contiguous() @ v
+        squares += float(v.square().sum())
+    out = torch.full((m, n), float("nan"), dtype=BF16, device=gu.DEV)
+    ws = torch.empty(gcq.orthogonalize_ws_bytes(1, m, n, BF16), dtype=torch.uint8, device=gu.DEV)
+    gcq.orthogonalize([x], [out], ws, coefficients=((a, b, c),), eps=EPS)
+    gu.sync()
+    norm = math.sqrt(squares) + EPS
+    A /= norm ** 2
+    P = b * A + c * (A @ A)
+    u, nA, nP = 2.0 ** -11, float(A.norm()), float(P.norm())
+    dA = 2 * u + 2.0 ** -24 * math.sqrt(m) + u * nA
+    dP = abs(b) * dA + abs(c) * (2 * nA * dA + 2 * u * nA ** 2) + u * nP
+    for r in range(0, m, at_once):
+        v = x[r:r + at_once].double() / norm
+        ref = a * v + v @ P
+        off = (out[r:r + at_once].double() - ref).norm(dim=1)
+        most = v.norm(dim=1) * (dP + u * nP) + 1.01 * po.HALF_STEP[BF16] * ref.norm(dim=1)
+        assert bool((off <= most).all()), (r, float((off / most).max()))
+
+
 # ---- the optimiser step ---------------------------------------------------------
 
 def step_case(count, m, n, t, seed=0):
@@ -383,6 +447,25 @@ def test_step_without_a_gradient_and_with_nan(gcq):
     assert bool((m0[0] == 0).all())
     assert bool(w[1].isnan().all()) and int(m0[1].isnan().sum()) == 1
     check_step([[v[2]] for v in case], m0[2:], w[2:])
+
+
+@pytest.mark.parametrize("shape", [(40, 90), (300, 257)], ids=str)
+def test_step_of_no_length(gcq, shape):
+    """A rate of zero leaves the weights bit for bit and moves the momenta."""
+    announce(f"step of no length {shape}")
+    m, n = shape
+    grads, momenta, weights = step_case(2, m, n, BF16)
+    gd, md, wd = ([v.to(gu.DEV) for v in t] for t in (grads, momenta, weights))
+    ws = torch.empty(gcq.muon_step_ws_bytes(2, m, n, BF16), dtype=torch.uint8, device=gu.DEV)
+    for kw in (dict(lr=0.0, weight_decay=0.1), dict(lr=0.1, update_scale=0.0)):
+        gcq.muon_step(gd, md, wd, ws, momentum=0.5, **kw)
+    gu.sync()
+    for k in range(2):
+        assert torch.equal(wd[k].cpu(), weights[k])
+        # a step rounds a difference, halved, and a sum: 2^-24 of the larger value each
+        ref = 0.25 * momenta[k].double() + 0.75 * grads[k].double()
+        size = torch.maximum(momenta[k].abs(), grads[k].abs()).double()
+        assert bool(((md[k].cpu().double() - ref).abs() <= 3 * F * size).all())
 
 
 def test_step_in_a_graph_follows_its_rate(gcq):
