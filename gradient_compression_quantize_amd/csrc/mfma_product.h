@@ -224,31 +224,48 @@ struct FragmentReader {
 };
 
 // The LDS of a tile, as variables of their own, so that the compiler knows
-// which loads a fragment read has to wait for.
+// which loads a fragment read has to wait for: a ring of four, or of eight.
 struct TileBuffers {
-    uint16_t *a[kBuffers], *b[kBuffers];
+    uint16_t *a[2 * kBuffers], *b[2 * kBuffers];
 };
 
-#define GCQ_TILE_BUFFERS(name, TA, TB)                                                                       \
-    __shared__ uint16_t name##_a0[(TA) * kStageK], name##_a1[(TA) * kStageK], name##_a2[(TA) * kStageK],       \
-        name##_a3[(TA) * kStageK], name##_b0[(TB) * kStageK], name##_b1[(TB) * kStageK],                     \
-        name##_b2[(TB) * kStageK], name##_b3[(TB) * kStageK];                                                \
-    const TileBuffers name = {{name##_a0, name##_a1, name##_a2, name##_a3},                                  \
+#define GCQ_FOUR_BUFFERS(name, values) \
+    __shared__ uint16_t name##0[values], name##1[values], name##2[values], name##3[values]
+
+#define GCQ_TILE_BUFFERS(name, TA, TB)                                             \
+    GCQ_FOUR_BUFFERS(name##_a, (TA) * kStageK);                                     \
+    GCQ_FOUR_BUFFERS(name##_b, (TB) * kStageK);                                     \
+    const TileBuffers name = {{name##_a0, name##_a1, name##_a2, name##_a3}, \
                               {name##_b0, name##_b1, name##_b2, name##_b3}}
+
+// (of a ring of four the others are not there: nothing reads them)
+#define GCQ_TILE_RING(name, T, ring)                                                                       \
+    GCQ_FOUR_BUFFERS(name##_a, (T) * kStageK);                                                              \
+    GCQ_FOUR_BUFFERS(name##_b, (T) * kStageK);                                                              \
+    GCQ_FOUR_BUFFERS(name##_c, (ring) == 8 ? (T) * kStageK : 1);                                            \
+    GCQ_FOUR_BUFFERS(name##_d, (ring) == 8 ? (T) * kStageK : 1);                                            \
+    const TileBuffers name = {                                                                             \
+        {name##_a0, name##_a1, name##_a2, name##_a3, name##_c0, name##_c1, name##_c2, name##_c3}, \
+        {name##_b0, name##_b1, name##_b2, name##_b3, name##_d0, name##_d1, name##_d2, name##_d3}}
 
 // kF16: fp16 operands, else bf16. kPlain: as of StageLoader, and planes that add
 // up as they are: no sum of segments is scaled. kPaired: of two such planes in both
 // operands all pairs but that of two second ones, as one segment: its turns are
 // of kTurnK / 2 values of k, whose planes are fetched and read out of LDS once for
 // all three products: 512 tiles of 128 x 128 over 2048 k in 116 us, 145 as three
-// segments; 256 of 256 x 256 in 181 and 191.
-template <bool kF16, bool kAK, bool kBK, int TA, int TB, int WA, int WB, bool kPlain = false, bool kPaired = false>
+// segments; 256 of 256 x 256 in 181 and 191. kRing: buffers of a tile; 8 keep seven
+// stages on their way, for small tiles, whose stages are over before what was asked
+// for three of them ago has come: 256 tiles of 64 x 64 over 8192 k in 34 us instead
+// of 48, over 768 in 7.6 instead of 8.0 (512, two to a compute unit: 72 and 64).
+template <bool kF16, bool kAK, bool kBK, int TA, int TB, int WA, int WB, bool kPlain = false, bool kPaired = false,
+          int kRing = kBuffers>
 struct TileProduct {
     static constexpr int kWaves = WA * WB;
     static constexpr int RA = TA / WA / 32, RB = TB / WB / 32;  // 32 x 32 products of a wave
     using LoadA = StageLoader<kAK, TA, kWaves, kPlain, kPaired>;
     using LoadB = StageLoader<kBK, TB, kWaves, kPlain, kPaired>;
     static constexpr int kOfTurn = kPaired ? kTurnK / 2 : kTurnK;
+    static_assert(kRing == kBuffers || (kRing == 2 * kBuffers && kPlain), "a ring of one turn or two");
 
     struct Acc {
         f32x16 v[RA][RB];
@@ -311,18 +328,21 @@ struct TileProduct {
         constexpr int kLoads = LoadA::kLoads + LoadB::kLoads;
         const auto load = [&](const Fetch& f, int s, int j) {
             if (j < LoadA::kLoads)
-                ga.load(A, f.pa, f.bytes, f.a, f.k0, s, j, lds.a[s]);
+                ga.load(A, f.pa, f.bytes, f.a, f.k0, s % kBuffers, j, lds.a[s]);
             else if (j < kLoads)
-                gb.load(B, f.pb, f.bytes, f.b, f.k0, s, j - LoadA::kLoads, lds.b[s]);
+                gb.load(B, f.pb, f.bytes, f.b, f.k0, s % kBuffers, j - LoadA::kLoads, lds.b[s]);
         };
 
         Fetch f = next_turn();
 #pragma unroll
-        for (int s = 0; s < kBuffers - 1; ++s)
+        for (int s = 0; s < kRing - 1; ++s) {
+            if (s > 0 && s % kBuffers == 0)
+                f = next_turn();
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
                 load(f, s, j);
-        wait_loads<2 * kLoads>();
+        }
+        wait_loads<(kRing - 2) * kLoads>();
         if constexpr (kPaired) {
             // Fragments of a second plane come in under the products of the two
             // first ones, those of the next stage's first planes under the third
@@ -334,12 +354,14 @@ struct TileProduct {
 #pragma unroll
             for (int i = 0; i < RA; ++i)
                 a[0][i] = fa.read(lds.a[0], i, 0);
-            for (uint32_t t = t0; t < t1; ++t) {
+            for (uint32_t t = t0; t < t1; t += kRing / kBuffers) {
 #pragma unroll
-                for (int s = 0; s < kBuffers; ++s) {
-                    wait_loads<kLoads>();
+                for (int s = 0; s < kRing; ++s) {
+                    if (s > 0 && s % kBuffers == 0 && t + s / kBuffers == t1)
+                        break;
+                    wait_loads<(kRing - 3) * kLoads>();
                     constexpr int kSteps = 3 * (RA > RB ? RA : RB), kEach = (kLoads + kSteps - 1) / kSteps;
-                    const int now = s & 1, next = now ^ 1, to = (s + 1) % kBuffers;
+                    const int now = s & 1, next = now ^ 1, to = (s + 1) % kRing;
 #pragma unroll
                     for (int phase = 0; phase < 3; ++phase)
 #pragma unroll
@@ -354,7 +376,7 @@ struct TileProduct {
                                 a[0][i] = fa.read(lds.a[to], i, 0);
 #pragma unroll
                             for (int e = 0; e < kEach; ++e)
-                                load(f, (s + kBuffers - 1) % kBuffers, (phase * (RA > RB ? RA : RB) + i) * kEach + e);
+                                load(f, (s + kRing - 1) % kRing, (phase * (RA > RB ? RA : RB) + i) * kEach + e);
                             if (i < RA) {
 #pragma unroll
                                 for (int j = 0; j < RB; ++j)
@@ -362,7 +384,7 @@ struct TileProduct {
                             }
                             __builtin_amdgcn_sched_barrier(0);
                         }
-                    if (s == 0)
+                    if (s % kBuffers == 0)
                         f = next_turn();
                 }
             }
@@ -378,17 +400,20 @@ struct TileProduct {
             a[0][i] = fa.read(lds.a[0], i, 0);
 
         const uint32_t fold = sh.fold * sh.turns;
-        for (uint32_t t = t0; t < t1; ++t) {
+        for (uint32_t t = t0; t < t1; t += kRing / kBuffers) {
             if (!kPlain && t == fold && t > t0)
                 scale(acc);
 #pragma unroll
-            for (int s = 0; s < kBuffers; ++s) {
+            for (int s = 0; s < kRing; ++s) {
+                if (s > 0 && s % kBuffers == 0 && t + s / kBuffers == t1)
+                    break;
                 // behind the barrier stage s + 1 is in LDS for everybody, and
-                // nobody reads the buffer of s - 1 any more, which s + 3 takes
-                wait_loads<kLoads>();
+                // nobody reads the buffer of s - 1 any more, which s + 3 (of a
+                // ring of four) takes
+                wait_loads<(kRing - 3) * kLoads>();
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    const int from = kk == 0 ? s : (s + 1) % kBuffers;
+                    const int from = kk == 0 ? s : (s + 1) % kRing;
                     // each row of products runs over the reads of a fragment
                     // of the next 16 k and one load
 #pragma unroll
@@ -400,7 +425,7 @@ struct TileProduct {
                         constexpr int kSteps = 2 * (RA > RB ? RA : RB), kEach = (kLoads + kSteps - 1) / kSteps;
 #pragma unroll
                         for (int e = 0; e < kEach; ++e)
-                            load(f, (s + kBuffers - 1) % kBuffers, (kk * (RA > RB ? RA : RB) + i) * kEach + e);
+                            load(f, (s + kRing - 1) % kRing, (kk * (RA > RB ? RA : RB) + i) * kEach + e);
                         if (i < RA) {
 #pragma unroll
                             for (int j = 0; j < RB; ++j)
@@ -410,7 +435,7 @@ struct TileProduct {
                     }
                 }
                 // the stages behind the last one of this turn are the next one's
-                if (s == 0)
+                if (s % kBuffers == 0)
                     f = next_turn();
             }
         }

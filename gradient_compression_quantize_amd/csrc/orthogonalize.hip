@@ -251,6 +251,8 @@ struct Tiles {
 template <int T>
 struct Waves {
     static constexpr int a = 2, b = T == 256 ? 4 : 2, threads = a * b * kWave;
+    // buffers of a tile: 1024 x 1024 takes 136 us, 161 with four
+    static constexpr int ring = T == 64 ? 8 : 4;
 };
 
 // What a wave's products leave through: its part of the tile, 32 rows of b at a
@@ -483,8 +485,8 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void symmetric_kernel(MatOper
                                                                          ProductShape sh, Tiles tiles, SymmetricOut out)
 {
     constexpr int WA = Waves<T>::a, WB = Waves<T>::b;
-    using P = TileProduct<true, kKRows, kKRows, T, T, WA, WB, true, kBoth>;
-    GCQ_TILE_BUFFERS(lds, T, T);
+    using P = TileProduct<true, kKRows, kKRows, T, T, WA, WB, true, kBoth, Waves<T>::ring>;
+    GCQ_TILE_RING(lds, T, Waves<T>::ring);
     const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), range = id / tiles.per_matrix;
     const uint32_t matrix = range / sh.splits, split = range - matrix * sh.splits;
     uint32_t ta, tb;
@@ -714,8 +716,8 @@ __global__ __launch_bounds__(Waves<T>::threads, 2) void update_kernel(MatOperand
                                                                       UpdateOut out, LastOut last)
 {
     constexpr int WA = Waves<T>::a, WB = Waves<T>::b;
-    using P = TileProduct<true, !kTall, false, T, T, WA, WB, true, kBoth>;
-    GCQ_TILE_BUFFERS(lds, T, T);
+    using P = TileProduct<true, !kTall, false, T, T, WA, WB, true, kBoth, Waves<T>::ring>;
+    GCQ_TILE_RING(lds, T, Waves<T>::ring);
     const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), matrix = id / tiles.per_matrix;
     uint32_t ta, tb;
     tile_of(id - matrix * tiles.per_matrix, tiles.a, tiles.b, ta, tb);
@@ -811,14 +813,14 @@ struct Plan {
 
 // Microseconds of `tiles` tiles of T over `turns` turns of 128 k, from what a turn
 // was measured to take (random values, 4096 and 16384 k): alone on a compute unit
-// with half of the chip's at work 2.8 (T = 256), 1.05 (128), 0.75 (64), with all of
-// them 3.9, 1.3 and 0.85; two of 128 to a compute unit 2.8, four of 64 2.5. Tiles
-// of 256 then come in rounds, the others fill in as places become free.
+// with half of the chip's at work 2.8 (T = 256), 1.05 (128), 0.52 (64), with all of
+// them 3.9, 1.3 and 0.55; two to a compute unit 2.8 (128) and 1.15 (64). Tiles of
+// 256 then come in rounds, the others fill in as places become free.
 double tiles_cost(int T, double tiles, double turns)
 {
-    const double cus = 256.0, places = T == 256 ? cus : T == 128 ? 2.0 * cus : 4.0 * cus;
-    const double few = T == 256 ? 2.8 : T == 128 ? 1.05 : 0.75, one = T == 256 ? 3.9 : T == 128 ? 1.3 : 0.85;
-    const double full = T == 256 ? 3.9 : T == 128 ? 2.8 : 2.5, end = T == 256 ? 8.0 : T == 128 ? 4.0 : 3.0;
+    const double cus = 256.0, places = T == 256 ? cus : 2.0 * cus;
+    const double few = T == 256 ? 2.8 : T == 128 ? 1.05 : 0.52, one = T == 256 ? 3.9 : T == 128 ? 1.3 : 0.55;
+    const double full = T == 256 ? 3.9 : T == 128 ? 2.8 : 1.15, end = T == 256 ? 8.0 : T == 128 ? 4.0 : 3.0;
     double turn, rounds = 1.0;
     if (tiles <= cus / 2)
         turn = few;
@@ -837,9 +839,9 @@ double tiles_cost(int T, double tiles, double turns)
 // each, what costs least. A turn of both planes is as long as 2.6 of one with
 // tiles of 256, 2.3 with smaller ones. Several ranges leave their sums in memory
 // (written and read at some 4 TB/s) for another launch (5 us): all five steps of 64
-// x 16384 take 100 us with 32 ranges, 445 with one, of 256 x 2304 112 and 146. With
-// tiles of one size alone: 4096 x 4096 1.53 ms with 256, 1.90 with 128, 2.93 with
-// 64; 768 x 768 383, 201 and 139 us; 48 of them 1054, 961 and 1159.
+// x 16384 take 99 us with 32 ranges, 327 with one, of 256 x 2304 106 and 127. With
+// tiles of one size alone: 4096 x 4096 1.59 ms with 256, 1.94 with 128, 2.82 with
+// 64; 768 x 768 369, 191 and 121 us; 48 of them 1054, 975 and 1287.
 template <typename Tiles>
 Plan plan_of(size_t count, size_t k, bool both, bool may_split, Tiles tiles)
 {
