@@ -16,6 +16,12 @@
 //   dgain = sum over rows of dh zhat,  dbias = sum over rows of dh
 // Both means go through one exchange. The sums over rows stay in registers,
 // leave one partial row a workgroup, and a second launch adds those in order.
+//
+// HBM bounds it: 16384 x 4096 bf16 takes 52 us forward (two activations, 5.2 TB/s,
+// what a large copy reaches) and 83 us backward (three, 4.8 TB/s, 5 us of it the
+// second launch); 8192 x 768 bf16 with dropout and sum 12.3 us (four, 4.1 TB/s);
+// 4095 x 1001 fp32 backward with dropout 24 us (five, 3.4 TB/s: rows off 16 bytes
+// draw two masks for four values). Of 16 x 768 the kernel takes 3 us, the call 7.5.
 #include "row_team.h"
 
 #include <algorithm>

@@ -1,4 +1,5 @@
-// mfma_product.h -- the tiled matrix product under linear_xent.hip.
+// mfma_product.h -- the tiled matrix product under linear_xent.hip and
+// orthogonalize.hip.
 //
 // out[b][a] = sum over segments, sum over k of A(a, k) * B(b, k), 16-bit
 // factors, fp32 sums in the matrix cores. An operand is a matrix of bf16 or
@@ -18,16 +19,16 @@
 // 2^-24, the smallest fp16, times 2^-11). A product then runs over segments,
 // one for each pair of planes: first those of one p1, whose sum is then
 // multiplied by 2^-11, then p0 p0. The pair of two p1, at most 2^-22 of a term,
-// is left out.
+// is left out. (orthogonalize.hip holds p1 as it is, in a range of its own: kPlain.)
 //
 // A workgroup of WA x WB waves owns a tile of TA x TB outputs. k advances in
 // stages of 32 values of both operands, moved straight into LDS
-// (buffer_load ... lds, 16 bytes a lane) by way of four buffers: while stage s
-// is multiplied, s + 1 is there (its first fragments are read under the last
-// products of s), s + 2 is on its way and s + 3 is asked for. LDS holds 16-byte
-// chunks permuted by an XOR of the row, which the loads apply to their global
-// addresses (LDS-direct loads write lane after lane) and the fragment reads to
-// their LDS addresses.
+// (buffer_load ... lds, 16 bytes a lane) by way of four buffers (eight of small
+// tiles: kRing): while stage s is multiplied, s + 1 is there (its first fragments
+// are read under the last products of s), s + 2 is on its way and s + 3 is asked
+// for. LDS holds 16-byte chunks permuted by an XOR of the row, which the loads
+// apply to their global addresses (LDS-direct loads write lane after lane) and
+// the fragment reads to their LDS addresses.
 //
 // Measured on 8192 x 64000 x 4096 bf16: 1.13 to 1.27 PFLOP/s (torch's library
 // product of that shape: 1.50). The matrix cores are busy 62 to 70% of the
@@ -167,8 +168,8 @@ struct StageLoader {
     {
         const auto to = (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + j) * 512);
         if (kClamped) {
-            // not past the last row that may be read; rows of a stage and the
-            // bytes of a row fit 24 bits
+            // not past the last row that may be read (a turn starts in front of
+            // it); rows of a stage and the bytes of a row fit 24 bits
             const uint32_t k = k0 + s * kStageK, first = min(k, m.krows - 1), last = m.krows - 1 - first;
             const uint32_t o = __umul24(min(row + j * kRowsPerLoad, last), m.ld * 2) + off[j];
             __builtin_amdgcn_raw_ptr_buffer_load_lds(view(p + size_t(first - k0) * m.ld, bytes), to, 16, o, 0, 0, 0);
