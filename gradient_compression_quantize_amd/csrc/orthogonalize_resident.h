@@ -32,7 +32,10 @@ struct Coefficients {
 };
 
 // A matrix of fp16 in LDS, rows of kLength values, in 16-byte chunks that an XOR
-// of the row spreads over the 64 banks.
+// of the row spreads over the 64 banks: the same chunk of 16 rows, which by_rows
+// reads in one clock, and 64 bytes of four rows, which by_k does: 256 x 128 takes
+// 41 us, 46 with the row itself (spread for by_k too, rows of 64 are slower: 576 x
+// 64 41 us instead of 38).
 template <int kLength>
 struct LdsMatrix {
     static constexpr int kChunks = kLength / 8, kSpread = kChunks < 16 ? kChunks : 16, kRowsOfBanks = 16 / kSpread;
@@ -41,7 +44,8 @@ struct LdsMatrix {
 
     __device__ __forceinline__ lds_u16* at(int row, int col) const
     {
-        const int chunk = (col >> 3) ^ ((row / kRowsOfBanks) & (kSpread - 1));
+        const int r = (row / kRowsOfBanks) & (kSpread - 1);
+        const int chunk = (col >> 3) ^ (kSpread == 16 ? 4 * (r & 3) + (r >> 2) : r);
         return p + row * kLength + chunk * 8 + (col & 7);
     }
 
