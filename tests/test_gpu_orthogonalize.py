@@ -307,42 +307,48 @@ def test_two_calls_at_once(gcq):
             assert torch.equal(outs[0], alone) and torch.equal(outs[1], alone)
 
 
-def test_past_32_bit_offsets(gcq):
-    """2^20 x 2100: more than 2^31 values, 2^32 bytes, 2^32 values of the planes.
-    One step, row by row: with |X| = 1 and u = 2^-11 a factor's rounding is at
-    most u, so that |dA| <= 2 u + 2^-24 sqrt(K) + u |A|, |dP| <= |b| |dA| + |c| (2 |A|
-    |dA| + 2 u |A|^2) + u |P|, and a row is off by |x| (|dP| + u |P|) and its rounding
-    (2^-22 of what is carried is far less)."""
-    announce("orthogonalize past 32 bits")
-    m, n, at_once = 1 << 20, 2100, 1 << 16
-    a, b, c = QUINTIC[0]
+@pytest.mark.parametrize("tall", [True, False], ids=["tall", "wide"])
+def test_past_32_bit_offsets(gcq, tall):
+    """2^20 x 2100 and 2100 x 2^20: more than 2^31 values, 2^32 bytes, 2^32 values of
+    the planes. One step, row (column) by row: with |X| = 1 and u = 2^-11 a factor's
+    rounding is at most u, so that |dA| <= 2 u + 2^-24 sqrt(K) + u |A|, |dP| <= |b| |dA|
+    + |c| (2 |A| |dA| + 2 u |A|^2) + u |P|, and a row is off by |x| (|dP| + u |P|) and its
+    rounding (2^-22 of what is carried is far less)."""
+    announce(f"orthogonalize past 32 bits {tall}")
+    c, r, at_once = 1 << 20, 2100, 1 << 16
+    a, b, c2 = QUINTIC[0]
     g = torch.Generator(device=gu.DEV).manual_seed(5)
-    right = torch.randn(4, n, generator=g, device=gu.DEV)
-    x = torch.empty(m, n, dtype=BF16, device=gu.DEV)
+    right = torch.randn(4, r, generator=g, device=gu.DEV)
+    shape = (c, r) if tall else (r, c)
+    x = torch.empty(shape, dtype=BF16, device=gu.DEV)
+
+    def part(t, k):
+        """Rows (of the wide one: columns) k on."""
+        return t[k:k + at_once] if tall else t[:, k:k + at_once].t()
     squares = 0.0
-    A = torch.zeros(n, n, dtype=torch.float64, device=gu.DEV)
-    for r in range(0, m, at_once):
+    A = torch.zeros(r, r, dtype=torch.float64, device=gu.DEV)
+    for k in range(0, c, at_once):
         rows = torch.randn(at_once, 4, generator=g, device=gu.DEV) @ right
-        x[r:r + at_once] = 0.1 * torch.randn(at_once, n, generator=g, device=gu.DEV) + rows
-        v = x[r:r + at_once].double()
+        part(x, k).copy_(0.1 * torch.randn(at_once, r, generator=g, device=gu.DEV) + rows)
+        v = part(x, k).double().contiguous()
         A += v.t().contiguous() @ v
         squares += float(v.square().sum())
-    out = torch.full((m, n), float("nan"), dtype=BF16, device=gu.DEV)
-    ws = torch.empty(gcq.orthogonalize_ws_bytes(1, m, n, BF16), dtype=torch.uint8, device=gu.DEV)
-    gcq.orthogonalize([x], [out], ws, coefficients=((a, b, c),), eps=EPS)
+    out = torch.full(shape, float("nan"), dtype=BF16, device=gu.DEV)
+    ws = torch.empty(gcq.orthogonalize_ws_bytes(1, *shape, BF16), dtype=torch.uint8, device=gu.DEV)
+    gcq.orthogonalize([x], [out], ws, coefficients=((a, b, c2),), eps=EPS)
     gu.sync()
     norm = math.sqrt(squares) + EPS
     A /= norm ** 2
-    P = b * A + c * (A @ A)
+    P = b * A + c2 * (A @ A)
     u, nA, nP = 2.0 ** -11, float(A.norm()), float(P.norm())
-    dA = 2 * u + 2.0 ** -24 * math.sqrt(m) + u * nA
-    dP = abs(b) * dA + abs(c) * (2 * nA * dA + 2 * u * nA ** 2) + u * nP
-    for r in range(0, m, at_once):
-        v = x[r:r + at_once].double() / norm
+    dA = 2 * u + 2.0 ** -24 * math.sqrt(c) + u * nA
+    dP = abs(b) * dA + abs(c2) * (2 * nA * dA + 2 * u * nA ** 2) + u * nP
+    for k in range(0, c, at_once):
+        v = part(x, k).double().contiguous() / norm
         ref = a * v + v @ P
-        off = (out[r:r + at_once].double() - ref).norm(dim=1)
+        off = (part(out, k).double() - ref).norm(dim=1)
         most = v.norm(dim=1) * (dP + u * nP) + 1.01 * po.HALF_STEP[BF16] * ref.norm(dim=1)
-        assert bool((off <= most).all()), (r, float((off / most).max()))
+        assert bool((off <= most).all()), (k, float((off / most).max()))
 
 
 # ---- the optimiser step ---------------------------------------------------------
