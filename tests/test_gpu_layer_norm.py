@@ -259,6 +259,24 @@ def test_no_rows(gcq):
     assert bool((dgain == 0).all()) and bool((dbias == 0).all())
 
 
+@pytest.mark.parametrize("d", [64, 1001, 6000])
+def test_everything_dropped(gcq, d):
+    """p = 1: y does not count, whatever it holds, and gets no gradient."""
+    announce(f"layer_norm p = 1, {d}")
+    c = case(9, d, torch.bfloat16, seed=12)
+    y = torch.full_like(c["x"], float("nan"))
+    z, h, alone = (torch.empty(9, d, dtype=torch.bfloat16, device=gu.DEV) for _ in range(3))
+    mean, rstd = (torch.empty(9, device=gu.DEV) for _ in range(2))
+    kw = dict(gain=on(c["gain"]), bias=on(c["bias"]), eps=EPS)
+    gcq.layer_norm(on(c["x"]), h, y=on(y), z=z, p=1.0, mean=mean, rstd=rstd, **kw)
+    gcq.layer_norm(on(c["x"]), alone, **kw)
+    dx, dy = torch.full_like(z, 7.0), torch.full_like(z, 7.0)
+    gcq.layer_norm_grad(z, on(c["dh"]), dx, torch.empty(gcq.layer_norm_grad_ws_bytes(9, d), dtype=torch.uint8, device=gu.DEV),
+                        dy=dy, gain=kw["gain"], p=1.0, mean=mean, rstd=rstd)
+    assert torch.equal(z.cpu(), c["x"]) and torch.equal(h, alone)
+    assert bool((dy == 0).all()) and bool(torch.isfinite(dx.float()).all())
+
+
 def test_rows_behind_the_last_are_left(gcq):
     announce("layer_norm padded")
     for d in (64, 1001, 6000):
