@@ -134,7 +134,7 @@ def _declare(L):
     pp = ctypes.POINTER(_vp)
     L.orthogonalize.argtypes = [pp, _i, _sz, _sz, _i, _vp, _i, _f, _f, pp, _i, _vp,
                                 ctypes.POINTER(_sz), _vp]
-    L.muon_step.argtypes = [pp, _i, _sz, _sz, pp, pp, _i, _i, _vp, _i, _f, _f, _f, _i, _f, _vp, _f,
+    L.muon_step.argtypes = [pp, _i, _sz, _sz, pp, pp, _i, _i, _vp, _i, _f, _f, dbl, _i, _f, _vp, _f,
                             _f, pp, pp, _vp, ctypes.POINTER(_sz), _vp]
     for name in ("compress_2bit", "decompress_2bit", "decompress_2bit_sum",
                  "compress_ternary", "decompress_ternary", "decompress_ternary_sum",

@@ -316,9 +316,9 @@ __global__ __launch_bounds__(kResidentWaves* kWave, 2) void resident_kernel(Resi
                 for (int i = 0; i < RB; ++i) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float g = v[k][i][e] * mo.grad_scale, now = mix(g, old[k][i][e], mo.beta);
+                        const float g = v[k][i][e] * mo.grad_scale, now = mix(g, old[k][i][e], mo);
                         old[k][i][e] = now;
-                        v[k][i][e] = mo.nesterov ? mix(g, now, mo.beta) : now;
+                        v[k][i][e] = mo.nesterov ? mix(g, now, mo) : now;
                     }
                     put(m1, GC_F32, nb + k, i, old[k][i]);
                 }

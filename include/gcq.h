@@ -508,8 +508,9 @@ int orthogonalize(const void* const* x, int count, size_t m, size_t n, int dtype
 
 /* One step of an optimiser that moves weight matrices along the orthogonalised
  * momentum of their gradients. For each of `count` matrices of m x n:
- *   g = grad_scale * grads;  new_momenta = g + momentum * (momenta - g)
- *   u = nesterov ? g + momentum * (new_momenta - g) : new_momenta
+ *   g = grad_scale * grads
+ *   new_momenta = (1 - momentum) * g + momentum * momenta
+ *   u = nesterov ? (1 - momentum) * g + momentum * new_momenta : new_momenta
  *   X = what orthogonalize() makes of u (coefficients, steps, eps)
  *   new_weights = (1 - r weight_decay) * weights - r update_scale X,
  *   r = lr * (lr_scale ? *lr_scale : 1)
@@ -522,7 +523,7 @@ int orthogonalize(const void* const* x, int count, size_t m, size_t n, int dtype
  *   update_dtype  says how exactly X is computed: as for an out of this type in
  *            orthogonalize() (it is not rounded to it). With weights of bf16 it
  *            is GC_BF16 for all that they hold
- *   momentum 0 .. 1 (below 1)
+ *   momentum 0 .. 1 (below 1); 1 - momentum is taken of all 64 bits
  *   lr_scale device fp32, read when the kernel runs, or NULL: a captured call
  *            follows a schedule that the graph or the caller advances
  *   ws       as in orthogonalize(), of (count, m, n, update_dtype); limits too
@@ -530,7 +531,7 @@ int orthogonalize(const void* const* x, int count, size_t m, size_t n, int dtype
 int muon_step(const float* const* grads, int count, size_t m, size_t n,
               const float* const* momenta, const void* const* weights, int dtype,
               int update_dtype, const float* coefficients, int steps, float eps,
-              float grad_scale, float momentum, int nesterov, float lr,
+              float grad_scale, double momentum, int nesterov, float lr,
               const float* lr_scale, float weight_decay, float update_scale,
               float* const* new_momenta, void* const* new_weights, void* ws,
               size_t* ws_bytes, hipStream_t stream);
