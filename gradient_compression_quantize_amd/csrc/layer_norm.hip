@@ -9,7 +9,8 @@
 // the mean itself. A wave finds the mean and the squares around it of its own
 // part of the row; a team of several waves joins them in one exchange,
 //   sum (z - mean)^2 = sum over waves of (squares + count (mean_w - mean)^2),
-// which loses nothing where the mean is far larger than the deviations.
+// which loses nothing where the mean is far larger than the deviations, or where
+// there are none.
 //
 // Gradient, with zhat = (z - mean) rstd and g = dh gain:
 //   dx = dz + rstd (g - mean(g) - zhat mean(g zhat)),  dy = dx mask / (1 - p)
@@ -58,7 +59,13 @@ __device__ __forceinline__ float wave_count(int w, uint32_t d)
     return float(n);
 }
 
-// Mean of the row x (zeros behind column d), and sum of squares around it.
+// Mean of the row x (zeros behind column d), and sum of squares around it. A sum
+// and its quotient round by some 2^-24 of the mean each, which is all that a row of
+// one value has for deviations: eps = 1e-12 would make them the size of the gain. The
+// deviations from the first mean, exact there, say how far it is off,
+//   mean += sum u / n,  squares = sum u^2 - (sum u)^2 / n
+// (one more sum, beside that of the squares: 16384 x 4096 bf16 52.2 us, 51.9 without;
+// 4096 x 8192 with dropout 59.0 and 57.4).
 template <typename R, int kTeam, int kVecs, bool kAligned>
 __device__ __forceinline__ void mean_and_squares(const typename R::F (&x)[kVecs], uint32_t d, float inv_d, int t,
                                                  float* lds, int& half, float& mean, float& squares)
@@ -73,16 +80,22 @@ __device__ __forceinline__ void mean_and_squares(const typename R::F (&x)[kVecs]
     s = wave_sum(s);
     const int wave = kWaves == 1 ? 0 : __builtin_amdgcn_readfirstlane(t / kWave);
     const float count = wave_count<R, kTeam, kVecs>(wave, d);
-    const float own = kWaves == 1 ? s * inv_d : count > 0.0f ? s / count : 0.0f;
-    float q = 0.0f;
+    const float inv = kWaves == 1 ? inv_d : count > 0.0f ? 1.0f / count : 0.0f;
+    const float first = s * inv;
+    float q = 0.0f, r = 0.0f;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
 #pragma unroll
         for (int e = 0; e < R::V; ++e) {
-            const float u = R::col(v, t) + (kAligned ? 0 : e) < d ? x[v][e] - own : 0.0f;
+            const float u = R::col(v, t) + (kAligned ? 0 : e) < d ? x[v][e] - first : 0.0f;
             q = __builtin_fmaf(u, u, q);
+            r += u;
         }
     q = wave_sum(q);
+    r = wave_sum(r);
+    const float more = r * inv, own = first + more;
+    q = __builtin_fmaf(-r, more, q);
+    q = q < 0.0f ? 0.0f : q;  // (a NaN stays)
     if (kWaves == 1) {
         mean = own;
         squares = q;
@@ -91,19 +104,22 @@ __device__ __forceinline__ void mean_and_squares(const typename R::F (&x)[kVecs]
     float* at = lds + half * (2 * kWaves);
     half ^= 1;
     if ((t & (kWave - 1)) == 0) {
-        at[wave] = s;
+        at[wave] = own;
         at[kWaves + wave] = q;
     }
     __syncthreads();
-    float total = 0.0f;
-    for (int w = 0; w < kWaves; ++w)
-        total += at[w];
-    mean = total * inv_d;
+    // (from wave 0's mean on, so that equal ones stay as they are)
+    float off = 0.0f;
+    for (int w = 1; w < kWaves; ++w) {
+        const float n = wave_count<R, kTeam, kVecs>(w, d);
+        off += n > 0.0f ? n * (at[w] - at[0]) : 0.0f;
+    }
+    mean = __builtin_fmaf(off, inv_d, at[0]);
     squares = 0.0f;
     for (int w = 0; w < kWaves; ++w) {
         const float n = wave_count<R, kTeam, kVecs>(w, d);
-        const float off = n > 0.0f ? at[w] / n - mean : 0.0f;
-        squares += at[kWaves + w] + n * (off * off);
+        const float u = n > 0.0f ? at[w] - mean : 0.0f;
+        squares += at[kWaves + w] + n * (u * u);
     }
 }
 

@@ -1,0 +1,36 @@
+"""Rows of one value have no deviations: h is the bias, mean the value, whatever
+their size, their length and eps. (The sum over a row and its quotient round;
+what that leaves, divided by an eps of 1e-12, was of the size of the gain.)"""
+import pytest
+import torch
+
+from conftest import announce
+
+pytestmark = pytest.mark.gpu
+gu = pytest.importorskip("gpu_util")
+
+VALUES = [3.25, 100.0, -7.5, 0.1, 1000.3, -31.7, 1e6, 3e-5]
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("d", [1, 5, 257, 768, 1000, 1001, 2040, 4104, 6000, 9001, 12288, 16384])
+@pytest.mark.parametrize("eps", [1e-5, 1e-12])
+def test_rows_of_one_value(gcq, d, t, eps):
+    announce(f"layer_norm rows of one value {d} {t} {eps}")
+    g = torch.Generator().manual_seed(d)
+    bias, gain = torch.randn(d, generator=g).to(gu.DEV), torch.randn(d, generator=g).to(gu.DEV)
+    values = torch.tensor([v for v in VALUES if t != torch.float16 or abs(v) < 6e4]).to(t)
+    x = values[:, None].repeat(1, d).to(gu.DEV)
+    h = torch.full_like(x, float("nan"))
+    mean = torch.full((len(values),), float("nan"), device=gu.DEV)
+    gcq.layer_norm(x, h, gain=gain, bias=bias, eps=eps, mean=mean)
+    gu.sync()
+    assert torch.equal(mean.cpu(), values.float())
+    assert torch.equal(h, bias.to(t).expand_as(h)), float((h - bias).abs().max())
+    # the same as a sum: x + y of rows that cancel
+    y = (torch.randn(len(values), d, generator=g) * 0.5).to(t).to(gu.DEV)
+    z = torch.full_like(x, float("nan"))
+    gcq.layer_norm(-y, h, y=y, z=z, gain=gain, bias=bias, eps=eps, mean=mean)
+    gu.sync()
+    assert bool((z == 0).all()) and bool((mean == 0).all())
+    assert torch.equal(h, bias.to(t).expand_as(h))
