@@ -908,8 +908,8 @@ def orthogonalize(xs: Sequence, outs: Sequence, ws, coefficients=NEWTON_SCHULZ,
     """outs[k] = scale * (xs[k] / (its norm + eps) after a step a X + b (X X') X
     + c (X X')^2 X for each triple of `coefficients`). xs and outs: up to 64
     matrices [m, n], the xs of one dtype and the outs of one; the dtype of the
-    outs says how exactly they are computed. outs[k] may be xs[k] itself. ws:
-    uint8 device tensor of at least orthogonalize_ws_bytes(count, m, n,
+    outs says how exactly they are computed. outs[k] may be xs[k] itself, but
+    overlap no other matrix of the call. ws: uint8 device tensor of at least orthogonalize_ws_bytes(count, m, n,
     out_dtype) bytes."""
     count, m, n = _matrices("orthogonalize", "xs outs", xs, outs)
     coef, steps = _coefficients(coefficients)
@@ -938,7 +938,7 @@ def muon_step(grads: Sequence, momenta: Sequence, weights: Sequence, ws,
     """Moves the momenta along the gradients, and the weights along the
     orthogonalised momenta. Up to 64 matrices [m, n]: grads and momenta
     float32, weights of one dtype; new_momenta and new_weights default to the
-    tensors themselves. update_dtype (by default the weights' dtype) says how
+    tensors themselves, and overlap no other matrix of the call. update_dtype (by default the weights' dtype) says how
     exactly the update is computed: bfloat16 is a third of the products of
     float32. lr_scale: one-element float32 device tensor multiplied to lr on
     the device. ws: uint8 device tensor of at least muon_step_ws_bytes(count,

@@ -1112,6 +1112,48 @@ bool take_pointers(PtrTable<T>& t, const void* const* p, size_t count, size_t by
     return true;
 }
 
+// The buffers of a call in memory, to find outputs that lie in others: whether
+// those are read first goes by the size of the matrices.
+class Buffers {
+public:
+    void reads(const void* p, size_t bytes) { add(p, bytes, false); }
+    // An output; `own`: the input that may be in its place.
+    void writes(const void* p, size_t bytes, const void* own, size_t own_bytes)
+    {
+        const bool in_place = p == own;
+        add(p, in_place ? std::max(bytes, own_bytes) : bytes, true);
+        if (own && !in_place)
+            add(own, own_bytes, false);
+    }
+
+    bool overlap()
+    {
+        std::sort(all_, all_ + count_, [](const One& a, const One& b) { return a.first < b.first; });
+        uintptr_t end = 0, end_of_outputs = 0;
+        for (size_t k = 0; k < count_; ++k) {
+            const One& o = all_[k];
+            if (o.first < (o.output ? end : end_of_outputs))
+                return true;
+            end = std::max(end, o.last);
+            end_of_outputs = o.output ? std::max(end_of_outputs, o.last) : end_of_outputs;
+        }
+        return false;
+    }
+
+private:
+    struct One {
+        uintptr_t first, last;
+        bool output;
+    };
+    void add(const void* p, size_t bytes, bool output)
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        all_[count_++] = One{at, at + bytes, output};
+    }
+    One all_[5 * GC_MAX_WORKERS];
+    size_t count_ = 0;
+};
+
 // What a call reads: matrices of `dtype`, or gradients and momenta.
 struct In {
     PtrTable<void> x;
@@ -1209,6 +1251,11 @@ GCQ_API int orthogonalize(const void* const* x, int count, size_t m, size_t n, i
     if (!take_pointers(in.x, x, c.count, dtype_bytes(dtype)) ||
         !take_pointers(last.out, out, c.count, dtype_bytes(out_dtype)))
         return refuse(c, "a matrix is NULL or misaligned");
+    Buffers at;
+    for (size_t k = 0; k < c.count; ++k)
+        at.writes(out[k], m * n * dtype_bytes(out_dtype), x[k], m * n * dtype_bytes(dtype));
+    if (at.overlap())
+        return refuse(c, "an out overlaps another matrix (out[k] may be x[k] itself)");
     last.dtype = out_dtype;
     last.m = uint32_t(m);
     last.n = uint32_t(n);
@@ -1247,6 +1294,14 @@ GCQ_API int muon_step(const float* const* grads, int count, size_t m, size_t n, 
         !take_pointers(in.new_momenta, reinterpret_cast<const void* const*>(new_momenta), c.count, 4) ||
         !take_pointers(last.weights, weights, c.count, b) || !take_pointers(last.out, new_weights, c.count, b))
         return refuse(c, "a matrix is NULL or misaligned");
+    Buffers at;
+    for (size_t k = 0; k < c.count; ++k) {
+        at.reads(grads[k], m * n * 4);
+        at.writes(new_momenta[k], m * n * 4, momenta[k], m * n * 4);
+        at.writes(new_weights[k], m * n * b, weights[k], m * n * b);
+    }
+    if (at.overlap())
+        return refuse(c, "new momenta or weights overlap another matrix (they may be the old ones themselves)");
     last.dtype = dtype;
     last.update = true;
     last.m = uint32_t(m);

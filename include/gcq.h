@@ -488,7 +488,7 @@ int linear_xent_grad(const void* hidden, const void* weight, int dtype, size_t N
  *   coefficients  host [steps][3] fp32, read before the call returns
  *   steps    1 .. 64;  eps >= 0 (0: a zero matrix gives NaN)
  *   out      host array of `count` pointers to [m, n] of out_dtype; out[k] may
- *            be x[k] itself
+ *            be x[k] itself, but overlap nothing else of x and out (refused)
  *   ws       16-byte-aligned workspace; ws == NULL: *ws_bytes = its size for
  *            (count, m, n, out_dtype) and nothing is enqueued. Otherwise
  *            *ws_bytes is its size and must be at least that. Calls that may
@@ -515,11 +515,12 @@ int orthogonalize(const void* const* x, int count, size_t m, size_t n, int dtype
  *   new_weights = (1 - r weight_decay) * weights - r update_scale X,
  *   r = lr * (lr_scale ? *lr_scale : 1)
  *   grads, momenta, new_momenta  host arrays of `count` pointers to [m, n] fp32;
- *            new_momenta[k] may be momenta[k] itself. What the reducers of (1)
+ *            new_momenta[k] may be momenta[k] itself, new_weights[k] weights[k];
+ *            they overlap no other matrix of the call (refused: gradients are
+ *            read again behind the new momenta). What the reducers of (1)
  *            and (2) write is read in place: grad_scale = 1 / W makes a mean of
  *            their sum
- *   weights, new_weights  host arrays of `count` pointers to [m, n] of `dtype`;
- *            new_weights[k] may be weights[k] itself
+ *   weights, new_weights  host arrays of `count` pointers to [m, n] of `dtype`
  *   update_dtype  says how exactly X is computed: as for an out of this type in
  *            orthogonalize() (it is not rounded to it). With weights of bf16 it
  *            is GC_BF16 for all that they hold
