@@ -1,6 +1,7 @@
 """orthogonalize and muon_step row by row and column by column, against 64 bits,
 with the bounds of rounded_newton_schulz.py (drawn from the roundings of the
-planes)."""
+planes); values of any size, rank one, zero and not finite in matrices of one
+workgroup and of tiles."""
 import pytest
 import torch
 
@@ -98,3 +99,62 @@ def test_larger_tiles(gcq, shape, both):
     order = [torch.randperm(m, generator=torch.Generator().manual_seed(k)) for k in range(count)]
     for got, o in zip(unrounded(gcq, [x[o].contiguous() for o in order], F32 if both else BF16), order):
         check(got, x, both, ref=ref[o], bounds=(matrix, line))
+
+
+# (matrices in one workgroup of one plane and two, in tiles of either)
+KINDS = [(40, 90, F32), (300, 30, F32), (128, 200, BF16), (500, 60, BF16), (70, 90, F32), (300, 290, BF16)]
+
+
+@pytest.mark.parametrize("m,n,t", KINDS, ids=str)
+@pytest.mark.parametrize("size", [1e30, 1e18, 1e-30, 3e-39], ids=str)
+def test_any_magnitude(gcq, m, n, t, size):
+    """A factor of a power of two changes no bit of the result, as long as all
+    values stay normal; below that, what is left of them is what counts."""
+    announce(f"orthogonalize {m} x {n} {t} near {size}")
+    x = update(m, n, seed=5) * 1e3 * size
+    check(orthogonalize(gcq, [x], t, eps=0.0)[0], x, t != BF16, eps=0.0)
+    if size > 1e-38:
+        times = 2.0 ** (20 if size < 1 else -20)
+        a, b = orthogonalize(gcq, [x], t, eps=0.0), orthogonalize(gcq, [x * times], t, eps=0.0)
+        assert torch.equal(a[0], b[0])
+
+
+@pytest.mark.parametrize("m,n,t", KINDS, ids=str)
+def test_rank_one_and_zero(gcq, m, n, t):
+    announce(f"orthogonalize rank one and zero {m} x {n} {t}")
+    g = torch.Generator().manual_seed(6)
+    # (values away from zero: each of a row and column of it is a line of its own)
+    u, v = (torch.randn(k, generator=g).sign() * (0.5 + torch.rand(k, generator=g)) for k in (m, n))
+    x, zero = torch.outer(u, v), torch.zeros(m, n)
+    got = orthogonalize(gcq, [x, zero, x], t)
+    # one singular value, of 1: what the steps make of it, along u v'
+    s = 1.0
+    for a, b, c in QUINTIC:
+        s = a * s + b * s ** 3 + c * s ** 5
+    way = torch.outer(u.double() / u.double().norm(), v.double() / v.double().norm())
+    ref = reference(x)
+    # (x is rounded, by at most 2^-24 of its norm, and what lies beside one direction
+    # grows by 3.4445 in each of the five steps: 485 times)
+    assert float((ref - s * way).norm()) < 3.4445 ** 5 * po.F32
+    check(got[0], x, t != BF16, ref=ref)
+    assert bool((got[1] == 0).all()) and torch.equal(got[0], got[2])
+    # without eps nothing says where zero goes
+    got = orthogonalize(gcq, [x, zero], t, eps=0.0)
+    assert bool(got[1].isnan().all()) and bool(got[0].isfinite().all())
+
+
+@pytest.mark.parametrize("m,n,t", KINDS, ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_value_that_is_not_finite_stays_in_its_matrix(gcq, m, n, t, bad):
+    announce(f"orthogonalize {m} x {n} {t} with {bad}")
+    xs = [update(m, n, seed=k) for k in range(3)]
+    ref = orthogonalize(gcq, xs, t)
+    for where in ((17, 3), (0, 0), (m - 1, n - 1)):
+        held = xs[1][where].clone()
+        xs[1][where] = bad
+        got = orthogonalize(gcq, xs, t)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[2], ref[2])
+        assert bool(got[1].isnan().all())
+        for series in (QUINTIC[:1], ((1.5, -0.5, 0.0),), ((1.0, 0.0, 0.0),)):
+            assert bool(orthogonalize(gcq, xs, t, series)[1].isnan().all()), series
+        xs[1][where] = held
