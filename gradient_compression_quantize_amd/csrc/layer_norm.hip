@@ -94,8 +94,8 @@ __device__ __forceinline__ void mean_and_squares(const typename R::F (&x)[kVecs]
     q = wave_sum(q);
     r = wave_sum(r);
     const float more = r * inv, own = first + more;
-    q = __builtin_fmaf(-r, more, q);
-    q = q < 0.0f ? 0.0f : q;  // (a NaN stays)
+    if (q < __builtin_inff())  // (what is not finite stays)
+        q = fmaxf(__builtin_fmaf(-r, more, q), 0.0f);
     if (kWaves == 1) {
         mean = own;
         squares = q;

@@ -34,3 +34,18 @@ def test_rows_of_one_value(gcq, d, t, eps):
     gu.sync()
     assert bool((z == 0).all()) and bool((mean == 0).all())
     assert torch.equal(h, bias.to(t).expand_as(h))
+
+
+@pytest.mark.parametrize("d", [64, 768, 4104, 12288])
+def test_squares_past_fp32(gcq, d):
+    """Deviations of 1e25 have an infinite variance in fp32, and rstd is 0."""
+    announce(f"layer_norm squares past fp32 {d}")
+    g = torch.Generator().manual_seed(d)
+    x, bias = (torch.randn(4, d, generator=g) * 1e25).to(gu.DEV), torch.randn(d, generator=g).to(gu.DEV)
+    x[1] = torch.randn(d, generator=g).to(gu.DEV)
+    h, rstd = torch.full_like(x, float("nan")), torch.full((4,), float("nan"), device=gu.DEV)
+    gcq.layer_norm(x, h, bias=bias, rstd=rstd)
+    gu.sync()
+    rows = torch.tensor([0, 2, 3], device=gu.DEV)
+    assert bool((rstd[rows] == 0).all()) and torch.equal(h[rows], bias.expand(3, d))
+    assert bool(h[1].isfinite().all()) and float(rstd[1]) > 0.5
