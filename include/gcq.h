@@ -389,7 +389,9 @@ int norm_residual_grad(const void* z, const void* y, int dtype, size_t rows, siz
  *   mean = mean(z),  rstd = 1 / sqrt(mean((z - mean)^2) + eps)
  * with the mask of dropout() at offset 0 over the rows x d values (p = 0: no
  * dropout). Everything between is fp32; the squares are those of the
- * deviations from the mean, and h is that of the z before its rounding.
+ * deviations from the mean, and h is that of the z before its rounding. The
+ * mean is corrected by the deviations from it: a row of one value has none, and
+ * its h is the bias for any eps above 0 (0: NaN).
  *   x, y, z, h  [rows, d] of `dtype`, rows contiguous; z NULL: not kept, and
  *               NULL without y. h may be x or y, z the other one
  *   gain, bias  [d] fp32, or NULL
@@ -492,7 +494,13 @@ int linear_xent_grad(const void* hidden, const void* weight, int dtype, size_t N
  *   ws       16-byte-aligned workspace; ws == NULL: *ws_bytes = its size for
  *            (count, m, n, out_dtype) and nothing is enqueued. Otherwise
  *            *ws_bytes is its size and must be at least that. Calls that may
- *            overlap in time need workspaces of their own.
+ *            overlap in time need workspaces of their own. Matrices that one
+ *            workgroup holds (bf16 outs: sides up to 64 and 1024 or 128 and 256;
+ *            others: 32 and 1024 or 64 and 256) need none to speak of. The rest
+ *            need 8 bytes for each value of the matrix with both sides rounded up
+ *            to 128, 4 (fp16, fp32: 8) for each of the smaller side's square, and
+ *            room for partial sums of long products. Thin matrices are mostly
+ *            padding: 48 of 16 x 16384 ask for 815 MB, one of 1 x 2^20 for 1.1 GB
  * The norm is summed in 64 bits. X is carried from step to step to 22 bits of a
  * value; the factors of the products are rounded to 11 bits for a bf16 out, to
  * 22 (three products for each one) for fp16 and fp32; their sums are fp32. The

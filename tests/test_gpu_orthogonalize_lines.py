@@ -62,7 +62,9 @@ def unrounded(gcq, xs, update_dtype, series=QUINTIC, eps=EPS):
 
 # one workgroup: each of its kinds, wide and tall; tiles of 64, 128 and 256, ragged
 SHAPES = [(17, 20), (20, 33), (31, 1000), (1000, 31), (64, 576), (576, 64), (50, 250), (250, 50), (128, 256), (200, 100),
-          (129, 257), (300, 290), (70, 90), (520, 1500), (1500, 520), (700, 640), (130, 3000)]
+          (129, 257), (300, 290), (70, 90), (520, 1500), (1500, 520), (700, 640), (130, 3000),
+          # thin ones past one workgroup, whose smaller side is mostly padding
+          (16, 16384), (16384, 16), (20, 5001), (5001, 20)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
@@ -85,6 +87,26 @@ def test_products_of_both_planes(gcq, shape, series):
     bounds = allowed(x, ref, series, True, EPS)
     check(unrounded(gcq, [x], F32, series)[0], x, True, ref=ref, bounds=bounds)
     check(orthogonalize(gcq, [x], F32, series)[0], x, True, ref=ref, bounds=bounds)
+
+
+@pytest.mark.parametrize("count,m,n", [(3, 1, 70001), (2, 70001, 1), (5, 3, 2000), (64, 2, 1500)])
+@pytest.mark.parametrize("t", [F32, BF16], ids=str)
+def test_vectors_and_a_few_rows(gcq, count, m, n, t):
+    """Of one row the singular value is 1 and stays beside it: what the steps make of
+    1, times x / |x|. Matrices of a call do not meet in each other's padding."""
+    announce(f"orthogonalize {count} of {m} x {n} {t}")
+    xs = [update(m, n, seed=k) for k in range(count)]
+    xs[count // 2][0, 0] = float("nan")
+    for k, (got, x) in enumerate(zip(orthogonalize(gcq, xs, t), xs)):
+        if k == count // 2:
+            assert bool(got.isnan().all())
+            continue
+        ref = reference(x)
+        # the few roundings of A and P, which all values share (2^-11 or 2^-22 of P up
+        # to 4.8 each, grown by at most 3.4445 in each of the other steps)
+        most = (2.0 ** -22 if t == F32 else 2.0 ** -11) * 4.8 * 6 * 3.4445 ** 4
+        off = float((got.cpu().double() - ref).norm() / ref.norm())
+        assert off <= most + po.HALF_STEP[t], (off, most)
 
 
 @pytest.mark.parametrize("shape", [(16, 1000, 1100), (16, 1100, 1000), (40, 700, 513), (64, 300, 290)], ids=str)
