@@ -20,9 +20,12 @@
 //
 // HBM bounds it: 16384 x 4096 bf16 takes 52 us forward (two activations, 5.2 TB/s,
 // what a large copy reaches) and 83 us backward (three, 4.8 TB/s, 5 us of it the
-// second launch); 8192 x 768 bf16 with dropout and sum 12.3 us (four, 4.1 TB/s);
-// 4095 x 1001 fp32 backward with dropout 24 us (five, 3.4 TB/s: rows off 16 bytes
-// draw two masks for four values). Of 16 x 768 the kernel takes 3 us, the call 7.5.
+// second launch); 8192 x 768 bf16 with dropout and sum 12.9 us (four, 3.9 TB/s) and
+// backward 19 us (five, 3.3 TB/s: two short launches); 4095 x 1001 fp32 backward with
+// dropout 24 us (five, 3.4 TB/s: rows off 16 bytes draw two masks for four values).
+// 16-bit rows past 8192 values, whose teams are alone on a compute unit, are
+// farthest from it: 4096 x 12288 68 us forward (3.0 TB/s) and 82 backward (3.7). Of 16
+// x 768 the kernel takes 3 us, the call 7.5.
 #include "row_team.h"
 
 #include <algorithm>
@@ -327,7 +330,8 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void layer_norm_grad_ker
 // compute unit in all, twice what it holds, so that some start while others end.
 // 16384 x 4096 bf16: 52.0 us, against 58.4, 60.3 and 56.2 with 8, 16 and 32 and 54.5
 // with 128; 4096 x 8192 with dropout 57.6 (65.7, 58.5, 59.1, 61.4). Teams of 16 waves
-// do with 32: 4096 x 12288 68.9 (118 with 8, 67.1 with 16, 76.2 with 64).
+// do with 32: 4096 x 12288 68.9 (118 with 8, 67.1 with 16, 76.2 with 64). (All without
+// the correction of the mean, which adds 0.3 and 1.6 us to the first two.)
 constexpr size_t forward_teams(int team)
 {
     return 256 * (team == 1024 ? 32 : 64) / (team / kWave);

@@ -29,13 +29,16 @@
 // Second planes end at 2^-39 in X, at 2^-37 in A and 2^-35 in P, where they only
 // are factors of something below 1 next to a X.
 //
-// Five steps of one plane take 1.54 to 1.60 ms for 4096 x 4096 (1.37 TFLOP, halves
-// of symmetric products left out: 0.86 to 0.89 PFLOP/s) and 7.4 ms for 25088 x 4096
-// (0.90 PFLOP/s); of both 1.86 ms for the step of 48 x 768 x 768 (three products: 0.70
-// PFLOP/s). Large ones are bound by the power that holds the clock (mfma_product.h)
-// and by tiles that start and end together; one of 768 x 768, 123 us, by its 17
-// launches of 5 to 8 us; up to some 128 x 256 orthogonalize_resident.h goes without
-// them.
+// Five steps of one plane take 1.54 to 1.62 ms for 4096 x 4096 (1.37 TFLOP, halves
+// of symmetric products left out: 0.85 to 0.89 PFLOP/s) and 7.4 to 7.6 ms for 25088 x
+// 4096 (0.88 to 0.90 PFLOP/s); of both 1.78 to 1.93 ms for the step of 48 x 768 x 768
+// (three products: 0.68 to 0.73 PFLOP/s). Large symmetric products are 136 or 144
+// tiles on 256 compute units (25088 x 4096: 470 to 485 us, 0.87 to 0.90 PFLOP/s), the
+// updates next to them (1.0 PFLOP/s at 4096) bound by the power that holds the clock
+// (mfma_product.h); one of 768 x 768, 123 us, by its 17 launches of 5 to 8 us; up to
+// some 128 x 256 orthogonalize_resident.h goes without them. Both sides are held
+// padded to 128: 48 of 16 x 16384, 50 MB of values, take 1.19 ms and 815 MB of
+// workspace.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -114,7 +117,7 @@ struct Momentum {
 // (1 - beta) g + beta m of g scaled, and of the momentum, old or new. It starts at
 // the end with the larger weight, whose value enters unrounded: from the other one,
 // m would be rounded at the size of m - g, which is that of g where gradients are
-// noise (6 times the momenta at beta 0.95: 1.7e-7 off 64 bits instead of 2.7e-8).
+// noise (6 times the momenta at beta 0.95: 1.7e-7 off 64 bits instead of 3.8e-8).
 __device__ __forceinline__ float mix(float g, float m, const Momentum& mo)
 {
     const float from = mo.far ? m : g, to = mo.far ? g : m;
