@@ -909,8 +909,8 @@ def orthogonalize(xs: Sequence, outs: Sequence, ws, coefficients=NEWTON_SCHULZ,
     + c (X X')^2 X for each triple of `coefficients`). xs and outs: up to 64
     matrices [m, n], the xs of one dtype and the outs of one; the dtype of the
     outs says how exactly they are computed. outs[k] may be xs[k] itself, but
-    overlap no other matrix of the call. ws: uint8 device tensor of at least orthogonalize_ws_bytes(count, m, n,
-    out_dtype) bytes."""
+    overlap no other matrix of the call. ws: uint8 device tensor of at least
+    orthogonalize_ws_bytes(count, m, n, out_dtype) bytes."""
     count, m, n = _matrices("orthogonalize", "xs outs", xs, outs)
     coef, steps = _coefficients(coefficients)
     size = _ws(ws, "orthogonalize")
@@ -938,11 +938,11 @@ def muon_step(grads: Sequence, momenta: Sequence, weights: Sequence, ws,
     """Moves the momenta along the gradients, and the weights along the
     orthogonalised momenta. Up to 64 matrices [m, n]: grads and momenta
     float32, weights of one dtype; new_momenta and new_weights default to the
-    tensors themselves, and overlap no other matrix of the call. update_dtype (by default the weights' dtype) says how
-    exactly the update is computed: bfloat16 is a third of the products of
-    float32. lr_scale: one-element float32 device tensor multiplied to lr on
-    the device. ws: uint8 device tensor of at least muon_step_ws_bytes(count,
-    m, n, update_dtype) bytes."""
+    tensors themselves, and overlap no other matrix of the call. update_dtype
+    (by default the weights' dtype) says how exactly the update is computed:
+    bfloat16 is a third of the products of float32. lr_scale: one-element
+    float32 device tensor multiplied to lr on the device. ws: uint8 device
+    tensor of at least muon_step_ws_bytes(count, m, n, update_dtype) bytes."""
     torch = _torch()
     new_momenta = momenta if new_momenta is None else new_momenta
     new_weights = weights if new_weights is None else new_weights

@@ -24,7 +24,7 @@
 // backward 19 us (five, 3.3 TB/s: two short launches); 4095 x 1001 fp32 backward with
 // dropout 24 us (five, 3.4 TB/s: rows off 16 bytes draw two masks for four values).
 // 16-bit rows past 8192 values, whose teams are alone on a compute unit, are
-// farthest from it: 4096 x 12288 68 us forward (3.0 TB/s) and 82 backward (3.7). Of 16
+// farthest from it: 4096 x 12288 57 us forward (3.5 TB/s) and 82 backward (3.7). Of 16
 // x 768 the kernel takes 3 us, the call 7.5.
 #include "row_team.h"
 
@@ -62,13 +62,26 @@ __device__ __forceinline__ float wave_count(int w, uint32_t d)
     return float(n);
 }
 
-// Mean of the row x (zeros behind column d), and sum of squares around it. A sum
-// and its quotient round by some 2^-24 of the mean each, which is all that a row of
-// one value has for deviations: eps = 1e-12 would make them the size of the gain. The
-// deviations from the first mean, exact there, say how far it is off,
-//   mean += sum u / n,  squares = sum u^2 - (sum u)^2 / n
-// (one more sum, beside that of the squares: 16384 x 4096 bf16 52.2 us, 51.9 without;
-// 4096 x 8192 with dropout 59.0 and 57.4).
+// A sum and its quotient round by some 2^-24 of the mean each, which is all that a
+// row of one value has for deviations: eps = 1e-12 would make them the size of the
+// gain. The deviations u from the mean, exact there, say how far it is off: sum u / n.
+// Not where they are above a 16th of the mean, as their sum then rounds by more than
+// the row's, nor of NaN or infinities: most rows are only asked.
+// q: sum u^2, inv: 1 / n.
+__device__ __forceinline__ bool mean_is_coarse(float mean, float q, float inv)
+{
+    return q * inv * 256.0f < mean * mean && q < __builtin_inff();
+}
+
+// r: sum u.
+__device__ __forceinline__ void correct_mean(float& mean, float& q, float r, float inv)
+{
+    const float more = r * inv;
+    mean += more;
+    q = fmaxf(__builtin_fmaf(-r, more, q), 0.0f);
+}
+
+// Mean of the row x (zeros behind column d), and sum of squares around it.
 template <typename R, int kTeam, int kVecs, bool kAligned>
 __device__ __forceinline__ void mean_and_squares(const typename R::F (&x)[kVecs], uint32_t d, float inv_d, int t,
                                                  float* lds, int& half, float& mean, float& squares)
@@ -84,46 +97,58 @@ __device__ __forceinline__ void mean_and_squares(const typename R::F (&x)[kVecs]
     const int wave = kWaves == 1 ? 0 : __builtin_amdgcn_readfirstlane(t / kWave);
     const float count = wave_count<R, kTeam, kVecs>(wave, d);
     const float inv = kWaves == 1 ? inv_d : count > 0.0f ? 1.0f / count : 0.0f;
-    const float first = s * inv;
+    float own = s * inv;
+    const auto deviation = [&](int v, int e, float from) {
+        return R::col(v, t) + (kAligned ? 0 : e) < d ? x[v][e] - from : 0.0f;
+    };
     float q = 0.0f, r = 0.0f;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
 #pragma unroll
         for (int e = 0; e < R::V; ++e) {
-            const float u = R::col(v, t) + (kAligned ? 0 : e) < d ? x[v][e] - first : 0.0f;
+            const float u = deviation(v, e, own);
             q = __builtin_fmaf(u, u, q);
-            r += u;
         }
     q = wave_sum(q);
-    r = wave_sum(r);
-    const float more = r * inv, own = first + more;
-    if (q < __builtin_inff())  // (what is not finite stays)
-        q = fmaxf(__builtin_fmaf(-r, more, q), 0.0f);
+    if (mean_is_coarse(own, q, inv)) {  // (the same in every lane)
+        float from = own;
+        asm volatile("" : "+v"(from));  // (or the deviations are held until here, 4 to 9 registers)
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+            for (int e = 0; e < R::V; ++e)
+                r += deviation(v, e, from);
+        correct_mean(own, q, wave_sum(r), inv);
+    }
     if (kWaves == 1) {
         mean = own;
         squares = q;
         return;
     }
-    float* at = lds + half * (2 * kWaves);
+    float* at = lds + half * (3 * kWaves);
     half ^= 1;
     if ((t & (kWave - 1)) == 0) {
-        at[wave] = own;
+        at[wave] = s;
         at[kWaves + wave] = q;
+        at[2 * kWaves + wave] = own;
     }
     __syncthreads();
-    // (from wave 0's mean on, so that equal ones stay as they are)
-    float off = 0.0f;
-    for (int w = 1; w < kWaves; ++w) {
-        const float n = wave_count<R, kTeam, kVecs>(w, d);
-        off += n > 0.0f ? n * (at[w] - at[0]) : 0.0f;
-    }
-    mean = __builtin_fmaf(off, inv_d, at[0]);
-    squares = 0.0f;
+    s = 0.0f;
+    for (int w = 0; w < kWaves; ++w)
+        s += at[w];
+    mean = s * inv_d;
+    // the same once more, of the waves' means
+    q = r = squares = 0.0f;
     for (int w = 0; w < kWaves; ++w) {
         const float n = wave_count<R, kTeam, kVecs>(w, d);
-        const float u = n > 0.0f ? at[w] - mean : 0.0f;
-        squares += at[kWaves + w] + n * (u * u);
+        const float u = n > 0.0f ? at[2 * kWaves + w] - mean : 0.0f;
+        q = __builtin_fmaf(n * u, u, q);
+        r = __builtin_fmaf(n, u, r);
+        squares += at[kWaves + w];
     }
+    if (mean_is_coarse(mean, q, inv_d))
+        correct_mean(mean, q, r, inv_d);
+    squares += q;
 }
 
 // ---- forward --------------------------------------------------------------------
@@ -137,7 +162,7 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void layer_norm_kernel(
 {
     using R = Row<T, kTeam, kVecs, kAligned>;
     using F = typename R::F;
-    __shared__ float lds[4 * (kTeam / kWave)];
+    __shared__ float lds[6 * (kTeam / kWave)];
     int half = 0;
     const int t = threadIdx.x % kTeam;
     const size_t team = size_t(blockIdx.x) * R::kTeams + R::team();
@@ -330,8 +355,9 @@ __global__ __launch_bounds__(kTeam < 256 ? 256 : kTeam) void layer_norm_grad_ker
 // compute unit in all, twice what it holds, so that some start while others end.
 // 16384 x 4096 bf16: 52.0 us, against 58.4, 60.3 and 56.2 with 8, 16 and 32 and 54.5
 // with 128; 4096 x 8192 with dropout 57.6 (65.7, 58.5, 59.1, 61.4). Teams of 16 waves
-// do with 32: 4096 x 12288 68.9 (118 with 8, 67.1 with 16, 76.2 with 64). (All without
-// the correction of the mean, which adds 0.3 and 1.6 us to the first two.)
+// do with 32: 4096 x 12288 68.9 (118 with 8, 67.1 with 16, 76.2 with 64). (All with
+// the waves' means found once more from their sums, by a division each; the last is
+// 57.3 now.)
 constexpr size_t forward_teams(int team)
 {
     return 256 * (team == 1024 ? 32 : 64) / (team / kWave);

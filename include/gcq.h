@@ -391,7 +391,7 @@ int norm_residual_grad(const void* z, const void* y, int dtype, size_t rows, siz
  * dropout). Everything between is fp32; the squares are those of the
  * deviations from the mean, and h is that of the z before its rounding. The
  * mean is corrected by the deviations from it: a row of one value has none, and
- * its h is the bias for any eps above 0 (0: NaN).
+ * its h is the bias (with an eps of 0: NaN).
  *   x, y, z, h  [rows, d] of `dtype`, rows contiguous; z NULL: not kept, and
  *               NULL without y. h may be x or y, z the other one
  *   gain, bias  [d] fp32, or NULL

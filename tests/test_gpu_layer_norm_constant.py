@@ -49,3 +49,20 @@ def test_squares_past_fp32(gcq, d):
     rows = torch.tensor([0, 2, 3], device=gu.DEV)
     assert bool((rstd[rows] == 0).all()) and torch.equal(h[rows], bias.expand(3, d))
     assert bool(h[1].isfinite().all()) and float(rstd[1]) > 0.5
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("d", [5, 100, 768, 1001, 2048, 4096, 6000, 8200, 12288, 16384])
+def test_mean_of_sums_that_are_exact(gcq, d, t):
+    """Small whole numbers have exact sums, however large their deviations are next
+    to the mean: 1 / d and its product round, and nothing else."""
+    announce(f"layer_norm mean of whole numbers {d} {t}")
+    g = torch.Generator().manual_seed(d)
+    x = torch.randint(-100, 101, (300, d), generator=g)
+    mean = torch.full((300,), float("nan"), device=gu.DEV)
+    x_dev = x.to(t).to(gu.DEV)
+    gcq.layer_norm(x_dev, torch.empty_like(x_dev), mean=mean)
+    gu.sync()
+    ref = x.double().sum(1) / d
+    off = (mean.cpu().double() - ref).abs()
+    assert bool((off <= 2.01 * 2.0 ** -24 * ref.abs()).all()), float((off / ref.abs()).nan_to_num(0.0).max())
