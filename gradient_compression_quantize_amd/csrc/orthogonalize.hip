@@ -117,7 +117,7 @@ struct Momentum {
 // (1 - beta) g + beta m of g scaled, and of the momentum, old or new. It starts at
 // the end with the larger weight, whose value enters unrounded: from the other one,
 // m would be rounded at the size of m - g, which is that of g where gradients are
-// noise (6 times the momenta at beta 0.95: 1.7e-7 off 64 bits instead of 3.8e-8).
+// noise (6 times the momenta at beta 0.95: 1.7e-7 off 64 bits instead of 2.7e-8).
 __device__ __forceinline__ float mix(float g, float m, const Momentum& mo)
 {
     const float from = mo.far ? m : g, to = mo.far ? g : m;
