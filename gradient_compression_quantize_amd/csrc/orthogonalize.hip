@@ -29,9 +29,9 @@
 // Second planes end at 2^-39 in X, at 2^-37 in A and 2^-35 in P, where they only
 // are factors of something below 1 next to a X.
 //
-// Five steps of one plane take 1.54 to 1.62 ms for 4096 x 4096 (1.37 TFLOP, halves
-// of symmetric products left out: 0.85 to 0.89 PFLOP/s) and 7.4 to 7.6 ms for 25088 x
-// 4096 (0.88 to 0.90 PFLOP/s); of both 1.78 to 1.93 ms for the step of 48 x 768 x 768
+// Five steps of one plane take 1.46 to 1.62 ms for 4096 x 4096 (1.37 TFLOP, halves
+// of symmetric products left out: 0.85 to 0.94 PFLOP/s) and 7.2 to 7.6 ms for 25088 x
+// 4096 (0.88 to 0.93 PFLOP/s); of both 1.78 to 1.93 ms for the step of 48 x 768 x 768
 // (three products: 0.68 to 0.73 PFLOP/s). Large symmetric products are 136 or 144
 // tiles on 256 compute units (25088 x 4096: 470 to 485 us, 0.87 to 0.90 PFLOP/s), the
 // updates next to them (1.0 PFLOP/s at 4096) bound by the power that holds the clock
